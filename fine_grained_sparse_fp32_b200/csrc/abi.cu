@@ -1,7 +1,9 @@
 // C ABI of the kmoe library: argument checks, workspace layout, dispatch to
 // the kernels, and the whole-layer forward.
 #include "common.cuh"
+#include "w4.cuh"
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -74,7 +76,10 @@ static kmoe_status check_act_dtype(int t, const char *name)
 // E4M3 weights with FP32 128 x 128 block scales (BF16 or FP8 activations).
 static bool fp8_weights(int w_dtype) { return w_dtype == KMOE_E4M3_B128 || w_dtype == KMOE_E4M3_B128_A8; }
 
-static bool known_w_dtype(int w_dtype) { return w_dtype == KMOE_F32 || w_dtype == KMOE_BF16 || fp8_weights(w_dtype); }
+static bool known_w_dtype(int w_dtype)
+{
+    return w_dtype == KMOE_F32 || w_dtype == KMOE_BF16 || w_dtype == KMOE_W4 || fp8_weights(w_dtype);
+}
 
 // FP8 activations need BF16 x and d % 256 == 0 (the FP8 FFN's down units);
 // checked on the host before anything is enqueued.
@@ -85,9 +90,51 @@ static kmoe_status check_a8(int x_dtype, int d, int w_dtype)
     return KMOE_OK;
 }
 
+// 4-bit weights need BF16 x; checked on the host before anything is enqueued.
+static kmoe_status check_w4_x(int x_dtype, int w_dtype)
+{
+    if (w_dtype == KMOE_W4 && x_dtype != KMOE_BF16) return fail(KMOE_ERR_UNSUPPORTED, "4-bit weights: x must be BF16");
+    return KMOE_OK;
+}
+
+static kmoe_status check_w4_group(int group)
+{
+    if (group != 32 && group != 64 && group != 128)
+        return fail(KMOE_ERR_UNSUPPORTED, "group=%d: 32, 64 or 128 columns", group);
+    return KMOE_OK;
+}
+
+static kmoe_status check_w4_cols(int cols)
+{
+    if (cols < 128 || cols % 128)
+        return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: must be a positive multiple of 128", cols);
+    return KMOE_OK;
+}
+
+static kmoe_status check_w4(const kmoe_w4 *w, const char *name)
+{
+    if (!w) return fail(KMOE_ERR_INVALID_ARG, "%s is NULL", name);
+    KMOE_TRY(check_w4_group(w->group));
+    KMOE_TRY(check_ptr(w->codes, "codes"));
+    KMOE_TRY(check_ptr(w->scales, "scales"));
+    return check_ptr(w->zeros, "zeros", true);
+}
+
+static W4Ptrs w4_ptrs(const kmoe_w4 &w)
+{
+    return {w.codes, static_cast<const __nv_bfloat16 *>(w.scales), w.zeros};
+}
+
 static kmoe_status check_experts(const kmoe_experts *x, const char *name)
 {
     if (!x) return fail(KMOE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (x->dtype == KMOE_W4) {
+        if (!x->w4) return fail(KMOE_ERR_INVALID_ARG, "%s: w4 is NULL", name);
+        for (int i = 0; i < 3; ++i) KMOE_TRY(check_w4(x->w4 + i, name));
+        if (x->w4[0].group != x->w4[1].group || !x->w4[0].zeros != !x->w4[1].zeros)
+            return fail(KMOE_ERR_UNSUPPORTED, "%s: gate and up differ in group size or zero points", name);
+        return KMOE_OK;
+    }
     if (x->dtype != KMOE_F32 && x->dtype != KMOE_BF16 && !fp8_weights(x->dtype))
         return fail(KMOE_ERR_UNSUPPORTED, "%s dtype %d unknown", name, x->dtype);
     KMOE_TRY(check_ptr(x->w_gate, "w_gate"));
@@ -110,6 +157,19 @@ static ExpertPtrs ptrs(const kmoe_experts *x)
         p.sd = x->s_down;
     }
     return p;
+}
+
+// The shared expert's weights have the routed ones' dtype, and in 4 bits their
+// group sizes and zero points too (one kernel serves both).
+static kmoe_status check_shared(const kmoe_experts *shared, const kmoe_experts *routed)
+{
+    KMOE_TRY(check_experts(shared, "shared"));
+    if (shared->dtype != routed->dtype) return fail(KMOE_ERR_UNSUPPORTED, "shared and routed dtypes differ");
+    if (routed->dtype != KMOE_W4) return KMOE_OK;
+    for (int i = 0; i < 3; ++i)
+        if (shared->w4[i].group != routed->w4[i].group || !shared->w4[i].zeros != !routed->w4[i].zeros)
+            return fail(KMOE_ERR_UNSUPPORTED, "shared and routed 4-bit weights differ in group size or zero points");
+    return KMOE_OK;
 }
 
 static size_t act_bytes(int w_dtype) { return w_dtype == KMOE_F32 ? 4 : 2; }
@@ -215,12 +275,60 @@ static FfnPath ffn_path(int x_dtype, int w_dtype, int N, int d)
     return N < kTcMinTokens ? kPathSwap : kPathTc;
 }
 
+// Grouped FFN with 4-bit weights: H = SiLU(W_g x) * (W_u x) for routed and
+// shared rows in one launch, then both down projections in another.
+static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E, int K, const int32_t *perm,
+                              const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, void *h, void *y_perm,
+                              void *y_shared, cudaStream_t st)
+{
+    W4Product a{};
+    a.P = N * K;
+    a.n_shared = s ? N : 0;
+    a.E = E;
+    a.offsets = offsets;
+    a.y_dtype = KMOE_BF16;
+    W4Product b = a;
+    a.x = x;
+    a.x_rows = N;
+    a.perm = perm;
+    a.rows = I;
+    a.cols = d;
+    a.group = r[0].group;
+    a.w = w4_ptrs(r[0]);
+    a.up = w4_ptrs(r[1]);
+    if (s) {
+        a.w_shared = w4_ptrs(s[0]);
+        a.up_shared = w4_ptrs(s[1]);
+    }
+    a.y = h;
+    KMOE_TRY(launch_w4(a, st));
+    b.x = static_cast<const __nv_bfloat16 *>(h);
+    b.x_rows = a.P + a.n_shared;
+    b.x_by_row = true;
+    b.rows = d;
+    b.cols = I;
+    b.group = r[2].group;
+    b.w = w4_ptrs(r[2]);
+    if (s) b.w_shared = w4_ptrs(s[2]);
+    b.y = y_perm;
+    b.y_shared = y_shared;
+    return launch_w4(b, st);
+}
+
 // `status` is the workspace status block: the status word, tickets, then
 // kSyncInts counters at kSyncOffset (all zeroed by clear_status).
 static kmoe_status run_ffn(const void *x, int x_dtype, int N, int d, int I, int E, int K, const int32_t *perm,
-                           const int32_t *offsets, int w_dtype, const ExpertPtrs &r, const ExpertPtrs *s,
+                           const int32_t *offsets, const kmoe_experts *routed, const kmoe_experts *shared,
                            const FfnScratch &f, void *y_perm, void *y_shared, int *status, cudaStream_t st)
 {
+    const int w_dtype = routed->dtype;
+    if (w_dtype == KMOE_W4)
+        return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm, offsets, routed->w4,
+                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, st);
+    const ExpertPtrs r = ptrs(routed);
+    ExpertPtrs sh{};
+    if (shared) sh = ptrs(shared);
+    const ExpertPtrs *s = shared ? &sh : nullptr;
     const FfnPath path = ffn_path(x_dtype, w_dtype, N, d);
     void *h = f.h;
     if (path == kPathA8) {
@@ -267,21 +375,44 @@ static kmoe_status check_score(int score)
     return KMOE_OK;
 }
 
-// Validation shared by moe_forward and moe_block_forward.
-static kmoe_status check_forward(int N, int d, int E, int K, int I, int score, const kmoe_experts *routed,
+static kmoe_status check_routing(const kmoe_routing *r, int E, int K)
+{
+    if (!r) return fail(KMOE_ERR_INVALID_ARG, "routing is NULL");
+    if (r->score != KMOE_ROUTE_SIGMOID && r->score != KMOE_ROUTE_SOFTMAX)
+        return fail(KMOE_ERR_INVALID_ARG, "routing score %d: KMOE_ROUTE_SIGMOID or KMOE_ROUTE_SOFTMAX", r->score);
+    if (r->group_score != KMOE_GROUP_MAX && r->group_score != KMOE_GROUP_TOP2)
+        return fail(KMOE_ERR_INVALID_ARG, "group_score %d: KMOE_GROUP_MAX or KMOE_GROUP_TOP2", r->group_score);
+    if (r->n_groups < 1 || r->n_groups > 32 || E % r->n_groups)
+        return fail(KMOE_ERR_UNSUPPORTED, "n_groups=%d: 1..32 and a divisor of E=%d", r->n_groups, E);
+    if (r->topk_groups < 1 || r->topk_groups > r->n_groups || r->topk_groups * (E / r->n_groups) < K)
+        return fail(KMOE_ERR_INVALID_ARG, "topk_groups=%d of %d: the groups kept must hold K=%d experts",
+                    r->topk_groups, r->n_groups, K);
+    if (r->renormalise != 0 && r->renormalise != 1)
+        return fail(KMOE_ERR_INVALID_ARG, "renormalise=%d: 0 or 1", r->renormalise);
+    if (!std::isfinite(r->scale)) return fail(KMOE_ERR_INVALID_ARG, "routing scale must be finite");
+    return KMOE_OK;
+}
+
+// The two routing rules of a layer call: `score` of moe_router_topk, or
+// kmoe_routing where `rule` is set.
+struct RouteBy {
+    int score;
+    const kmoe_routing *rule;
+};
+
+// Validation shared by moe_forward, moe_block_forward and their _routed forms
+// (N == 0 leaves the pointers unchecked).
+static kmoe_status check_forward(int N, int d, int E, int K, int I, const RouteBy &by, const kmoe_experts *routed,
                                  const kmoe_experts *shared, const float *w_router, const float *bias,
                                  int32_t *topk_idx_out, float *topk_w_out, int32_t *counts_out, void *ws)
 {
     KMOE_TRY(check_sizes(N, d, E, K, I));
-    KMOE_TRY(check_score(score));
+    KMOE_TRY(by.rule ? check_routing(by.rule, E, K) : check_score(by.score));
     KMOE_TRY(check_experts(routed, "routed"));
-    if (shared) {
-        KMOE_TRY(check_experts(shared, "shared"));
-        if (shared->dtype != routed->dtype) return fail(KMOE_ERR_UNSUPPORTED, "shared and routed dtypes differ");
-    }
+    if (shared) KMOE_TRY(check_shared(shared, routed));
     if (N == 0) return KMOE_OK;
     KMOE_TRY(check_ptr(w_router, "w_router"));
-    KMOE_TRY(check_ptr(bias, "bias"));
+    KMOE_TRY(check_ptr(bias, "bias", by.rule != nullptr));
     KMOE_TRY(check_ptr(topk_idx_out, "topk_idx_out", true));
     KMOE_TRY(check_ptr(topk_w_out, "topk_w_out", true));
     KMOE_TRY(check_ptr(counts_out, "counts_out", true));
@@ -297,7 +428,7 @@ static kmoe_status check_forward(int N, int d, int E, int K, int I, int score, c
 // call's, so the programmatic launch chain carries over).
 static bool router_zeroes_status(int N) { return N <= kSmallRouteTokens; }
 
-static kmoe_status forward_path(const void *x, int x_dtype, int N, int d, int E, int K, int I, int score,
+static kmoe_status forward_path(const void *x, int x_dtype, int N, int d, int E, int K, int I, const RouteBy &by,
                                 const float *w_router, const float *bias, const kmoe_experts *routed,
                                 const kmoe_experts *shared, void *y, int y_dtype, int32_t *topk_idx_out,
                                 float *topk_w_out, int32_t *counts_out, const Layout &L, const void *h_res,
@@ -318,16 +449,75 @@ static kmoe_status forward_path(const void *x, int x_dtype, int N, int d, int E,
                                   L.status, st));
     else
         KMOE_TRY(launch_router_logits(x, x_dtype, w_router, N, d, E, L.logits, st));
-    KMOE_TRY(launch_topk(L.logits, bias, N, E, K, score, idx, w, st, chunked ? L.hist : nullptr));
+    int32_t *hist = chunked ? L.hist : nullptr;
+    KMOE_TRY(by.rule ? launch_route(L.logits, KMOE_F32, bias, N, E, K, *by.rule, idx, w, st, hist)
+                     : launch_topk(L.logits, bias, N, E, K, by.score, idx, w, st, hist));
     KMOE_TRY(launch_permute(idx, N, K, E, counts, L.offsets, L.perm, L.inv, L.hist, st, chunked));
-    const ExpertPtrs r = ptrs(routed);
-    ExpertPtrs s{};
-    if (shared) s = ptrs(shared);
-    KMOE_TRY(run_ffn(x, x_dtype, N, d, I, E, K, L.perm, L.offsets, routed->dtype, r, shared ? &s : nullptr,
-                     L.ffn, L.y_perm, L.y_shared, L.status, st));
+    KMOE_TRY(run_ffn(x, x_dtype, N, d, I, E, K, L.perm, L.offsets, routed, shared, L.ffn, L.y_perm, L.y_shared,
+                     L.status, st));
     const int yin = routed->dtype == KMOE_F32 ? KMOE_F32 : KMOE_BF16;
     return launch_combine(L.y_perm, shared ? L.y_shared : nullptr, yin, w, L.inv, N, K, d, y, y_dtype, L.status, st,
                           h_res, g_post, eps);
+}
+
+// moe_forward and moe_forward_routed, after clear_error().
+static kmoe_status run_forward(const void *x, int x_dtype, int N, int d, int E, int K, int I, const RouteBy &by,
+                               const float *w_router, const float *bias, const kmoe_experts *routed,
+                               const kmoe_experts *shared, void *y, int y_dtype, int32_t *topk_idx_out,
+                               float *topk_w_out, int32_t *counts_out, void *ws, size_t ws_bytes, void *stream)
+{
+    KMOE_TRY(check_act_dtype(x_dtype, "x"));
+    KMOE_TRY(check_act_dtype(y_dtype, "y"));
+    KMOE_TRY(check_forward(N, d, E, K, I, by, routed, shared, w_router, bias, topk_idx_out, topk_w_out, counts_out,
+                           ws));
+    KMOE_TRY(check_a8(x_dtype, d, routed->dtype));
+    KMOE_TRY(check_w4_x(x_dtype, routed->dtype));
+    if (N == 0) return KMOE_OK;
+    KMOE_TRY(check_ptr(x, "x"));
+    KMOE_TRY(check_ptr(y, "y"));
+    const Layout need = layout(nullptr, N, d, E, K, I, routed->dtype);
+    if (ws_bytes < need.bytes) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need.bytes);
+    // the base the Carver sees is 256-aligned by construction of the pieces
+    const Layout L = layout(ws, N, d, E, K, I, routed->dtype);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!router_zeroes_status(N)) KMOE_TRY(clear_status(L.status, st, kFfnStatusBytes));
+    return forward_path(x, x_dtype, N, d, E, K, I, by, w_router, bias, routed, shared, y, y_dtype, topk_idx_out,
+                        topk_w_out, counts_out, L, nullptr, nullptr, 0.f, st);
+}
+
+// moe_block_forward and moe_block_forward_routed, after clear_error().
+static kmoe_status run_block(const void *h, int N, int d, int E, int K, int I, const RouteBy &by,
+                             const void *gamma_pre, const void *gamma_post, float eps, const float *w_router,
+                             const float *bias, const kmoe_experts *routed, const kmoe_experts *shared, void *h_out,
+                             void *x_out, int32_t *topk_idx_out, float *topk_w_out, int32_t *counts_out, void *ws,
+                             size_t ws_bytes, void *stream)
+{
+    KMOE_TRY(check_forward(N, d, E, K, I, by, routed, shared, w_router, bias, topk_idx_out, topk_w_out, counts_out,
+                           ws));
+    if (routed->dtype == KMOE_F32)
+        return fail(KMOE_ERR_UNSUPPORTED, "block: routed weights must be BF16, E4M3 with 128x128 scales or 4-bit");
+    if (!(eps >= 0.f) || eps > 1.f) return fail(KMOE_ERR_INVALID_ARG, "eps=%g: must be in [0, 1]", (double)eps);
+    if (d % 256) return fail(KMOE_ERR_UNSUPPORTED, "block: d=%d must be a multiple of 256", d);
+    const size_t row_smem = (size_t)(K + (shared ? 1 : 0)) * d * 2;
+    if (2 * row_smem > 100 * 1024)
+        return fail(KMOE_ERR_UNSUPPORTED, "block: (K + 1) * d = %zu BF16 values per token exceed the combine's "
+                    "staging buffer", row_smem / 2);
+    if (N == 0) return KMOE_OK;
+    KMOE_TRY(check_ptr(h, "h"));
+    KMOE_TRY(check_ptr(gamma_pre, "gamma_pre"));
+    KMOE_TRY(check_ptr(gamma_post, "gamma_post"));
+    KMOE_TRY(check_ptr(h_out, "h_out"));
+    KMOE_TRY(check_ptr(x_out, "x_out", true));
+    const Layout need = layout(nullptr, N, d, E, K, I, routed->dtype, true);
+    if (ws_bytes < need.bytes) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need.bytes);
+    const Layout L = layout(ws, N, d, E, K, I, routed->dtype, true);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!router_zeroes_status(N)) KMOE_TRY(clear_status(L.status, st, kFfnStatusBytes));
+    __nv_bfloat16 *x = x_out ? static_cast<__nv_bfloat16 *>(x_out) : L.x_norm;
+    KMOE_TRY(launch_rmsnorm(static_cast<const __nv_bfloat16 *>(h), static_cast<const __nv_bfloat16 *>(gamma_pre), eps,
+                            N, d, x, st));
+    return forward_path(x, KMOE_BF16, N, d, E, K, I, by, w_router, bias, routed, shared, h_out, KMOE_BF16,
+                        topk_idx_out, topk_w_out, counts_out, L, h, gamma_post, eps, st);
 }
 
 }  // namespace kmoe
@@ -424,11 +614,9 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
     KMOE_TRY(check_sizes(N, d, E, K, I));
     KMOE_TRY(check_act_dtype(x_dtype, "x"));
     KMOE_TRY(check_experts(routed, "routed"));
-    if (shared) {
-        KMOE_TRY(check_experts(shared, "shared"));
-        if (shared->dtype != routed->dtype) return fail(KMOE_ERR_UNSUPPORTED, "shared and routed dtypes differ");
-    }
+    if (shared) KMOE_TRY(check_shared(shared, routed));
     KMOE_TRY(check_a8(x_dtype, d, routed->dtype));
+    KMOE_TRY(check_w4_x(x_dtype, routed->dtype));
     if (N == 0) return KMOE_OK;
     KMOE_TRY(check_ptr(x, "x"));
     KMOE_TRY(check_ptr(perm_token, "perm_token"));
@@ -438,16 +626,12 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
     KMOE_TRY(check_ptr(ws, "ws"));
     const size_t need = ffn_ws_bytes(N, d, K, I, routed->dtype);
     if (ws_bytes < need) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
-    const ExpertPtrs r = ptrs(routed);
-    ExpertPtrs s{};
-    if (shared) s = ptrs(shared);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Carver c(ws);
     int *status = c.take<int>(kStatusInts);
     const FfnScratch f = take_ffn_scratch(c, N, d, K, I, routed->dtype);
     KMOE_TRY(clear_status(status, st, kFfnStatusBytes));
-    return run_ffn(x, x_dtype, N, d, I, E, K, perm_token, offsets, routed->dtype, r, shared ? &s : nullptr, f,
-                   y_perm, y_shared, status, st);
+    return run_ffn(x, x_dtype, N, d, I, E, K, perm_token, offsets, routed, shared, f, y_perm, y_shared, status, st);
 }
 
 kmoe_status moe_combine(const void *y_perm, const void *y_shared, int y_in_dtype, const float *topk_w,
@@ -473,28 +657,26 @@ kmoe_status moe_forward(const void *x, int x_dtype, int N, int d, int E, int K, 
                         float *topk_w_out, int32_t *counts_out, void *ws, size_t ws_bytes, void *stream)
 {
     clear_error();
-    KMOE_TRY(check_act_dtype(x_dtype, "x"));
-    KMOE_TRY(check_act_dtype(y_dtype, "y"));
-    KMOE_TRY(check_forward(N, d, E, K, I, score, routed, shared, w_router, bias, topk_idx_out, topk_w_out, counts_out,
-                           ws));
-    KMOE_TRY(check_a8(x_dtype, d, routed->dtype));
-    if (N == 0) return KMOE_OK;
-    KMOE_TRY(check_ptr(x, "x"));
-    KMOE_TRY(check_ptr(y, "y"));
-    const Layout need = layout(nullptr, N, d, E, K, I, routed->dtype);
-    if (ws_bytes < need.bytes) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need.bytes);
-    // the base the Carver sees is 256-aligned by construction of the pieces
-    const Layout L = layout(ws, N, d, E, K, I, routed->dtype);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!router_zeroes_status(N)) KMOE_TRY(clear_status(L.status, st, kFfnStatusBytes));
-    return forward_path(x, x_dtype, N, d, E, K, I, score, w_router, bias, routed, shared, y, y_dtype, topk_idx_out,
-                        topk_w_out, counts_out, L, nullptr, nullptr, 0.f, st);
+    return run_forward(x, x_dtype, N, d, E, K, I, {score, nullptr}, w_router, bias, routed, shared, y, y_dtype,
+                       topk_idx_out, topk_w_out, counts_out, ws, ws_bytes, stream);
+}
+
+kmoe_status moe_forward_routed(const void *x, int x_dtype, int N, int d, int E, int K, int I,
+                               const kmoe_routing *routing, const float *w_router, const float *bias,
+                               const kmoe_experts *routed, const kmoe_experts *shared, void *y, int y_dtype,
+                               int32_t *topk_idx_out, float *topk_w_out, int32_t *counts_out, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    clear_error();
+    if (!routing) return fail(KMOE_ERR_INVALID_ARG, "routing is NULL");
+    return run_forward(x, x_dtype, N, d, E, K, I, {0, routing}, w_router, bias, routed, shared, y, y_dtype,
+                       topk_idx_out, topk_w_out, counts_out, ws, ws_bytes, stream);
 }
 
 size_t moe_block_workspace_size(int N, int d, int E, int K, int I, int w_dtype)
 {
     if (check_sizes(N, d, E, K, I) != KMOE_OK) return 0;
-    if (w_dtype != KMOE_BF16 && !fp8_weights(w_dtype)) return 0;
+    if (w_dtype != KMOE_BF16 && w_dtype != KMOE_W4 && !fp8_weights(w_dtype)) return 0;
     clear_error();
     return layout(nullptr, N, d, E, K, I, w_dtype, true).bytes;
 }
@@ -506,32 +688,72 @@ kmoe_status moe_block_forward(const void *h, int N, int d, int E, int K, int I, 
                               size_t ws_bytes, void *stream)
 {
     clear_error();
-    KMOE_TRY(check_forward(N, d, E, K, I, score, routed, shared, w_router, bias, topk_idx_out, topk_w_out, counts_out,
-                           ws));
-    if (routed->dtype != KMOE_BF16 && !fp8_weights(routed->dtype))
-        return fail(KMOE_ERR_UNSUPPORTED, "block: routed weights must be BF16 or E4M3 with 128x128 scales");
-    if (!(eps >= 0.f) || eps > 1.f) return fail(KMOE_ERR_INVALID_ARG, "eps=%g: must be in [0, 1]", (double)eps);
-    if (d % 256) return fail(KMOE_ERR_UNSUPPORTED, "block: d=%d must be a multiple of 256", d);
-    const size_t row_smem = (size_t)(K + (shared ? 1 : 0)) * d * 2;
-    if (2 * row_smem > 100 * 1024)
-        return fail(KMOE_ERR_UNSUPPORTED, "block: (K + 1) * d = %zu BF16 values per token exceed the combine's "
-                    "staging buffer", row_smem / 2);
+    return run_block(h, N, d, E, K, I, {score, nullptr}, gamma_pre, gamma_post, eps, w_router, bias, routed, shared,
+                     h_out, x_out, topk_idx_out, topk_w_out, counts_out, ws, ws_bytes, stream);
+}
+
+kmoe_status moe_block_forward_routed(const void *h, int N, int d, int E, int K, int I, const kmoe_routing *routing,
+                                     const void *gamma_pre, const void *gamma_post, float eps,
+                                     const float *w_router, const float *bias, const kmoe_experts *routed,
+                                     const kmoe_experts *shared, void *h_out, void *x_out, int32_t *topk_idx_out,
+                                     float *topk_w_out, int32_t *counts_out, void *ws, size_t ws_bytes, void *stream)
+{
+    clear_error();
+    if (!routing) return fail(KMOE_ERR_INVALID_ARG, "routing is NULL");
+    return run_block(h, N, d, E, K, I, {0, routing}, gamma_pre, gamma_post, eps, w_router, bias, routed, shared,
+                     h_out, x_out, topk_idx_out, topk_w_out, counts_out, ws, ws_bytes, stream);
+}
+
+kmoe_status moe_route(const void *logits, int l_dtype, const float *bias, int N, int E, int K,
+                      const kmoe_routing *routing, int32_t *topk_idx, float *topk_w, void *stream)
+{
+    clear_error();
+    KMOE_TRY(check_sizes(N, 128, E, K, -1));
+    KMOE_TRY(check_act_dtype(l_dtype, "logits"));
+    KMOE_TRY(check_routing(routing, E, K));
     if (N == 0) return KMOE_OK;
-    KMOE_TRY(check_ptr(h, "h"));
-    KMOE_TRY(check_ptr(gamma_pre, "gamma_pre"));
-    KMOE_TRY(check_ptr(gamma_post, "gamma_post"));
-    KMOE_TRY(check_ptr(h_out, "h_out"));
-    KMOE_TRY(check_ptr(x_out, "x_out", true));
-    const Layout need = layout(nullptr, N, d, E, K, I, routed->dtype, true);
-    if (ws_bytes < need.bytes) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need.bytes);
-    const Layout L = layout(ws, N, d, E, K, I, routed->dtype, true);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!router_zeroes_status(N)) KMOE_TRY(clear_status(L.status, st, kFfnStatusBytes));
-    __nv_bfloat16 *x = x_out ? static_cast<__nv_bfloat16 *>(x_out) : L.x_norm;
-    KMOE_TRY(launch_rmsnorm(static_cast<const __nv_bfloat16 *>(h), static_cast<const __nv_bfloat16 *>(gamma_pre), eps,
-                            N, d, x, st));
-    return forward_path(x, KMOE_BF16, N, d, E, K, I, score, w_router, bias, routed, shared, h_out, KMOE_BF16,
-                        topk_idx_out, topk_w_out, counts_out, L, h, gamma_post, eps, st);
+    KMOE_TRY(check_ptr(logits, "logits"));
+    KMOE_TRY(check_ptr(bias, "bias", true));
+    KMOE_TRY(check_ptr(topk_idx, "topk_idx"));
+    KMOE_TRY(check_ptr(topk_w, "topk_w"));
+    return launch_route(logits, l_dtype, bias, N, E, K, *routing, topk_idx, topk_w, static_cast<cudaStream_t>(stream));
+}
+
+kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
+                          const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w, void *y, int y_dtype,
+                          void *stream)
+{
+    clear_error();
+    if (x_dtype != KMOE_BF16) return fail(KMOE_ERR_UNSUPPORTED, "4-bit weights: x must be BF16");
+    KMOE_TRY(check_act_dtype(y_dtype, "y"));
+    if (N < 0 || P < 0) return fail(KMOE_ERR_INVALID_ARG, "N=%d and P=%d must be >= 0", N, P);
+    if (N > (1 << 30) || P > (1 << 30)) return fail(KMOE_ERR_UNSUPPORTED, "N=%d, P=%d: at most 2^30 rows", N, P);
+    if (rows < 1 || rows > 65536) return fail(KMOE_ERR_UNSUPPORTED, "rows=%d: supported 1..65536", rows);
+    KMOE_TRY(check_w4_cols(cols));
+    if (cols > 65536) return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: supported up to 65536", cols);
+    if (E < 1 || E > 1024) return fail(KMOE_ERR_UNSUPPORTED, "E=%d: supported 1..1024", E);
+    if (!offsets && E != 1) return fail(KMOE_ERR_INVALID_ARG, "E=%d matrices need offsets", E);
+    if (!perm_token && P > N) return fail(KMOE_ERR_INVALID_ARG, "P=%d rows of y without perm_token, x has N=%d", P, N);
+    KMOE_TRY(check_w4(w, "w"));
+    if (P == 0) return KMOE_OK;
+    KMOE_TRY(check_ptr(x, "x", N == 0));
+    KMOE_TRY(check_ptr(perm_token, "perm_token", true));
+    KMOE_TRY(check_ptr(offsets, "offsets", true));
+    KMOE_TRY(check_ptr(y, "y"));
+    W4Product a{};
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.x_rows = N;
+    a.P = P;
+    a.rows = rows;
+    a.cols = cols;
+    a.E = E;
+    a.perm = perm_token;
+    a.offsets = offsets;
+    a.w = w4_ptrs(*w);
+    a.group = w->group;
+    a.y = y;
+    a.y_dtype = y_dtype;
+    return launch_w4(a, static_cast<cudaStream_t>(stream));
 }
 
 kmoe_status moe_quant_1x128(const void *x, int rows, int cols, uint8_t *codes, float *scales, void *stream)
@@ -545,6 +767,35 @@ kmoe_status moe_quant_1x128(const void *x, int rows, int cols, uint8_t *codes, f
     KMOE_TRY(check_ptr(scales, "scales"));
     return launch_quant_1x128(static_cast<const __nv_bfloat16 *>(x), rows, cols, codes, scales,
                               static_cast<cudaStream_t>(stream));
+}
+
+kmoe_status moe_quant_w4(const void *w, int w_dtype, int rows, int cols, int group, uint8_t *codes, void *scales,
+                         uint8_t *zeros, void *stream)
+{
+    clear_error();
+    KMOE_TRY(check_act_dtype(w_dtype, "w"));
+    if (rows < 0) return fail(KMOE_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
+    KMOE_TRY(check_w4_cols(cols));
+    KMOE_TRY(check_w4_group(group));
+    if (rows == 0) return KMOE_OK;
+    KMOE_TRY(check_ptr(w, "w"));
+    KMOE_TRY(check_ptr(codes, "codes"));
+    KMOE_TRY(check_ptr(scales, "scales"));
+    KMOE_TRY(check_ptr(zeros, "zeros", true));
+    return launch_quant_w4(w, w_dtype, rows, cols, group, codes, static_cast<__nv_bfloat16 *>(scales), zeros,
+                           static_cast<cudaStream_t>(stream));
+}
+
+kmoe_status moe_dequant_w4(const kmoe_w4 *w, int rows, int cols, void *out, int out_dtype, void *stream)
+{
+    clear_error();
+    KMOE_TRY(check_act_dtype(out_dtype, "out"));
+    if (rows < 0) return fail(KMOE_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
+    KMOE_TRY(check_w4_cols(cols));
+    if (rows == 0) return KMOE_OK;
+    KMOE_TRY(check_w4(w, "w"));
+    KMOE_TRY(check_ptr(out, "out"));
+    return launch_dequant_w4(w4_ptrs(*w), w->group, rows, cols, out, out_dtype, static_cast<cudaStream_t>(stream));
 }
 
 kmoe_status moe_set_wait_limit(long long cycles)

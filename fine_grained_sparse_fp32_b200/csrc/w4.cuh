@@ -1,0 +1,78 @@
+// The 4-bit weight format (kmoe_w4 in kmoe.h): helpers shared by its kernels.
+//
+//   W[r][c] = (q[r][c] - z[r][c / group]) * s[r][c / group]
+// A block of 128 columns of a row is 64 bytes: the sixteen 8-column words of
+// the block as a transposed 4 x 4 square. Lane t (0..3) of a matrix fragment
+// so finds in 16 consecutive bytes its 8 columns of each 32-column slice:
+// word jj of the 16 bytes holds columns 32 jj + 8 t .. + 7.
+#pragma once
+
+#include "common.cuh"
+
+namespace kmoe {
+
+constexpr int kW4Block = 128;                     // columns of one 64-byte block
+
+// Place of 8-column word v (0..15) in its block.
+__host__ __device__ constexpr int w4_place(int v) { return 4 * (v & 3) + (v >> 2); }
+
+// One stack of 4-bit matrices, as seen by the kernels.
+struct W4Ptrs {
+    const uint8_t *q;
+    const __nv_bfloat16 *s;
+    const uint8_t *z;     // NULL: 8 everywhere
+};
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<__nv_bfloat162 *>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// Columns 2i, 2i + 1 of a word as BF16 values 128 + q: the four bits are the
+// low mantissa bits of a BF16 number with exponent 7 (its last place is 1).
+__device__ __forceinline__ uint32_t w4_biased(uint32_t word, int i)
+{
+    return ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+}
+
+// The same pair as q - z, with zz = {128 + z, 128 + z}: exact in BF16, since
+// both sides are whole numbers below 256 and their difference is below 16.
+__device__ __forceinline__ uint32_t w4_codes(uint32_t word, int i, __nv_bfloat162 zz)
+{
+    return as_u32(__hsub2(as_bf162(w4_biased(word, i)), zz));
+}
+
+__device__ __forceinline__ __nv_bfloat162 w4_zero(uint32_t z)      // {128 + z, 128 + z}
+{
+    return as_bf162((0x4300u | z) * 0x00010001u);
+}
+
+}  // namespace kmoe
+
+namespace kmoe {
+
+kmoe_status launch_quant_w4(const void *w, int w_dtype, int rows, int cols, int group, uint8_t *codes,
+                            __nv_bfloat16 *scales, uint8_t *zeros, cudaStream_t st);
+kmoe_status launch_dequant_w4(const W4Ptrs &w, int group, int rows, int cols, void *out, int out_dtype,
+                              cudaStream_t st);
+
+// One launch of the 4-bit products: y[p] = W_e x[row(p)], or with `up` set
+// H[p] = SiLU(W x) * (up x). Rows p in [offsets[e], offsets[e + 1]) belong to
+// expert e < E; with `shared` rows P .. P + n_shared - 1 belong to the shared
+// expert. x row of p: perm[p] below P (p itself without perm), p - P
+// for the shared expert, or p itself everywhere with x_by_row.
+struct W4Product {
+    const __nv_bfloat16 *x;
+    int x_rows, P, n_shared, rows, cols, E;
+    const int32_t *perm, *offsets;       // offsets NULL: E == 1, all P rows
+    W4Ptrs w, up, w_shared, up_shared;   // up.q NULL: no SwiGLU
+    int group;
+    bool x_by_row;                       // x is indexed by p, the shared rows behind the P routed ones
+    void *y, *y_shared;                  // y [P (+ n_shared for SwiGLU), rows]
+    int y_dtype;
+};
+kmoe_status launch_w4(const W4Product &a, cudaStream_t st);
+
+// Routing by the rule of kmoe_routing. hist as in launch_topk.
+kmoe_status launch_route(const void *logits, int l_dtype, const float *bias, int N, int E, int K,
+                         const kmoe_routing &r, int32_t *idx, float *w, cudaStream_t st, int32_t *hist = nullptr);
+
+}  // namespace kmoe

@@ -8,7 +8,9 @@ and mixture weights are separate": a 2560-wide residual stream, 384 routed
 micro-experts plus one shared expert, top-6, and SwiGLU experts made of two
 2560->512 projections and one 512->2560 projection. The FP8 weight format
 follows the same page, section "The FP8 path is explicitly mixed precision":
-E4M3 values in 128x128 blocks, one FP32 scale per block.
+E4M3 values in 128x128 blocks, one FP32 scale per block. "w4" weights are held
+in 4 bits with a BF16 scale (and optionally a zero point) for every w4_group
+columns of a row; the stored order is that of kmoe_w4 in include/kmoe.h.
 
 Draw order (one torch.Generator on the target device, seeded once):
   x, router weight (drawn [d, E], stored transposed as [E, d]), correction
@@ -25,6 +27,8 @@ index E is the shared expert, so one allocation holds all E+1 experts.
   w_down       : [E+1, d, I]
   s_gate, s_up : [E+1, I/128, d/128]  FP32 block scales (E4M3 only)
   s_down       : [E+1, d/128, I/128]
+With "w4": w_* hold bytes [E+1, I, d/2] and [E+1, d, I/2], s_* BF16 [..., cols /
+group] and z_* (with zero points) bytes of the same shape.
 """
 from __future__ import annotations
 
@@ -44,8 +48,10 @@ class LayerConfig:
     K: int          # experts selected per token
     I: int          # SwiGLU intermediate width of one expert
     x_dtype: str    # "f32" | "bf16"
-    w_dtype: str    # "f32" | "bf16" | "e4m3" | "e4m3_a8" (E4M3 weights, FP8 activations in the expert GEMMs)
+    w_dtype: str    # "f32" | "bf16" | "e4m3" | "e4m3_a8" (E4M3 weights, FP8 activations in the expert GEMMs) | "w4"
     skew: bool = False   # Zipf expert popularity added to the correction bias
+    w4_group: int = 128      # "w4": columns that share a scale
+    w4_zeros: bool = False   # "w4": a zero point per group
 
     @property
     def fp8_weights(self) -> bool:
@@ -61,7 +67,7 @@ class LayerConfig:
         return replace(self, N=N)
 
 
-# The six workloads. "tiny" is small enough for the oracle to run every token
+# The workloads. "tiny" is small enough for the oracle to run every token
 # in well under a second; the rest use the Kolibri-1 layer shape.
 CONFIGS = {
     "tiny": LayerConfig("tiny", 128, 512, 64, 6, 128, "f32", "f32"),
@@ -72,6 +78,9 @@ CONFIGS = {
     # the same layers with FP8 activations in the expert GEMMs ("Inside Kolibri 1", FP8 section)
     "fp8a8_decode": LayerConfig("fp8a8_decode", 32, 2560, 384, 6, 512, "bf16", "e4m3_a8"),
     "fp8a8_prefill": LayerConfig("fp8a8_prefill", 4096, 2560, 384, 6, 512, "bf16", "e4m3_a8"),
+    # the same layers with the experts in 4 bits, one BF16 scale per 128 columns of a row
+    "w4_decode": LayerConfig("w4_decode", 32, 2560, 384, 6, 512, "bf16", "w4"),
+    "w4_prefill": LayerConfig("w4_prefill", 4096, 2560, 384, 6, 512, "bf16", "w4"),
     "skew": LayerConfig("skew", 65536, 2560, 384, 6, 512, "bf16", "bf16", skew=True),
 }
 
@@ -102,6 +111,34 @@ def _quantise_e4m3(w: torch.Tensor):
     return q, scale.to(torch.float32)
 
 
+W4_NIBBLES = (0, 2, 4, 6, 1, 3, 5, 7)     # columns of an 8-column word, lowest nibble first
+
+
+def pack_w4(q: torch.Tensor) -> torch.Tensor:
+    """Codes 0..15 [..., cols] (uint8) in the stored order of kmoe_w4: bytes [..., cols / 2]."""
+    w = q.unflatten(-1, (-1, 4, 4, 8)).transpose(-2, -3)[..., list(W4_NIBBLES)]
+    return (w[..., 0::2] | (w[..., 1::2] << 4)).flatten(-4).contiguous()
+
+
+def unpack_w4(codes: torch.Tensor) -> torch.Tensor:
+    """The codes 0..15 [..., cols] of stored bytes [..., cols / 2]."""
+    w = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).unflatten(-1, (-1, 4, 4, 8))
+    order = sorted(range(8), key=W4_NIBBLES.__getitem__)
+    return w[..., order].transpose(-2, -3).flatten(-4).contiguous()
+
+
+def _quantise_w4(w: torch.Tensor, group: int, zeros: bool):
+    """[rows, cols] FP32 into codes 0..15, BF16 scales and zero points (None without)."""
+    b = w.unflatten(-1, (-1, group))
+    hi, lo = b.amax(-1).clamp_(min=0), b.amin(-1).clamp_(max=0)
+    span = hi - lo if zeros else torch.maximum(hi, -lo)
+    s = (span / torch.full_like(span, 15.0 if zeros else 7.0)).to(torch.bfloat16)
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    z = torch.round(-lo / s.float()).clamp_(0, 15) if zeros else torch.full_like(lo, 8.0)
+    q = (torch.round(b / s.float().unsqueeze(-1)) + z.unsqueeze(-1)).clamp_(0, 15)
+    return q.to(torch.uint8).flatten(-2), s, (z.to(torch.uint8) if zeros else None)
+
+
 def make_inputs(cfg: LayerConfig, seed: int = 0, device: str | torch.device = "cpu") -> dict:
     """Draw one layer's inputs and weights for `cfg` on `device`."""
     dev = torch.device(device)
@@ -126,6 +163,13 @@ def make_inputs(cfg: LayerConfig, seed: int = 0, device: str | torch.device = "c
         s_gate = torch.empty((G, I // FP8_BLOCK, d // FP8_BLOCK), device=dev, dtype=torch.float32)
         s_up = torch.empty_like(s_gate)
         s_down = torch.empty((G, d // FP8_BLOCK, I // FP8_BLOCK), device=dev, dtype=torch.float32)
+    elif cfg.w_dtype == "w4":
+        w4 = {}
+        for m, (rows, cols) in {"gate": (I, d), "up": (I, d), "down": (d, I)}.items():
+            w4["w_" + m] = torch.empty((G, rows, cols // 2), device=dev, dtype=torch.uint8)
+            w4["s_" + m] = torch.empty((G, rows, cols // cfg.w4_group), device=dev, dtype=torch.bfloat16)
+            w4["z_" + m] = torch.empty((G, rows, cols // cfg.w4_group), device=dev, dtype=torch.uint8) \
+                if cfg.w4_zeros else None
     else:
         wt = _TORCH_DTYPES[cfg.w_dtype]
         w_gate = torch.empty((G, I, d), device=dev, dtype=wt)
@@ -139,11 +183,20 @@ def make_inputs(cfg: LayerConfig, seed: int = 0, device: str | torch.device = "c
             w_gate[e], s_gate[e] = _quantise_e4m3(g_)
             w_up[e], s_up[e] = _quantise_e4m3(u_)
             w_down[e], s_down[e] = _quantise_e4m3(d_)
+        elif cfg.w_dtype == "w4":
+            for m, w in (("gate", g_), ("up", u_), ("down", d_)):
+                q, s, z = _quantise_w4(w, cfg.w4_group, cfg.w4_zeros)
+                w4["w_" + m][e], w4["s_" + m][e] = pack_w4(q), s
+                if cfg.w4_zeros:
+                    w4["z_" + m][e] = z
         else:
             w_gate[e].copy_(g_)
             w_up[e].copy_(u_)
             w_down[e].copy_(d_)
-    out.update(w_gate=w_gate, w_up=w_up, w_down=w_down)
+    if cfg.w_dtype == "w4":
+        out.update(w4)
+    else:
+        out.update(w_gate=w_gate, w_up=w_up, w_down=w_down)
     if cfg.fp8_weights:
         out.update(s_gate=s_gate, s_up=s_up, s_down=s_down)
 
@@ -192,4 +245,4 @@ def to_host(inputs: dict) -> dict:
 
 
 __all__ = ["LayerConfig", "CONFIGS", "make_inputs", "make_x", "make_block_inputs", "to_host",
-           "expected_distinct_experts", "E4M3_MAX", "FP8_BLOCK", "SKEW_BETA", "SKEW_EMPTY"]
+           "expected_distinct_experts", "pack_w4", "unpack_w4", "E4M3_MAX", "FP8_BLOCK", "SKEW_BETA", "SKEW_EMPTY"]

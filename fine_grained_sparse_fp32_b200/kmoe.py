@@ -14,8 +14,9 @@ import torch
 from ._build import LIB
 
 KMOE_OK, KMOE_ERR_INVALID_ARG, KMOE_ERR_UNSUPPORTED, KMOE_ERR_CUDA, KMOE_ERR_WORKSPACE, KMOE_ERR_DEVICE = range(6)
-KMOE_F32, KMOE_BF16, KMOE_E4M3_B128, KMOE_E4M3_B128_A8 = 0, 1, 2, 3
-SCORES = {"sigmoid": 0, "softmax": 1}     # kmoe_score
+KMOE_F32, KMOE_BF16, KMOE_E4M3_B128, KMOE_E4M3_B128_A8, KMOE_W4 = range(5)
+SCORES = {"sigmoid": 0, "softmax": 1}     # kmoe_score, kmoe_route_score
+GROUP_SCORES = {"max": 0, "top2": 1}      # kmoe_group_score
 
 # Bytes at the head of a moe_grouped_ffn workspace: the status word, tickets
 # and the grouped FFN's unit counters (include/kmoe.h).
@@ -23,6 +24,8 @@ FFN_STATUS_BYTES = (64 + 1088) * 4
 
 EXPORTS = ["moe_workspace_size", "moe_router_topk", "moe_permute", "moe_permute_noalloc", "moe_grouped_ffn",
            "moe_combine", "moe_forward", "moe_block_workspace_size", "moe_block_forward", "moe_quant_1x128",
+           "moe_route", "moe_linear_w4", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
+           "moe_dequant_w4",
            "moe_device_status", "moe_set_wait_limit", "moe_last_error", "moe_abi_version"]
 
 
@@ -32,11 +35,78 @@ class KmoeError(RuntimeError):
         self.status = status
 
 
+class _W4Struct(ctypes.Structure):
+    """kmoe_w4: matrices held in 4 bits with group scales."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("group", ctypes.c_int)]
+
+
 class Experts(ctypes.Structure):
     """kmoe_experts: one stack of SwiGLU experts."""
     _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p),
-                ("dtype", ctypes.c_int)]
+                ("dtype", ctypes.c_int), ("w4", ctypes.POINTER(_W4Struct))]
+
+
+class _RoutingStruct(ctypes.Structure):
+    """kmoe_routing."""
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Routing:
+    """How experts are chosen and weighted (kmoe_routing in include/kmoe.h): scores from a sigmoid or
+    a softmax over all experts, the correction bias added to the score, selection limited to the best
+    groups of experts, weights optionally renormalised and scaled."""
+
+    def __init__(self, score: str = "sigmoid", n_groups: int = 1, topk_groups: int | None = None,
+                 group_score: str = "top2", renormalise: bool = True, scale: float = 1.0):
+        if score not in SCORES:
+            raise ValueError(f"score {score!r}: one of {sorted(SCORES)}")
+        if group_score not in GROUP_SCORES:
+            raise ValueError(f"group_score {group_score!r}: one of {sorted(GROUP_SCORES)}")
+        self.score, self.n_groups, self.group_score = score, n_groups, group_score
+        self.topk_groups = n_groups if topk_groups is None else topk_groups
+        self.renormalise, self.scale = renormalise, scale
+        self._struct = _RoutingStruct(SCORES[score], self.n_groups, self.topk_groups, GROUP_SCORES[group_score],
+                                      int(bool(renormalise)), float(scale))
+        self._ref = ctypes.byref(self._struct)
+
+
+class W4:
+    """Weights in the 4-bit format of kmoe_w4: codes uint8 [..., rows, cols / 2], scales BF16
+    [..., rows, cols / group], zeros uint8 of the scales' shape or None (8 everywhere). One leading
+    dimension stacks the matrices of several experts."""
+
+    def __init__(self, codes, scales, zeros=None):
+        if codes.dim() not in (2, 3) or codes.dtype != torch.uint8 or not codes.is_contiguous():
+            raise ValueError("codes: a dense uint8 tensor [rows, cols / 2] or [E, rows, cols / 2]")
+        self.rows, self.cols = codes.shape[-2], codes.shape[-1] * 2
+        self.E = codes.shape[0] if codes.dim() == 3 else 1
+        groups = scales.shape[-1] if scales.dim() else 0
+        if groups < 1 or self.cols % groups:
+            raise ValueError("scales: [..., rows, cols / group]")
+        self.group = self.cols // groups
+        shape = tuple(codes.shape[:-1]) + (groups,)
+        _dense(scales, "scales", torch.bfloat16, shape, codes.device)
+        if zeros is not None:
+            _dense(zeros, "zeros", torch.uint8, shape, codes.device)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self._struct = _W4Struct(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                 self.group)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _dense(t, name, dtype, shape, device):
+    """Refuses a tensor that the library would read wrongly."""
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
 
 
 _lib = None
@@ -70,10 +140,21 @@ def load(path: str | None = None):
     lib.moe_block_forward.argtypes = [vp, i, i, i, i, i, i, vp, vp, ctypes.c_float, vp, vp,
                                       ctypes.POINTER(Experts), ctypes.POINTER(Experts), vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_quant_1x128.argtypes = [vp, i, i, vp, vp, vp]
+    lib.moe_route.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp]
+    lib.moe_linear_w4.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp]
+    lib.moe_forward_routed.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, ctypes.POINTER(Experts),
+                                       ctypes.POINTER(Experts), vp, i, vp, vp, vp, vp, sz, vp]
+    lib.moe_block_forward_routed.argtypes = [vp, i, i, i, i, i, vp, vp, vp, ctypes.c_float, vp, vp,
+                                             ctypes.POINTER(Experts), ctypes.POINTER(Experts), vp, vp, vp, vp, vp,
+                                             vp, sz, vp]
+    lib.moe_quant_w4.argtypes = [vp, i, i, i, i, vp, vp, vp, vp]
+    lib.moe_dequant_w4.argtypes = [vp, i, i, vp, i, vp]
     lib.moe_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
     lib.moe_set_wait_limit.argtypes = [ctypes.c_longlong]
     for f in ("moe_router_topk", "moe_permute", "moe_permute_noalloc", "moe_grouped_ffn", "moe_combine",
-              "moe_forward", "moe_block_forward", "moe_quant_1x128", "moe_device_status", "moe_set_wait_limit"):
+              "moe_forward", "moe_block_forward", "moe_quant_1x128", "moe_device_status", "moe_set_wait_limit",
+              "moe_route", "moe_linear_w4", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
+              "moe_dequant_w4"):
         getattr(lib, f).restype = i
     if lib.moe_abi_version() != 3:
         raise RuntimeError("libkmoe ABI version mismatch")
@@ -95,12 +176,47 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _call(name, t, stream, *args):
+    """Calls entry point `name` for tensors on t's device: on `stream`, or on that device's current
+    stream, with that device current."""
+    dev = t.device.index
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device != t.device:
+        raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+    else:
+        s = stream.cuda_stream
+    fn = getattr(_lib or load(), name)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status:
+        _check(status)
+
+
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on a CUDA device")
+
+
+_DTYPE_CODES = {torch.float32: KMOE_F32, torch.bfloat16: KMOE_BF16}
+
+
 def dtype_code(t: torch.dtype) -> int:
-    return {torch.float32: KMOE_F32, torch.bfloat16: KMOE_BF16}[t]
+    return _DTYPE_CODES[t]
+
+
+def _act_code(t, name):
+    if t not in _DTYPE_CODES:
+        raise ValueError(f"{name}: dtype {t}, must be torch.float32 or torch.bfloat16")
+    return _DTYPE_CODES[t]
 
 
 def w_dtype_code(name: str) -> int:
-    return {"f32": KMOE_F32, "bf16": KMOE_BF16, "e4m3": KMOE_E4M3_B128, "e4m3_a8": KMOE_E4M3_B128_A8}[name]
+    return {"f32": KMOE_F32, "bf16": KMOE_BF16, "e4m3": KMOE_E4M3_B128, "e4m3_a8": KMOE_E4M3_B128_A8,
+            "w4": KMOE_W4}[name]
 
 
 def act_dtype_for(w_dtype: str) -> torch.dtype:
@@ -112,6 +228,16 @@ def experts_of(layer: dict, which: str = "routed") -> Experts:
     """kmoe_experts for a generator-layout layer: routed = experts 0..E-1, shared = index E."""
     cfg = layer["cfg"]
     e = cfg.E if which == "shared" else 0
+    if cfg.w_dtype == "w4":
+        shapes = {"gate": (cfg.I, cfg.d), "up": (cfg.I, cfg.d), "down": (cfg.d, cfg.I)}
+        w4 = []
+        for m, (rows, cols) in shapes.items():
+            w = W4(layer["w_" + m], layer["s_" + m], layer.get("z_" + m))
+            if w.codes.dim() != 3 or (w.E <= e or w.E < cfg.E or (w.rows, w.cols) != (rows, cols)):
+                raise ValueError(f"w_{m}: shape {tuple(w.codes.shape)} is not [{cfg.E} + 1, {rows}, {cols // 2}]")
+            w4.append(_W4Struct(*(None if t is None else t[e].data_ptr() for t in (w.codes, w.scales, w.zeros)),
+                                w.group))
+        return Experts(dtype=KMOE_W4, w4=(_W4Struct * 3)(*w4))
 
     def at(name):
         t = layer.get(name)
@@ -232,14 +358,21 @@ class Layer:
 
     `forward(x)` is one moe_forward call and `block_forward(h, ...)` one
     moe_block_forward call (workspace sized for it when `block` is set);
-    outputs are written into tensors owned here (or passed in)."""
+    outputs are written into tensors owned here (or passed in). With `routing`
+    (a Routing) both choose and weigh the experts by it (moe_forward_routed,
+    moe_block_forward_routed), `score` is not used and the layer's bias may be
+    None. `grouped_ffn` is one moe_grouped_ffn call on the same workspace. A
+    workspace serves one call at a time: calls on several streams, and graphs
+    that may run at the same time, need a Layer each."""
 
     def __init__(self, layer: dict, max_tokens: int, y_dtype=torch.bfloat16, score: str = "sigmoid",
-                 block: bool = False):
+                 block: bool = False, routing: Routing | None = None):
         self.layer = layer
+        self.routing = routing
         cfg = self.cfg = layer["cfg"]
         self.routed = experts_of(layer, "routed")
         self.shared = experts_of(layer, "shared")
+        self._routed_ref, self._shared_ref = ctypes.byref(self.routed), ctypes.byref(self.shared)
         dev = layer["w_gate"].device
         self.x_code = w_dtype_code(cfg.x_dtype)
         if block:
@@ -261,6 +394,12 @@ class Layer:
         if y is None:
             y = torch.empty((N, cfg.d), dtype=self.y_dtype, device=x.device)
         L = self.layer
+        if self.routing is not None:
+            _call("moe_forward_routed", x, stream, _ptr(x), dtype_code(x.dtype), N, cfg.d, cfg.E, cfg.K, cfg.I,
+                  self.routing._ref, _ptr(L["w_router"]), _ptr(L["bias"]), ctypes.byref(self.routed),
+                  ctypes.byref(self.shared), _ptr(y), dtype_code(y.dtype), _ptr(topk_idx), _ptr(topk_w), _ptr(counts),
+                  _ptr(self.ws), self.ws.numel())
+            return y
         _check(load().moe_forward(_ptr(x), dtype_code(x.dtype), N, cfg.d, cfg.E, cfg.K, cfg.I, self.score,
                                   _ptr(L["w_router"]), _ptr(L["bias"]), ctypes.byref(self.routed),
                                   ctypes.byref(self.shared), _ptr(y), dtype_code(y.dtype), _ptr(topk_idx),
@@ -278,6 +417,12 @@ class Layer:
         if h_out is None:
             h_out = torch.empty_like(h)
         L = self.layer
+        if self.routing is not None:
+            _call("moe_block_forward_routed", h, stream, _ptr(h), N, cfg.d, cfg.E, cfg.K, cfg.I, self.routing._ref,
+                  _ptr(gamma_pre), _ptr(gamma_post), float(eps), _ptr(L["w_router"]), _ptr(L["bias"]),
+                  ctypes.byref(self.routed), ctypes.byref(self.shared), _ptr(h_out), _ptr(x_out), _ptr(topk_idx),
+                  _ptr(topk_w), _ptr(counts), _ptr(self.ws), self.ws.numel())
+            return h_out
         _check(load().moe_block_forward(_ptr(h), N, cfg.d, cfg.E, cfg.K, cfg.I, self.score, _ptr(gamma_pre),
                                         _ptr(gamma_post), float(eps), _ptr(L["w_router"]), _ptr(L["bias"]),
                                         ctypes.byref(self.routed), ctypes.byref(self.shared), _ptr(h_out),
@@ -286,11 +431,36 @@ class Layer:
         return h_out
 
 
-def moe_forward(x, layer, y_dtype=torch.bfloat16, with_outputs=False, stream=None, score="sigmoid"):
+    def grouped_ffn(self, x, perm_token, offsets, with_shared=True, out=None, stream=None):
+        """moe_grouped_ffn: y_perm [N*K, d] and y_shared [N, d] (None without the shared expert) of x
+        dispatched by perm_token and offsets (moe_permute)."""
+        cfg = self.cfg
+        N = x.shape[0]
+        if N > self.max_tokens:
+            raise ValueError("more tokens than the workspace was sized for")
+        _dense(x, "x", tuple(_DTYPE_CODES), (N, cfg.d), self.ws.device)
+        _dense(perm_token, "perm_token", torch.int32, (N * cfg.K,), x.device)
+        _dense(offsets, "offsets", torch.int32, (cfg.E + 1,), x.device)
+        adt = act_dtype_for(cfg.w_dtype)
+        if out is None:
+            y_perm = torch.empty((N * cfg.K, cfg.d), dtype=adt, device=x.device)
+            y_shared = torch.empty((N, cfg.d), dtype=adt, device=x.device) if with_shared else None
+        else:
+            y_perm, y_shared = out
+            _dense(y_perm, "y_perm", adt, (N * cfg.K, cfg.d), x.device)
+            if with_shared:
+                _dense(y_shared, "y_shared", adt, (N, cfg.d), x.device)
+        _call("moe_grouped_ffn", x, stream, x.data_ptr(), _DTYPE_CODES[x.dtype], N, cfg.d, cfg.I, cfg.E, cfg.K,
+              perm_token.data_ptr(), offsets.data_ptr(), self._routed_ref, self._shared_ref if with_shared else None,
+              y_perm.data_ptr(), y_shared.data_ptr() if with_shared else None, self.ws.data_ptr(), self.ws.numel())
+        return y_perm, y_shared
+
+
+def moe_forward(x, layer, y_dtype=torch.bfloat16, with_outputs=False, stream=None, score="sigmoid", routing=None):
     """One whole-layer call; with_outputs also returns (topk_idx, topk_w, counts)."""
     cfg = layer["cfg"]
     N = x.shape[0]
-    lay = Layer(layer, N, y_dtype, score)
+    lay = Layer(layer, N, y_dtype, score, routing=routing)
     if not with_outputs:
         return lay.forward(x, stream=stream)
     idx = torch.empty((N, cfg.K), dtype=torch.int32, device=x.device)
@@ -301,11 +471,11 @@ def moe_forward(x, layer, y_dtype=torch.bfloat16, with_outputs=False, stream=Non
 
 
 def moe_block_forward(h, layer, gamma_pre, gamma_post, eps: float, with_outputs=False, stream=None,
-                      score="sigmoid", h_out=None):
+                      score="sigmoid", h_out=None, routing=None):
     """One sandwich-block call; with_outputs also returns (x, topk_idx, topk_w, counts)."""
     cfg = layer["cfg"]
     N = h.shape[0]
-    lay = Layer(layer, N, torch.bfloat16, score, block=True)
+    lay = Layer(layer, N, torch.bfloat16, score, block=True, routing=routing)
     if not with_outputs:
         return lay.block_forward(h, gamma_pre, gamma_post, eps, h_out=h_out, stream=stream)
     idx = torch.empty((N, cfg.K), dtype=torch.int32, device=h.device)
@@ -326,3 +496,96 @@ def moe_quant_1x128(x, codes=None, scales=None, stream=None):
         scales = torch.empty((rows, cols // 128), dtype=torch.float32, device=x.device)
     _check(load().moe_quant_1x128(_ptr(x), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
+
+
+def moe_route(logits, K, bias=None, routing=None, topk_idx=None, topk_w=None, stream=None):
+    """Experts and weights of logits [N, E] (FP32 or BF16) by `routing` (a Routing; the default is a
+    renormalised sigmoid): topk_idx [N, K] int32, topk_w [N, K] FP32."""
+    if logits.dim() != 2:
+        raise ValueError("logits: [N, E]")
+    N, E = logits.shape
+    dev = logits.device
+    _on_gpu(logits, "logits")
+    _dense(logits, "logits", tuple(_DTYPE_CODES), (N, E), dev)
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E,), dev)
+    if topk_idx is None:
+        topk_idx = torch.empty((N, K), dtype=torch.int32, device=dev)
+    else:
+        _dense(topk_idx, "topk_idx", torch.int32, (N, K), dev)
+    if topk_w is None:
+        topk_w = torch.empty((N, K), dtype=torch.float32, device=dev)
+    else:
+        _dense(topk_w, "topk_w", torch.float32, (N, K), dev)
+    _call("moe_route", logits, stream, logits.data_ptr(), _DTYPE_CODES[logits.dtype],
+          None if bias is None else bias.data_ptr(), N, E, K, (routing or _DEFAULT_ROUTING)._ref, topk_idx.data_ptr(),
+          topk_w.data_ptr())
+    return topk_idx, topk_w
+
+
+_DEFAULT_ROUTING = Routing()
+
+
+def moe_quant_w4(w, group=128, zeros=False, out=None, stream=None) -> W4:
+    """w [..., rows, cols] (FP32 or BF16) in the 4-bit format, with zero points if `zeros`. `out`: a W4 of
+    the same shape, group and zero points, which is overwritten."""
+    if w.dim() not in (2, 3):
+        raise ValueError("w: [rows, cols] or [E, rows, cols]")
+    _on_gpu(w, "w")
+    _dense(w, "w", tuple(_DTYPE_CODES), w.shape, w.device)
+    lead, cols = tuple(w.shape[:-1]), w.shape[-1]
+    if group not in (32, 64, 128) or cols % 128 or cols < 128:
+        raise ValueError(f"group {group} (32, 64 or 128) of cols {cols} (a multiple of 128)")
+    if out is None:
+        shape = lead + (cols // group,)
+        out = W4(torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device),
+                 torch.empty(shape, dtype=torch.bfloat16, device=w.device),
+                 torch.empty(shape, dtype=torch.uint8, device=w.device) if zeros else None)
+    elif tuple(out.codes.shape) != lead + (cols // 2,) or out.group != group or (out.zeros is None) == bool(zeros) \
+            or out.codes.device != w.device:
+        raise ValueError("out: another shape, group, device or zero points")
+    _call("moe_quant_w4", w, stream, w.data_ptr(), _DTYPE_CODES[w.dtype], w.numel() // cols, cols, group,
+          out.codes.data_ptr(), out.scales.data_ptr(), None if out.zeros is None else out.zeros.data_ptr())
+    return out
+
+
+def moe_dequant_w4(w4: W4, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of 4-bit weights, [..., rows, cols] in FP32 (exact) or BF16 (rounded)."""
+    shape = tuple(w4.codes.shape[:-1]) + (w4.cols,)
+    _on_gpu(w4.codes, "codes")
+    if out is None:
+        _act_code(dtype, "out")
+        out = torch.empty(shape, dtype=dtype, device=w4.codes.device)
+    else:
+        _dense(out, "out", tuple(_DTYPE_CODES), shape, w4.codes.device)
+    _call("moe_dequant_w4", w4.codes, stream, w4._ref, out.numel() // w4.cols, w4.cols, out.data_ptr(),
+          _DTYPE_CODES[out.dtype])
+    return out
+
+
+def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat16, out=None, stream=None):
+    """y[p] = W_e x[perm_token[p]] with 4-bit weights: one matrix for all rows, or (offsets [E + 1], from
+    moe_permute) the matrix of the expert whose range holds p. x [N, cols] BF16; y [P, rows]."""
+    if x.dim() != 2:
+        raise ValueError("x: [N, cols]")
+    _on_gpu(x, "x")
+    dev = x.device
+    N = x.shape[0]
+    _dense(x, "x", torch.bfloat16, (N, w4.cols), dev)
+    if w4.codes.device != dev:
+        raise ValueError(f"w4: on {w4.codes.device}, not on {dev}")
+    P = N
+    if perm_token is not None:
+        P = perm_token.numel()
+        _dense(perm_token, "perm_token", torch.int32, (P,), dev)
+    if offsets is not None:
+        _dense(offsets, "offsets", torch.int32, (w4.E + 1,), dev)
+    if out is None:
+        _act_code(y_dtype, "y")
+        out = torch.empty((P, w4.rows), dtype=y_dtype, device=dev)
+    else:
+        _dense(out, "out", tuple(_DTYPE_CODES), (P, w4.rows), dev)
+    _call("moe_linear_w4", x, stream, x.data_ptr(), KMOE_BF16, N, P, w4.rows, w4.cols, w4.E,
+          None if perm_token is None else perm_token.data_ptr(), None if offsets is None else offsets.data_ptr(),
+          w4._ref, out.data_ptr(), _DTYPE_CODES[out.dtype])
+    return out

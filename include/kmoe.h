@@ -31,7 +31,8 @@
  *   - Return value: KMOE_OK, or an error code with a message available from
  *     moe_last_error(). Argument errors are detected on the host before any
  *     work is enqueued. KMOE_ERR_CUDA reports a failed launch.
- *   - Inputs are assumed finite.
+ *   - Inputs are assumed finite, unless an entry point says what it does with
+ *     others.
  */
 #ifndef KMOE_H
 #define KMOE_H
@@ -70,6 +71,7 @@ typedef enum {
     KMOE_F32 = 0,           /* IEEE binary32 */
     KMOE_BF16 = 1,          /* bfloat16 */
     KMOE_E4M3_B128 = 2,     /* OCP E4M3 bytes + one FP32 scale per 128x128 block */
+    KMOE_W4 = 4,            /* expert weights only: 4-bit codes with group scales (kmoe_w4) */
     KMOE_E4M3_B128_A8 = 3   /* expert weights only: stored exactly as KMOE_E4M3_B128, and
                                the expert GEMMs run on FP8 activations ("Inside Kolibri 1",
                                FP8 section: activations quantised dynamically in groups of
@@ -86,12 +88,42 @@ typedef enum {
 } kmoe_dtype;
 
 /*
+ * G matrices [rows, cols] held in 4 bits, with one scale (and, optionally, one
+ * zero point) for every `group` consecutive columns of a row:
+ *   W[g][r][c] = (q[g][r][c] - z[g][r][c / group]) * s[g][r][c / group]
+ * with codes q and zero points z in 0..15; without zero points z = 8
+ * everywhere. group is 32, 64 or 128; cols is a multiple of 128; rows is any
+ * number. Values are used as this product, not rounded to BF16 first, except
+ * where an entry point says so.
+ *   codes  : device [G, rows, cols / 2] bytes. The 128 columns of a block take
+ *            64 bytes: sixteen little-endian 32-bit words of eight columns,
+ *            columns 8v .. 8v + 7 of the block in word 4 * (v % 4) + v / 4 (a
+ *            transposed 4 x 4 square of words, so that 16 consecutive bytes
+ *            hold one matrix fragment's share of each 32 columns). In a word,
+ *            column 2i is at bits 4i .. 4i + 3 and column 2i + 1 at bits
+ *            16 + 4i .. 19 + 4i, for i = 0..3.
+ *   scales : device [G, rows, cols / group] BF16
+ *   zeros  : device [G, rows, cols / group] bytes, or NULL
+ * moe_quant_w4 writes this format.
+ */
+typedef struct {
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;
+    int group;
+} kmoe_w4;
+
+/*
  * One stack of G SwiGLU experts (routed: G = E; shared: G = 1).
  *   w_gate, w_up : device [G, I, d]  row i = weights of intermediate feature i
  *   w_down       : device [G, d, I]  row j = weights of output feature j
  *   s_gate, s_up : device [G, I/128, d/128] FP32 block scales (E4M3 only,
  *   s_down       : device [G, d/128, I/128]  else ignored and may be NULL)
  * The weight value of an E4M3 element is decode(q) * scale of its block.
+ * With KMOE_W4 the six pointers above are ignored and w4 points to three host
+ * structs, {gate, up, down}: [G, I, d] twice and [G, d, I]; gate and up have
+ * the same group size, and both have zero points or neither. w4 is read with
+ * KMOE_W4 only, so a caller built without this member is not affected by it.
  */
 typedef struct {
     const void *w_gate;
@@ -101,7 +133,45 @@ typedef struct {
     const float *s_up;
     const float *s_down;
     int dtype;           /* kmoe_dtype of the weights */
+    const kmoe_w4 *w4;   /* KMOE_W4 only: {gate, up, down} */
 } kmoe_experts;
+
+/*
+ * How experts are chosen and weighted from the logits l of a token, for the
+ * entry points that take it:
+ *   s    = sigmoid(l), or the softmax of l over all E experts     (score)
+ *   c    = s + bias                                     (selection score)
+ *   group score = the largest c of a group, or the sum of its two largest;
+ *          the E experts form n_groups groups of consecutive experts, and the
+ *          topk_groups groups with the largest score stay
+ *   idx  = the K experts of the groups that stayed with the largest c,
+ *          largest first
+ *   w    = s[idx], divided by their sum with renormalise, times scale
+ * On equal scores the lower group or expert index wins; c is compared as
+ * computed in FP64 from the FP32 (or BF16) logits and the FP32 bias. An expert
+ * whose logit or bias is -infinity or NaN is masked: s = 0, and it is chosen
+ * only where the groups that stayed have no other expert left (lowest index
+ * first, weight 0). A masked expert does not count towards a group's score; a
+ * group of masked experts comes last. A sum of 0 leaves the weights 0.
+ */
+typedef enum {
+    KMOE_ROUTE_SIGMOID = 0,
+    KMOE_ROUTE_SOFTMAX = 1
+} kmoe_route_score;
+
+typedef enum {
+    KMOE_GROUP_MAX = 0,
+    KMOE_GROUP_TOP2 = 1
+} kmoe_group_score;
+
+typedef struct {
+    int score;          /* kmoe_route_score */
+    int n_groups;       /* 1..32, a divisor of E; 1 = no groups */
+    int topk_groups;    /* 1..n_groups, with topk_groups * E / n_groups >= K */
+    int group_score;    /* kmoe_group_score (ignored with n_groups == topk_groups) */
+    int renormalise;    /* 0 or 1 */
+    float scale;        /* finite */
+} kmoe_routing;
 
 /*
  * Bytes of device workspace that any entry point below needs for these
@@ -135,6 +205,16 @@ kmoe_status moe_router_topk(const void *x, int x_dtype, const float *w_router,
                             const float *bias, int N, int d, int E, int K, int score,
                             float *logits, int32_t *topk_idx, float *topk_w,
                             void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Routing from given logits by the rule of kmoe_routing.
+ * logits   device [N, E], l_dtype KMOE_F32 or KMOE_BF16 (finite or not)
+ * bias     device [E] FP32, or NULL for none
+ * topk_idx device [N, K] int32 output;  topk_w device [N, K] FP32 output
+ * routing  host struct, read during the call
+ */
+kmoe_status moe_route(const void *logits, int l_dtype, const float *bias, int N, int E, int K,
+                      const kmoe_routing *routing, int32_t *topk_idx, float *topk_w, void *stream);
 
 /*
  * Dispatch: histogram, exclusive scan and a stable permutation of the N*K
@@ -193,6 +273,8 @@ kmoe_status moe_permute_noalloc(const int32_t *topk_idx, int N, int K, int E,
  * row (x, and H before the down projection) is held as two E4M3 terms with
  * one FP32 scale, v = s * (hi + lo / 16), within about 2^-8 of |v| (BF16's
  * own rounding is 2^-9), over the whole BF16 range.
+ * With KMOE_W4 weights x must be BF16 (KMOE_ERR_UNSUPPORTED otherwise); H is
+ * BF16.
  * x device [N, d] (x_dtype F32 or BF16). perm_token, offsets as produced by
  * moe_permute. Output dtype: FP32 when the weights are FP32, else BF16.
  * y_perm device [N*K, d]; y_shared device [N, d]. With KMOE_E4M3_B128_A8
@@ -206,6 +288,22 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
                             const kmoe_experts *routed, const kmoe_experts *shared,
                             void *y_perm, void *y_shared,
                             void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Products with 4-bit weights, one matrix or one per expert:
+ *   y[p] = W_e x[perm_token ? perm_token[p] : p]   for offsets[e] <= p < offsets[e+1]
+ * accumulated in FP32. With offsets NULL every row uses W_0 (E must be 1).
+ * Every x[.] row is BF16; a row p that no expert's range holds keeps what y
+ * held. Row ranges are cut to [0, P), and a perm_token entry outside [0, N)
+ * stands for a row of zeros.
+ * x device [N, cols] BF16; w: E matrices [rows, cols]; perm_token device [P]
+ * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
+ * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,
+ * 128 <= cols <= 65536 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
+ */
+kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
+                          const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,
+                          void *y, int y_dtype, void *stream);
 
 /*
  * Weighted combine ("Kolibri 1 Deep Dive", section 1, the layer-output
@@ -238,6 +336,17 @@ kmoe_status moe_forward(const void *x, int x_dtype, int N, int d, int E, int K, 
                         void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * moe_forward with the routing rule of kmoe_routing in place of `score`
+ * (logits in FP32 as in moe_router_topk); bias may be NULL.
+ */
+kmoe_status moe_forward_routed(const void *x, int x_dtype, int N, int d, int E, int K, int I,
+                               const kmoe_routing *routing, const float *w_router, const float *bias,
+                               const kmoe_experts *routed, const kmoe_experts *shared,
+                               void *y, int y_dtype,
+                               int32_t *topk_idx_out, float *topk_w_out, int32_t *counts_out,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/*
  * The sandwich block around the layer ("Inside Kolibri 1", section "The
  * released stack": RMSNorm before and after the MoE sublayer, residual added
  * after the second norm):
@@ -251,8 +360,8 @@ kmoe_status moe_forward(const void *x, int x_dtype, int N, int d, int E, int K, 
  * [N, d] BF16, which may be the same buffer as h (each element of h is read
  * before its h_out element is written, by the same thread) but must not
  * overlap it otherwise. x_out: optional device [N, d] BF16 output of the
- * normalised layer input x (NULL keeps it in the workspace). Routed (and shared) weights must be BF16 or E4M3
- * with 128 x 128 scales (KMOE_E4M3_B128 or KMOE_E4M3_B128_A8) and d a multiple of 256
+ * normalised layer input x (NULL keeps it in the workspace). Routed (and shared) weights must be BF16, E4M3
+ * with 128 x 128 scales (KMOE_E4M3_B128 or KMOE_E4M3_B128_A8) or KMOE_W4, and d a multiple of 256
  * (KMOE_ERR_UNSUPPORTED otherwise), and
  * (K + 1) * d <= 25600 BF16 values must fit the combine's staging buffer
  * (K + 1 counts the shared expert). Other arguments and outputs as in
@@ -269,6 +378,19 @@ kmoe_status moe_block_forward(const void *h, int N, int d, int E, int K, int I, 
                               void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * moe_block_forward with the routing rule of kmoe_routing in place of `score`;
+ * bias may be NULL.
+ */
+kmoe_status moe_block_forward_routed(const void *h, int N, int d, int E, int K, int I,
+                                     const kmoe_routing *routing,
+                                     const void *gamma_pre, const void *gamma_post, float eps,
+                                     const float *w_router, const float *bias,
+                                     const kmoe_experts *routed, const kmoe_experts *shared,
+                                     void *h_out, void *x_out,
+                                     int32_t *topk_idx_out, float *topk_w_out, int32_t *counts_out,
+                                     void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Dynamic FP8 quantisation of activations ("Inside Kolibri 1", FP8 section:
  * activations are quantised dynamically in groups of 1 x 128). For each row
  * and each group of 128 consecutive columns:
@@ -282,6 +404,31 @@ kmoe_status moe_block_forward(const void *h, int N, int d, int E, int K, int I, 
  */
 kmoe_status moe_quant_1x128(const void *x, int rows, int cols, uint8_t *codes, float *scales,
                             void *stream);
+
+/*
+ * Quantisation of weights into the 4-bit format of kmoe_w4, row by row and
+ * group by group, in FP32 with IEEE division, rint to nearest even:
+ *   without zero points (zeros NULL):
+ *     s = bf16(max |w| / 7), 1 where that is 0
+ *     q = clamp(rint(w / s), -8, 7) + 8
+ *   with zero points, lo = min(w, 0) and hi = max(w, 0) over the group:
+ *     s = bf16((hi - lo) / 15), 1 where that is 0
+ *     z = clamp(rint(-lo / s), 0, 15)
+ *     q = clamp(rint(w / s) + z, 0, 15)
+ * w device [rows, cols] of w_dtype (F32 or BF16), |w| < 1e38 (a group holding
+ * an Inf or a NaN gets an unspecified scale and codes); codes, scales, zeros:
+ * outputs as in kmoe_w4 with G * rows rows. cols a multiple of 128; group 32,
+ * 64 or 128. rows == 0 is a no-op.
+ */
+kmoe_status moe_quant_w4(const void *w, int w_dtype, int rows, int cols, int group,
+                         uint8_t *codes, void *scales, uint8_t *zeros, void *stream);
+
+/*
+ * The values of 4-bit weights: out[r][c] = (q - z) * s, exact in FP32 and
+ * rounded to nearest even in BF16. w: [rows, cols]; out device [rows, cols] of
+ * out_dtype (F32 or BF16). rows == 0 is a no-op.
+ */
+kmoe_status moe_dequant_w4(const kmoe_w4 *w, int rows, int cols, void *out, int out_dtype, void *stream);
 
 /*
  * Device status word. moe_forward, moe_block_forward and moe_grouped_ffn clear the first 4
