@@ -174,8 +174,12 @@ static kmoe_status check_shared(const kmoe_experts *shared, const kmoe_experts *
 
 static size_t act_bytes(int w_dtype) { return w_dtype == KMOE_F32 ? 4 : 2; }
 
-// Bytes of one H element: the output dtype, or an E4M3 code with FP8 activations.
-static size_t h_bytes(int w_dtype) { return w_dtype == KMOE_E4M3_B128_A8 ? 1 : act_bytes(w_dtype); }
+// Bytes of one H element: the output dtype, an E4M3 code with FP8 activations,
+// or FP32 with 4-bit weights.
+static size_t h_bytes(int w_dtype)
+{
+    return w_dtype == KMOE_E4M3_B128_A8 ? 1 : w_dtype == KMOE_W4 ? 4 : act_bytes(w_dtype);
+}
 
 // Batches that run E4M3 weights on the FP8 tensor cores with two-term
 // (BF16-precision) activations: below kTcMinTokens tokens.
@@ -302,7 +306,8 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
     }
     a.y = h;
     KMOE_TRY(launch_w4(a, st));
-    b.x = static_cast<const __nv_bfloat16 *>(h);
+    b.x = h;
+    b.x_f32 = true;
     b.x_rows = a.P + a.n_shared;
     b.x_by_row = true;
     b.rows = d;
@@ -730,7 +735,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     if (N > (1 << 30) || P > (1 << 30)) return fail(KMOE_ERR_UNSUPPORTED, "N=%d, P=%d: at most 2^30 rows", N, P);
     if (rows < 1 || rows > 65536) return fail(KMOE_ERR_UNSUPPORTED, "rows=%d: supported 1..65536", rows);
     KMOE_TRY(check_w4_cols(cols));
-    if (cols > 65536) return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: supported up to 65536", cols);
+    if (cols > 10240) return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: supported up to 10240", cols);
     if (E < 1 || E > 1024) return fail(KMOE_ERR_UNSUPPORTED, "E=%d: supported 1..1024", E);
     if (!offsets && E != 1) return fail(KMOE_ERR_INVALID_ARG, "E=%d matrices need offsets", E);
     if (!perm_token && P > N) return fail(KMOE_ERR_INVALID_ARG, "P=%d rows of y without perm_token, x has N=%d", P, N);
@@ -741,7 +746,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     KMOE_TRY(check_ptr(offsets, "offsets", true));
     KMOE_TRY(check_ptr(y, "y"));
     W4Product a{};
-    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.x = x;
     a.x_rows = N;
     a.P = P;
     a.rows = rows;

@@ -23,27 +23,7 @@ struct W4Ptrs {
     const uint8_t *z;     // NULL: 8 everywhere
 };
 
-__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<__nv_bfloat162 *>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t *>(&v); }
-
-// Columns 2i, 2i + 1 of a word as BF16 values 128 + q: the four bits are the
-// low mantissa bits of a BF16 number with exponent 7 (its last place is 1).
-__device__ __forceinline__ uint32_t w4_biased(uint32_t word, int i)
-{
-    return ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-}
-
-// The same pair as q - z, with zz = {128 + z, 128 + z}: exact in BF16, since
-// both sides are whole numbers below 256 and their difference is below 16.
-__device__ __forceinline__ uint32_t w4_codes(uint32_t word, int i, __nv_bfloat162 zz)
-{
-    return as_u32(__hsub2(as_bf162(w4_biased(word, i)), zz));
-}
-
-__device__ __forceinline__ __nv_bfloat162 w4_zero(uint32_t z)      // {128 + z, 128 + z}
-{
-    return as_bf162((0x4300u | z) * 0x00010001u);
-}
 
 }  // namespace kmoe
 
@@ -60,12 +40,13 @@ kmoe_status launch_dequant_w4(const W4Ptrs &w, int group, int rows, int cols, vo
 // expert. x row of p: perm[p] below P (p itself without perm), p - P
 // for the shared expert, or p itself everywhere with x_by_row.
 struct W4Product {
-    const __nv_bfloat16 *x;
+    const void *x;
     int x_rows, P, n_shared, rows, cols, E;
     const int32_t *perm, *offsets;       // offsets NULL: E == 1, all P rows
     W4Ptrs w, up, w_shared, up_shared;   // up.q NULL: no SwiGLU
     int group;
     bool x_by_row;                       // x is indexed by p, the shared rows behind the P routed ones
+    bool x_f32;                          // x (H) in FP32
     void *y, *y_shared;                  // y [P (+ n_shared for SwiGLU), rows]
     int y_dtype;
 };

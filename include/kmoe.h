@@ -273,8 +273,8 @@ kmoe_status moe_permute_noalloc(const int32_t *topk_idx, int N, int K, int E,
  * row (x, and H before the down projection) is held as two E4M3 terms with
  * one FP32 scale, v = s * (hi + lo / 16), within about 2^-8 of |v| (BF16's
  * own rounding is 2^-9), over the whole BF16 range.
- * With KMOE_W4 weights x must be BF16 (KMOE_ERR_UNSUPPORTED otherwise); H is
- * BF16.
+ * With KMOE_W4 weights x must be BF16 (KMOE_ERR_UNSUPPORTED otherwise) and H is
+ * FP32.
  * x device [N, d] (x_dtype F32 or BF16). perm_token, offsets as produced by
  * moe_permute. Output dtype: FP32 when the weights are FP32, else BF16.
  * y_perm device [N*K, d]; y_shared device [N, d]. With KMOE_E4M3_B128_A8
@@ -299,7 +299,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * x device [N, cols] BF16; w: E matrices [rows, cols]; perm_token device [P]
  * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
  * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,
- * 128 <= cols <= 65536 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
+ * 128 <= cols <= 10240 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
  */
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,
