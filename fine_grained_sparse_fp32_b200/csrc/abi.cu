@@ -280,10 +280,11 @@ static FfnPath ffn_path(int x_dtype, int w_dtype, int N, int d)
 }
 
 // Grouped FFN with 4-bit weights: H = SiLU(W_g x) * (W_u x) for routed and
-// shared rows in one launch, then both down projections in another.
+// shared rows in one launch, then both down projections in another. `status`
+// (NULL: left alone) is set to 0 by the first.
 static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E, int K, const int32_t *perm,
                               const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, void *h, void *y_perm,
-                              void *y_shared, cudaStream_t st)
+                              void *y_shared, int *status, cudaStream_t st)
 {
     W4Product a{};
     a.P = N * K;
@@ -293,6 +294,7 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
     a.y_dtype = KMOE_BF16;
     W4Product b = a;
     a.x = x;
+    a.status = status;
     a.x_rows = N;
     a.perm = perm;
     a.rows = I;
@@ -329,7 +331,7 @@ static kmoe_status run_ffn(const void *x, int x_dtype, int N, int d, int I, int 
     const int w_dtype = routed->dtype;
     if (w_dtype == KMOE_W4)
         return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm, offsets, routed->w4,
-                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, st);
+                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, nullptr, st);
     const ExpertPtrs r = ptrs(routed);
     ExpertPtrs sh{};
     if (shared) sh = ptrs(shared);
@@ -635,6 +637,9 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
     Carver c(ws);
     int *status = c.take<int>(kStatusInts);
     const FfnScratch f = take_ffn_scratch(c, N, d, K, I, routed->dtype);
+    if (routed->dtype == KMOE_W4)   // these kernels clear the status word themselves: no memset in front of them
+        return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm_token, offsets, routed->w4,
+                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, st);
     KMOE_TRY(clear_status(status, st, kFfnStatusBytes));
     return run_ffn(x, x_dtype, N, d, I, E, K, perm_token, offsets, routed, shared, f, y_perm, y_shared, status, st);
 }

@@ -44,6 +44,7 @@ using namespace sm100;
 constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Tiles = 4;                       // fragments of two tokens (three digits each) in a unit
+constexpr int kW4Tokens = 2 * kW4Tiles;
 constexpr int kW4Stages = 5;                      // steps of a warp's copies in flight, plus the one in use
 constexpr int kW4MaxGroups = 1025;
 constexpr int kW4Entries = 64;                    // token blocks of a phase
@@ -59,6 +60,7 @@ struct W4Args {
     int groups;         // experts, the shared one included
     int x_tiles;        // token pairs whose digits fit into shared memory
     int tokens;         // tokens of a unit: 2 * kW4Tiles, fewer where x_tiles is less
+    int q_jump, s_jump; // from the end of a row to the row of the next tile: code bytes, groups
 };
 
 // D += A B with unsigned codes and signed digits, 16 rows x 8 columns, 32 deep.
@@ -87,13 +89,12 @@ struct W4Stage {
 
 struct W4Smem {
     float head[kW4Warps][kW4Tiles][32];           // sums of a unit that an earlier warp began
-    W4Entry ent[kW4Entries];
-    int start[kW4MaxGroups + 1];                  // first row of every expert
-    int pre[kW4MaxGroups + 1];                    // token blocks of the experts before
     long long cost[kW4MaxGroups + 1];             // cost of the experts before
     long long scan_tmp[32];
-    long long begin, end, phase_end;              // units
-    int n_ent, used;
+    W4Entry ent[kW4Entries];
+    int row[kW4Entries * kW4Tokens];              // x row of every staged token (two per pair), -1: none
+    int pre[kW4MaxGroups + 1];                    // token blocks of the experts before
+    int start[kW4MaxGroups + 1], count[kW4MaxGroups + 1];     // rows of every expert
 };
 // behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][32], digit sums int [pair][block][128 / G][8], scales float [pair][block][2]
 __host__ __device__ constexpr size_t w4_x_bytes(int cols, int G) { return (size_t)(cols / kW4Block) * (1024 + 32 * (kW4Block / G) + 8); }
@@ -146,29 +147,27 @@ __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
     *cost = before >> 30;
 }
 
-// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x).
+// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x, n <= 1056), by a
+// whole warp in two looks.
 template <class T>
 __device__ __forceinline__ int last_not_above(const T *v, int n, T x)
 {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (v[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
+    const int lane = threadIdx.x & 31, chunk = (n + 31) >> 5;
+    const unsigned c = __ballot_sync(0xffffffffu, lane * chunk < n && v[lane * chunk] <= x);
+    const int base = (31 - __clz(c)) * chunk;
+    unsigned f = __ballot_sync(0xffffffffu, lane < chunk && base + lane < n && v[base + lane] <= x);
+    const int at = base + 31 - __clz(f);
+    return chunk > 32 && base + 32 < n && v[base + 32] <= x ? base + 32 : at;
 }
 
-// The unit at which a share that begins at cost c starts.
+// The unit at which a share that begins at cost c starts (by a whole warp).
 __device__ __forceinline__ long long unit_at(const W4Args &a, const W4Smem &sm, long long c)
 {
     if (c >= sm.cost[a.groups]) return (long long)sm.pre[a.groups] * a.tiles;
-    const int g = last_not_above(sm.cost, a.groups, c);
-    int start, count;
-    group_rows(a.p, g, &start, &count);
+    const int g = last_not_above(sm.cost, a.groups, c), count = sm.count[g];
     long long rem = c - sm.cost[g];
     const long long full = (long long)a.tiles * w4_cost(a.tokens);
-    const int tb = (int)min(rem / full, (long long)(count - 1) / a.tokens);
+    const int tb = (int)min(rem / full, (long long)((count - 1) / a.tokens));
     rem -= tb * full;
     return ((long long)sm.pre[g] + tb) * a.tiles + min(rem / w4_cost(min(a.tokens, count - tb * a.tokens)), (long long)a.tiles);
 }
@@ -201,6 +200,7 @@ constexpr int aux_word(int G) { return G == 32 ? 8 : 4; }
 template <bool kUp, int G, bool kZeros>
 struct Copier {
     int ent, tile, left;                          // left: blocks of the unit still to copy
+    int a_jump;                                   // aux: from the end of a row to the next tile's row
     const uint8_t *qa, *qb, *aux;                 // aux: lanes 0, 1 of a row scales of rows g, g + 8; 2, 3 zero points
 
     __device__ __forceinline__ void unit(const W4Args &a, const W4Smem &sm, int block)
@@ -213,6 +213,7 @@ struct Copier {
         const W4Ptrs *w = t & 1 ? r.wb : r.wa;
         aux = t < 2 ? reinterpret_cast<const uint8_t *>(w->s + at) : kZeros ? w->z + at : nullptr;
         left = a.p.cols / kW4Block - block;
+        a_jump = a.s_jump * (t < 2 ? 2 : 1);
     }
     // One step into `st`, which ends the unit's walk or goes on in it.
     __device__ __forceinline__ void step(const W4Args &a, const W4Smem &sm, W4Stage<G> &st, bool more)
@@ -233,11 +234,18 @@ struct Copier {
         qb += 64;
         aux += t < 2 ? 2 * GB : GB;
         if (--left == 0 && more) {
-            if (++tile == a.tiles) {
-                tile = 0;
-                ++ent;
+            if (++tile < a.tiles - 1) {           // whole tiles of one matrix lie at equal distances
+                qa += a.q_jump;
+                qb += a.q_jump;
+                aux += a_jump;
+                left = a.p.cols / kW4Block;
+            } else {
+                if (tile == a.tiles) {
+                    tile = 0;
+                    ++ent;
+                }
+                unit(a, sm, 0);
             }
-            unit(a, sm, 0);
         }
     }
 };
@@ -370,155 +378,173 @@ __device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e,
     }
 }
 
+// Two 4-byte operand words per digit from eight fixed-point values: bytes of
+// columns 0 4 1 5 and 2 6 3 7. v + 0x808080 has the balanced digits + 128 as its
+// bytes, and flipping their top bits makes them signed bytes.
+__device__ __forceinline__ void split_digits(const int (&v)[8], uint32_t (&w)[3][2])
+{
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = ((uint32_t)v[i] + 0x808080u) ^ 0x808080u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {                 // columns 2h, 2h + 4, 2h + 1, 2h + 5
+        const uint32_t lo = __byte_perm(b[2 * h], b[2 * h + 4], 0x5140), lo1 = __byte_perm(b[2 * h + 1], b[2 * h + 5], 0x5140);
+        const uint32_t hi = __byte_perm(b[2 * h], b[2 * h + 4], 0x0062), hi1 = __byte_perm(b[2 * h + 1], b[2 * h + 5], 0x0062);
+        w[2][h] = __byte_perm(lo, lo1, 0x5410);
+        w[1][h] = __byte_perm(lo, lo1, 0x7632);
+        w[0][h] = __byte_perm(hi, hi1, 0x5410);
+    }
+}
+
 // Digits of the phase's tokens: 16 lanes take 128 columns of one token, eight
 // each. Pairs without a second token get zeros in its place.
 template <int G, bool kZeros, class XT>
-__device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, uint4 *dig, int *sums, float *sx)
+__device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, int pairs, uint4 *dig, int *sums, float *sx)
 {
     constexpr int GB = kW4Block / G, GL = G / 8;  // groups of a block; lanes of a group
+    constexpr int kAhead = 4, kItems = kW4Threads / 16;
     const W4Product &p = a.p;
-    const int blocks = p.cols / kW4Block, items = sm.used * 2 * blocks;
+    const int blocks = p.cols / kW4Block, items = pairs * 2 * blocks;
     const int l16 = threadIdx.x & 15, jj = l16 >> 2, t = l16 & 3;
-    for (int it0 = 0; it0 < items; it0 += kW4Threads / 16) {
-        const int it = it0 + (threadIdx.x >> 4);
-        const int slot = it / blocks, b = it - slot * blocks, pair = slot >> 1, tok = slot & 1;
-        float v[8];
+    for (int it0 = threadIdx.x >> 4; it0 - (int)(threadIdx.x >> 4) < items; it0 += kItems * kAhead) {
+        float v[kAhead][8];                       // all loads first: their latencies overlap
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        if (it < items) {
-            int e = 0;                            // the token block of this pair
-            while (e + 1 < sm.n_ent && sm.ent[e + 1].tile0 <= pair) ++e;
-            const W4Entry en = sm.ent[e];
-            const int i = (pair - en.tile0) * 2 + tok;
-            int xi = -1;
-            if (i < en.n) {
-                xi = en.row0 + i;
-                if (!p.x_by_row) xi = en.grp >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
-                if ((unsigned)xi >= (unsigned)p.x_rows) xi = -1;      // a token that is not there: zeros
+        for (int k = 0; k < kAhead; ++k) {
+            const int it = it0 + k * kItems, slot = it / blocks, b = it - slot * blocks;
+            const int xi = it < items ? sm.row[slot] : -1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+            if (xi >= 0) load8(static_cast<const XT *>(p.x) + (size_t)xi * p.cols + b * kW4Block + l16 * 8, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int it = it0 + k * kItems, slot = it / blocks, b = it - slot * blocks, tok = slot & 1;
+            if (it - (int)(threadIdx.x >> 4) % 2 >= items) break;     // both halves of the warp are past the end
+            uint32_t top = 0;                     // bits of the largest |x|; NaN and infinity are the largest
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // exponent field of 2^E; below 2^-105 the digits stay at that scale (off by less than 2^-127)
+            const uint32_t ex = max(top >> 23, 22u);
+            const float mul = __uint_as_float((275u - ex) << 23);     // 2^(21 - E)
+            int q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(v[k][i] * mul);
+            uint32_t w[3][2];
+            split_digits(q, w);
+            int sum[3];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) sum[j] = __dp4a((int)w[j][0], 0x01010101, __dp4a((int)w[j][1], 0x01010101, 0));
+#pragma unroll
+            for (int o = 1; o < GL; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < 3; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+            if (it >= items) continue;
+            const int at = (slot >> 1) * blocks + b;
+            uint2 *out = reinterpret_cast<uint2 *>(dig + (at * 2 + (jj >> 1)) * 32) + (jj & 1);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) out[((tok * 4 + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
+            out[((tok * 4 + 3) * 4 + t) * 2] = make_uint2(0, 0);
+            if (l16 % GL == 0) {
+                int *c = sums + (at * GB + l16 / GL) * 8 + tok * 4;
+                const int f = kZeros ? 1 : -8;
+                *reinterpret_cast<int4 *>(c) = make_int4(f * sum[0], f * sum[1], f * sum[2], 0);
             }
-            if (xi >= 0) load8(static_cast<const XT *>(p.x) + (size_t)xi * p.cols + b * kW4Block + l16 * 8, v);
+            // a block with an infinity or a NaN makes this token's results NaN, and no other's
+            if (l16 == 0) sx[at * 2 + tok] = (top >> 23) == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((ex - 21u) << 23);
         }
-        uint32_t top = 0;                         // bits of the largest |x|; NaN and infinity are the largest
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // exponent field of 2^E; below 2^-105 the digits stay at that scale (off by less than 2^-127)
-        const uint32_t ex = max(top >> 23, 22u);
-        const float mul = __uint_as_float((275u - ex) << 23);         // 2^(21 - E)
-        uint32_t w[3][2];                         // this lane's operand bytes: columns 0 4 1 5, 2 6 3 7
-        int sum[3] = {0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) w[k][0] = w[k][1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            constexpr int kWord[8] = {0, 0, 1, 1, 0, 0, 1, 1}, kByte[8] = {0, 2, 0, 2, 1, 3, 1, 3};
-            int q = __float2int_rn(v[i] * mul);
-#pragma unroll
-            for (int k = 2; k >= 0; --k) {
-                const int d = (int)(int8_t)(q & 255);
-                w[k][kWord[i]] |= (uint32_t)(d & 255) << (8 * kByte[i]);
-                sum[k] += d;
-                q = (q - d) >> 8;
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < GL; o <<= 1)
-#pragma unroll
-            for (int k = 0; k < 3; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-        if (it >= items) continue;
-        const size_t at = (size_t)pair * blocks + b;
-        uint2 *out = reinterpret_cast<uint2 *>(dig + (at * 2 + (jj >> 1)) * 32) + (jj & 1);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) out[((tok * 4 + k) * 4 + t) * 2] = make_uint2(w[k][0], w[k][1]);
-        out[((tok * 4 + 3) * 4 + t) * 2] = make_uint2(0, 0);
-        if (l16 % GL == 0) {
-            int *c = sums + (at * GB + l16 / GL) * 8 + tok * 4;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) c[k] = kZeros ? sum[k] : -8 * sum[k];
-            c[3] = 0;
-        }
-        // a block with an infinity or a NaN makes this token's results NaN, and no other's
-        if (l16 == 0) sx[at * 2 + tok] = (top >> 23) == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((ex - 21u) << 23);
     }
 }
 
 // What a warp carries from unit to unit of a phase.
 struct WarpRun {
     int s, s1, issued, stage;                     // step, end, steps copied, ring stage of this step
+    int block;                                    // first block of the unit at hand
     bool open;                                    // the last unit goes on in later warps; v holds its sums so far
-    int ent, tile;                                // that unit
+    int ent, tile;                                // the unit at hand
     float v[kW4Tiles];
 };
 
-// The steps of one unit that are this warp's (from block `block` on), for NT token pairs.
+// The units of one token block that are this warp's, for its NT token pairs.
 template <bool kUp, int G, bool kZeros, class YT, int NT>
-__device__ __forceinline__ void run_unit(const W4Args &a, W4Smem &sm, W4Stage<G> *ring, const uint4 *dig, const int *sums, const float *sx,
-                                         int block, WarpRun &r, Copier<kUp, G, kZeros> &cp)
+__device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G> *ring, const uint4 *dig, const int *sums,
+                                          const float *sx, WarpRun &r, Copier<kUp, G, kZeros> &cp)
 {
     constexpr int GB = kW4Block / G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
     const int blocks = a.p.cols / kW4Block;
     const W4Entry e = sm.ent[r.ent];
-    uint32_t la, lb, lza = 0, lzb = 0;            // low address bits of this unit's scales and zero points
-    {
-        const UnitRows<kUp, G> w(a, e.grp, r.tile);
-        const uint32_t gpr = a.p.cols / G, b = block * GB;
-        const uint32_t ia = (uint32_t)w.ra * gpr + b, ib = (uint32_t)w.rb * gpr + b;
-        la = 2 * ia;                              // the arrays themselves are 16-byte aligned
-        lb = 2 * ib;
-        lza = ia;
-        lzb = ib;
-    }
-    const int at = e.tile0 * blocks + block;
-    const uint4 *d = dig + at * 64 + lane;
-    const int2 *c = reinterpret_cast<const int2 *>(sums) + at * GB * 4 + t;
-    const float *x = sx + at * 2 + (t >> 1);
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    const int n_steps = min(blocks - block, r.s1 - r.s);
-    for (int i = 0; i < n_steps; ++i) {
-        W4Stage<G> &st = ring[r.stage];
-        cp_async_wait<kW4Stages - 2>();
-        __syncwarp();                             // every lane's copies of this step; reads of the last one are done
-        const uint4 qa = st.q[0][lane], qb = st.q[1][lane];
-        float sa[GB], sb[GB];
-        int za[GB], zb[GB];
-        read_aux<G, kZeros>(st.aux[lane >> 2], la, lb, lza, lzb, sa, sb, za, zb);
-        // the stage used one step ago takes the copy kW4Stages - 1 steps ahead
-        const int prev = r.stage == 0 ? kW4Stages - 1 : r.stage - 1;
-        if (r.issued < r.s1) {
-            ++r.issued;
-            cp.step(a, sm, ring[prev], r.issued < r.s1);
+    const int at = e.tile0 * blocks;
+    const uint4 *d0 = dig + at * 64 + lane;
+    const int2 *c0 = reinterpret_cast<const int2 *>(sums) + at * GB * 4 + t;
+    const float *x0 = sx + at * 2 + (t >> 1);
+    uint32_t ia = 0, ib = 0;                      // low bits of the group's index, which tell the place in its copied word
+    bool fresh = true;
+    while (true) {
+        if (fresh || r.tile == a.tiles - 1) {     // the last tile of a matrix may repeat rows
+            const UnitRows<kUp, G> w(a, e.grp, r.tile);
+            const uint32_t gpr = a.p.cols / G;
+            ia = (uint32_t)w.ra * gpr + r.block * GB;
+            ib = (uint32_t)w.rb * gpr + r.block * GB;
+            fresh = false;
         }
-        cp_async_commit();                        // an empty group past the end keeps the count
-        r.stage = r.stage + 1 == kW4Stages ? 0 : r.stage + 1;
-        w4_step<G, kZeros, NT>(qa, qb, sa, sb, za, zb, d, c, x, blocks, acc);
-        d += 64;
-        c += GB * 4;
-        x += 2;
-        la += 2 * GB;
-        lb += 2 * GB;
-        lza += GB;
-        lzb += GB;
-    }
-    r.s += n_steps;
-    const bool whole = block == 0, ends = block + n_steps == blocks;
-    float v[NT];
+        const uint4 *d = d0 + r.block * 64;
+        const int2 *c = c0 + r.block * GB * 4;
+        const float *x = x0 + r.block * 2;
+        float acc[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) v[n] = join_digits(acc[n]);
-    if (whole && ends) {
-        store_unit<kUp, YT, NT>(a.p, e, r.tile, v);
-    } else if (!whole) {                          // begun by an earlier warp
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sm.head[warp][n][lane] = v[n];
-    } else {
-        r.open = true;
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        const int n_steps = min(blocks - r.block, r.s1 - r.s);
+        for (int i = 0; i < n_steps; ++i) {
+            W4Stage<G> &st = ring[r.stage];
+            cp_async_wait<kW4Stages - 2>();
+            __syncwarp();                         // every lane's copies of this step; reads of the last one are done
+            const uint4 qa = st.q[0][lane], qb = st.q[1][lane];
+            float sa[GB], sb[GB];
+            int za[GB], zb[GB];
+            read_aux<G, kZeros>(st.aux[lane >> 2], 2 * ia, 2 * ib, ia, ib, sa, sb, za, zb);
+            // the stage used one step ago takes the copy kW4Stages - 1 steps ahead
+            const int prev = r.stage == 0 ? kW4Stages - 1 : r.stage - 1;
+            if (r.issued < r.s1) {
+                ++r.issued;
+                cp.step(a, sm, ring[prev], r.issued < r.s1);
+            }
+            cp_async_commit();                    // an empty group past the end keeps the count
+            r.stage = r.stage + 1 == kW4Stages ? 0 : r.stage + 1;
+            w4_step<G, kZeros, NT>(qa, qb, sa, sb, za, zb, d, c, x, blocks, acc);
+            d += 64;
+            c += GB * 4;
+            x += 2;
+            ia += GB;
+            ib += GB;
+        }
+        r.s += n_steps;
+        const bool whole = r.block == 0, ends = r.block + n_steps == blocks;
+        r.block = 0;
+        float v[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) r.v[n] = v[n];
+        for (int n = 0; n < NT; ++n) v[n] = join_digits(acc[n]);
+        if (whole && ends) {
+            store_unit<kUp, YT, NT>(a.p, e, r.tile, v);
+        } else if (!whole) {                      // begun by an earlier warp
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sm.head[warp][n][lane] = v[n];
+        } else {
+            r.open = true;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) r.v[n] = v[n];
+        }
+        if (r.s >= r.s1) return;
+        ia += a.s_jump;
+        ib += a.s_jump;
+        if (++r.tile == a.tiles) {
+            r.tile = 0;
+            ++r.ent;
+            return;
+        }
     }
 }
 
@@ -538,79 +564,84 @@ w4_kernel(const __grid_constant__ W4Args a)
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.p.status && blockIdx.x == 0 && threadIdx.x == 0) *a.p.status = 0;
 
-    // token blocks and cost of every expert, as exclusive prefixes
-    const int per = (a.groups + kW4Threads - 1) / kW4Threads;
-    auto blocks_of = [&](int g, int *cost) {
-        int start, count;
-        group_rows(p, g, &start, &count);
-        const int full = count / a.tokens, rest = count - full * a.tokens;
-        *cost = full * w4_cost(a.tokens) + (rest ? w4_cost(rest) : 0);
-        return full + (rest > 0);
-    };
-    int run = 0;
-    long long run_cost = 0;
-    for (int i = 0; i < per; ++i) {
-        const int g = threadIdx.x * per + i;
-        int cost;
-        if (g < a.groups) {
-            run += blocks_of(g, &cost);
-            run_cost += cost;
-        }
-    }
-    scan2(&run, &run_cost, sm);
-    for (int i = 0; i < per; ++i) {
-        const int g = threadIdx.x * per + i;
-        if (g >= a.groups) break;
-        int cost;
-        sm.pre[g] = run;
-        sm.cost[g] = run_cost * a.tiles;
-        run += blocks_of(g, &cost);
-        run_cost += cost;
-        if (g == a.groups - 1) {
-            sm.pre[a.groups] = run;
-            sm.cost[a.groups] = run_cost * a.tiles;
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {                        // this CTA's share of the cost
-        const long long c = sm.cost[a.groups];
-        const int b = blockIdx.x + threadIdx.x;
-        // c * b / gridDim.x in parts that stay below 2^63
-        const long long at = c / gridDim.x * b + c % gridDim.x * b / gridDim.x;
-        (threadIdx.x ? sm.end : sm.begin) = unit_at(a, sm, at);
-    }
-    __syncthreads();
-
-    const long long u1 = sm.end;
-    for (long long u0 = sm.begin; u0 < u1;) {
-        if (threadIdx.x == 0) {                   // the phase's token blocks
-            int tb = (int)(u0 / a.tiles), g = last_not_above(sm.pre, a.groups, tb), used = 0, k = 0;
-            for (; k < kW4Entries && (long long)tb * a.tiles < u1; ++k, ++tb) {
-                while (sm.pre[g + 1] <= tb) ++g;
+    // rows, token blocks and cost of every expert, the latter as exclusive prefixes
+    {
+        const int per = (a.groups + kW4Threads - 1) / kW4Threads;     // 1 to 3
+        int n_blocks[3], cost[3], run = 0;
+        long long run_cost = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int g = threadIdx.x * per + i;
+            n_blocks[i] = cost[i] = 0;
+            if (i < per && g < a.groups) {
                 int start, count;
                 group_rows(p, g, &start, &count);
-                const int first = (tb - sm.pre[g]) * a.tokens, n = min(a.tokens, count - first);
-                if (k && used + (n + 1) / 2 > a.x_tiles) break;
-                sm.ent[k] = {g, start + first, n, used};
-                used += (n + 1) / 2;
+                sm.start[g] = start;
+                sm.count[g] = count;
+                const int full = count / a.tokens, rest = count - full * a.tokens;
+                n_blocks[i] = full + (rest > 0);
+                cost[i] = full * w4_cost(a.tokens) + (rest ? w4_cost(rest) : 0);
             }
-            sm.n_ent = k;
-            sm.used = used;
-            sm.phase_end = min((long long)tb * a.tiles, u1);
+            run += n_blocks[i];
+            run_cost += cost[i];
+        }
+        if (a.groups > 1) scan2(&run, &run_cost, sm);
+        else run = 0, run_cost = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int g = threadIdx.x * per + i;
+            if (i >= per || g >= a.groups) break;
+            sm.pre[g] = run;
+            sm.cost[g] = run_cost * a.tiles;
+            run += n_blocks[i];
+            run_cost += cost[i];
+            if (g == a.groups - 1) {
+                sm.pre[a.groups] = run;
+                sm.cost[a.groups] = run_cost * a.tiles;
+            }
+        }
+    }
+    __syncthreads();
+    // this CTA's share of the cost c: from c b / gridDim.x on, in parts that stay below 2^63
+    const long long c = sm.cost[a.groups];
+    auto at_share = [&](int b) { return unit_at(a, sm, c / gridDim.x * b + c % gridDim.x * b / gridDim.x); };
+    const long long u1 = at_share(blockIdx.x + 1);
+    for (long long u0 = at_share(blockIdx.x); u0 < u1;) {
+        // the phase's token blocks: every warp works them out, each writes its share
+        int n_ent = 0, used = 0;
+        long long phase_end;
+        {
+            int tb = (int)(u0 / a.tiles), g = last_not_above(sm.pre, a.groups, tb);
+            for (; n_ent < kW4Entries && (long long)tb * a.tiles < u1; ++n_ent, ++tb) {
+                while (sm.pre[g + 1] <= tb) ++g;
+                const int first = (tb - sm.pre[g]) * a.tokens, n = min(a.tokens, sm.count[g] - first);
+                const int pairs = (n + 1) / 2, row0 = sm.start[g] + first;
+                if (n_ent && used + pairs > a.x_tiles) break;
+                if (n_ent % kW4Warps == warp) {
+                    if (lane == 0) sm.ent[n_ent] = {g, row0, n, used};
+                    if (lane < 2 * pairs) {       // x rows; a token that is not there stands for zeros
+                        int xi = row0 + lane;
+                        if (lane < n && !p.x_by_row) xi = g >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
+                        sm.row[used * 2 + lane] = lane < n && (unsigned)xi < (unsigned)p.x_rows ? xi : -1;
+                    }
+                }
+                used += pairs;
+            }
+            phase_end = min((long long)tb * a.tiles, u1);
         }
         __syncthreads();
-        const int first_tile = (int)(u0 % a.tiles), steps = (int)(sm.phase_end - u0) * blocks;
+        const int first_tile = (int)(u0 % a.tiles), steps = (int)(phase_end - u0) * blocks;
         const int s0 = (int)((long long)steps * warp / kW4Warps);
-        WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, false, 0, 0, {}};
+        WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, s0 % blocks, false, 0, 0, {}};
         Copier<kUp, G, kZeros> cp{};
-        int block = s0 % blocks;
         if (r.s < r.s1) {
             r.ent = (first_tile + s0 / blocks) / a.tiles;
             r.tile = first_tile + s0 / blocks - r.ent * a.tiles;
             cp.ent = r.ent;
             cp.tile = r.tile;
-            cp.unit(a, sm, block);
+            cp.unit(a, sm, r.block);
         }
         for (int i = 0; i < kW4Stages - 1; ++i) {
             if (r.issued < r.s1) {
@@ -619,21 +650,14 @@ w4_kernel(const __grid_constant__ W4Args a)
             }
             cp_async_commit();
         }
-        stage_digits<G, kZeros, XT>(a, sm, dig, sums, sx);
+        stage_digits<G, kZeros, XT>(a, sm, used, dig, sums, sx);
         __syncthreads();
         while (r.s < r.s1) {
             const int nt = (sm.ent[r.ent].n + 1) / 2;
-            if (nt == 1) run_unit<kUp, G, kZeros, YT, 1>(a, sm, ring, dig, sums, sx, block, r, cp);
-            else if (nt == 2) run_unit<kUp, G, kZeros, YT, 2>(a, sm, ring, dig, sums, sx, block, r, cp);
-            else if (nt == 3) run_unit<kUp, G, kZeros, YT, 3>(a, sm, ring, dig, sums, sx, block, r, cp);
-            else run_unit<kUp, G, kZeros, YT, 4>(a, sm, ring, dig, sums, sx, block, r, cp);
-            if (r.s < r.s1) {
-                block = 0;
-                if (++r.tile == a.tiles) {
-                    r.tile = 0;
-                    ++r.ent;
-                }
-            }
+            if (nt == 1) run_entry<kUp, G, kZeros, YT, 1>(a, sm, ring, dig, sums, sx, r, cp);
+            else if (nt == 2) run_entry<kUp, G, kZeros, YT, 2>(a, sm, ring, dig, sums, sx, r, cp);
+            else if (nt == 3) run_entry<kUp, G, kZeros, YT, 3>(a, sm, ring, dig, sums, sx, r, cp);
+            else run_entry<kUp, G, kZeros, YT, 4>(a, sm, ring, dig, sums, sx, r, cp);
         }
         __syncthreads();
         if (r.open) {                             // the warp that began a shared unit adds it up
@@ -649,8 +673,8 @@ w4_kernel(const __grid_constant__ W4Args a)
             }
             store_unit<kUp, YT, kW4Tiles>(p, e, r.tile, r.v);
         }
-        u0 = sm.phase_end;
-        __syncthreads();                          // tables and digits are free for the next phase
+        u0 = phase_end;
+        if (u0 < u1) __syncthreads();             // tables and digits are free for the next phase
     }
 }
 
@@ -670,6 +694,9 @@ static kmoe_status run_w4(W4Args a, cudaStream_t st)
     a.x_tiles = (int)std::min<size_t>((kW4SmemMax - kW4FixedSmem<G>) / x_bytes, kW4Entries * kW4Tiles);
     if (a.x_tiles < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
     a.tokens = 2 * std::min(a.x_tiles, kW4Tiles);
+    constexpr int kTileRows = kUp ? 8 : 16;
+    a.q_jump = (kTileRows - 1) * (a.p.cols / 2);
+    a.s_jump = (kTileRows - 1) * (a.p.cols / G);
     // no more CTAs than units there can be: an expert with rows has at least one token block
     const long long most = ((long long)std::min(a.p.E, a.p.P) + (a.p.P + a.p.n_shared) / a.tokens + 1) * a.tiles;
     const int grid = (int)std::min<long long>(sm_count_w4(), most);
@@ -692,7 +719,7 @@ static kmoe_status pick_w4(const W4Args &a, cudaStream_t st)
 
 kmoe_status launch_w4(const W4Product &p, cudaStream_t st)
 {
-    W4Args a{p, 0, p.E + (p.n_shared > 0 ? 1 : 0), 0, 0};
+    W4Args a{p, 0, p.E + (p.n_shared > 0 ? 1 : 0), 0, 0, 0, 0};
     if (a.groups > kW4MaxGroups) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: too many experts");
     const bool up = p.up.q != nullptr;
     a.tiles = up ? (p.rows + 7) / 8 : (p.rows + 15) / 16;

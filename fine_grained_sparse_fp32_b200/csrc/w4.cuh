@@ -49,6 +49,7 @@ struct W4Product {
     bool x_f32;                          // x (H) in FP32
     void *y, *y_shared;                  // y [P (+ n_shared for SwiGLU), rows]
     int y_dtype;
+    int *status;                         // set to 0 (NULL: none)
 };
 kmoe_status launch_w4(const W4Product &a, cudaStream_t st);
 
