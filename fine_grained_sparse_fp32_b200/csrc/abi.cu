@@ -740,7 +740,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     if (N > (1 << 30) || P > (1 << 30)) return fail(KMOE_ERR_UNSUPPORTED, "N=%d, P=%d: at most 2^30 rows", N, P);
     if (rows < 1 || rows > 65536) return fail(KMOE_ERR_UNSUPPORTED, "rows=%d: supported 1..65536", rows);
     KMOE_TRY(check_w4_cols(cols));
-    if (cols > 10240) return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: supported up to 10240", cols);
+    if (cols > 8192) return fail(KMOE_ERR_UNSUPPORTED, "cols=%d: supported up to 8192", cols);
     if (E < 1 || E > 1024) return fail(KMOE_ERR_UNSUPPORTED, "E=%d: supported 1..1024", E);
     if (!offsets && E != 1) return fail(KMOE_ERR_INVALID_ARG, "E=%d matrices need offsets", E);
     if (!perm_token && P > N) return fail(KMOE_ERR_INVALID_ARG, "P=%d rows of y without perm_token, x has N=%d", P, N);

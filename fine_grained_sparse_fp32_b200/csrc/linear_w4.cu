@@ -14,25 +14,26 @@
 // with t in -128..127. r is 0 for every BF16 x within 2^14 of the block's
 // largest value, so sums are at least as exact as with FP32 products. The
 // digits of a token are three columns of the fragment, and the integer sums of
-// a group are exact; zero points come off as -z * (sum of the digits), the
-// start value of the sum. Group scale and 2^(E - 21) multiply the sums in FP32.
+// a group are exact, as is 256 t0 + t1 of them (below 2^27). Zero points come
+// off as -z times the sum of the digits. Group scale and 2^(E - 21) multiply
+// the sums in FP32.
 //
 // With `up` weights, rows 0-7 of a fragment are eight gate features and rows
 // 8-15 the same eight up features, and SiLU(gate) * up is written.
 //
-// A unit is one fragment row tile (16 rows; 8 features) of one expert for up
-// to 8 tokens. The units of all experts that have rows are numbered through
-// and every CTA (one per SM) takes a contiguous share of them, in phases: as
-// many units as the digits of their tokens fit into shared memory (nearly
-// always all). A unit's columns are steps of 128, and a phase's steps are
-// shared out evenly and contiguously among the warps. So a warp streams one
-// long run of weights with no barrier in it: each lane copies its 16 bytes of
-// both its rows (and lanes 0 to 3 of a row its scales and zero points)
-// kW4Stages - 1 steps ahead into the warp's shared memory (cp.async), which
-// keeps about 64 KB of an SM's weight traffic in flight without registers.
-// Units that two or more warps share are added in warp order at the end, so
-// results do not depend on timing. A unit of more tokens costs more
-// instructions for the same weights; the CTAs' shares are cut by that cost.
+// A unit is two fragments (32 rows; 16 features) of one expert for up to 8
+// tokens: the digits read for one fragment serve both. The units of all experts
+// that have rows are numbered through and every CTA (one per SM) takes a
+// contiguous share of them, in phases: as many units as the digits of their
+// tokens fit into shared memory (nearly always all). A unit of more tokens
+// costs more instructions for the same weights; shares are cut by that cost. A
+// unit's columns are steps of 128, and a phase's steps are shared out evenly
+// and contiguously among the warps. So a warp streams one long run of weights
+// with no barrier in it: each lane copies its 16 bytes of four rows, and its
+// share of their scales and zero points, kW4Stages - 1 steps ahead into the
+// warp's shared memory (cp.async), which keeps 64 KB of an SM's weight traffic
+// in flight without registers. Units that two or more warps share are added in
+// warp order at the end, so results do not depend on timing.
 #include "w4.cuh"
 #include "sm100.cuh"
 
@@ -43,24 +44,34 @@ using namespace sm100;
 
 constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;
-constexpr int kW4Tiles = 4;                       // fragments of two tokens (three digits each) in a unit
-constexpr int kW4Tokens = 2 * kW4Tiles;
-constexpr int kW4Stages = 5;                      // steps of a warp's copies in flight, plus the one in use
+constexpr int kW4Frags = 2;                       // row fragments of a unit
+constexpr int kW4Pairs = 4;                       // column fragments of two tokens (three digits each) of a unit
+constexpr int kW4Tokens = 2 * kW4Pairs;
+constexpr int kW4Stages = 3;                      // steps of a warp's copies in flight, plus the one in use
 constexpr int kW4MaxGroups = 1025;
-constexpr int kW4Entries = 64;                    // token blocks of a phase
+constexpr int kW4Entries = 32;                    // token blocks of a phase
 constexpr int kW4SmemMax = 226 * 1024;
 
-// Instructions of a step by its token pairs, in units of about 25: what the
-// CTAs' shares are cut by.
-__host__ __device__ constexpr int w4_cost(int tokens) { return 3 + (tokens + 1) / 2; }
+// Instructions of a step by its tokens, in units of about 55: what the CTAs'
+// shares are cut by.
+__host__ __device__ constexpr int w4_cost(int tokens) { return 2 + (tokens + 1) / 2; }
+
+// Division by a number that the host knows: the high word of n * ceil(2^64 / d),
+// exact for n < 2^32 and 1 < d < 2^32.
+struct DivideBy {
+    unsigned long long m;     // 0 stands for d = 1
+    static DivideBy make(uint32_t d) { return {d > 1 ? ~0ull / d + 1 : 0}; }
+    __device__ __forceinline__ int operator()(int n) const { return m ? (int)__umul64hi((unsigned long long)(uint32_t)n, m) : n; }
+};
 
 struct W4Args {
     W4Product p;
-    int tiles;          // row tiles of one expert
-    int groups;         // experts, the shared one included
-    int x_tiles;        // token pairs whose digits fit into shared memory
-    int tokens;         // tokens of a unit: 2 * kW4Tiles, fewer where x_tiles is less
-    int q_jump, s_jump; // from the end of a row to the row of the next tile: code bytes, groups
+    int tiles;              // units of one expert and token block
+    int groups;             // experts, the shared one included
+    int x_pairs;            // token pairs whose digits fit into shared memory
+    int tokens;             // tokens of a unit: 2 * kW4Pairs, fewer where x_pairs is less
+    int q_jump, s_jump;     // from the end of a row to the row of the next tile: code bytes, groups
+    DivideBy by_blocks, by_tiles, by_tokens, by_grid;
 };
 
 // D += A B with unsigned codes and signed digits, 16 rows x 8 columns, 32 deep.
@@ -78,26 +89,30 @@ struct W4Entry {
     int grp, row0, n, tile0;                      // expert, first row, rows, first staged token pair
 };
 
-// One step's copies of a warp: code bytes by lane, then the words that hold the
-// scales and zero points of the row pair g: {scale g, scale g + 8, zero g,
-// zero g + 8}, of 4 bytes each (8 with groups of 32).
+// One step's copies of a warp: code bytes of rows g, g + 8 (gate, up) of both
+// fragments by lane, then for each g the words that hold the four rows' scales
+// (4 bytes; 8 with groups of 32) and the words that hold their zero points.
 template <int G>
 struct W4Stage {
-    uint4 q[2][32];
-    uint4 aux[8][G == 32 ? 2 : 1];
+    uint4 q[2 * kW4Frags][32];
+    uint4 s[8][G == 32 ? 2 : 1];
+    uint4 z[8];
 };
 
 struct W4Smem {
-    float head[kW4Warps][kW4Tiles][32];           // sums of a unit that an earlier warp began
-    long long cost[kW4MaxGroups + 1];             // cost of the experts before
+    float head[kW4Warps][kW4Pairs][kW4Frags][32]; // sums of a unit that an earlier warp began
     long long scan_tmp[32];
     W4Entry ent[kW4Entries];
+    int share[4];                                 // this CTA's first unit and the one behind its last: token block, tile
+    int n_ent, used;                              // the phase's token blocks, their token pairs
     int row[kW4Entries * kW4Tokens];              // x row of every staged token (two per pair), -1: none
     int pre[kW4MaxGroups + 1];                    // token blocks of the experts before
+    int cost[kW4MaxGroups + 1];                   // and their cost
     int start[kW4MaxGroups + 1], count[kW4MaxGroups + 1];     // rows of every expert
 };
-// behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][32], digit sums int [pair][block][128 / G][8], scales float [pair][block][2]
-__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G) { return (size_t)(cols / kW4Block) * (1024 + 32 * (kW4Block / G) + 8); }
+// behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][32], digit sums int [pair][block][128 / G][4],
+// scales of the digits float [pair][block][2]
+__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G) { return (size_t)(cols / kW4Block) * (1024 + 16 * (kW4Block / G) + 8); }
 constexpr size_t kW4Tables = (sizeof(W4Smem) + 127) / 128 * 128;
 template <int G>
 constexpr size_t kW4FixedSmem = kW4Tables + sizeof(W4Stage<G>) * kW4Warps * kW4Stages;
@@ -147,97 +162,141 @@ __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
     *cost = before >> 30;
 }
 
-// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x, n <= 1056), by a
-// whole warp in two looks.
-template <class T>
-__device__ __forceinline__ int last_not_above(const T *v, int n, T x)
+// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x).
+__device__ __forceinline__ int last_not_above(const int *v, int n, int x)
 {
-    const int lane = threadIdx.x & 31, chunk = (n + 31) >> 5;
-    const unsigned c = __ballot_sync(0xffffffffu, lane * chunk < n && v[lane * chunk] <= x);
-    const int base = (31 - __clz(c)) * chunk;
-    unsigned f = __ballot_sync(0xffffffffu, lane < chunk && base + lane < n && v[base + lane] <= x);
-    const int at = base + 31 - __clz(f);
-    return chunk > 32 && base + 32 < n && v[base + 32] <= x ? base + 32 : at;
+    int lo = 0;
+    for (int w = 1 << (31 - __clz(n)); w > 0; w >>= 1)
+        if (lo + w < n && v[lo + w] <= x) lo += w;
+    return lo;
 }
 
-// The unit at which a share that begins at cost c starts (by a whole warp).
-__device__ __forceinline__ long long unit_at(const W4Args &a, const W4Smem &sm, long long c)
+// The unit (token block, numbered through all experts, and tile) at which share
+// b of gridDim.x begins: the place b / gridDim.x of the total cost, in whole
+// units of cost and a rest over gridDim.x, so that everything fits into 32 bits.
+__device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Smem &sm, int b)
 {
-    if (c >= sm.cost[a.groups]) return (long long)sm.pre[a.groups] * a.tiles;
-    const int g = last_not_above(sm.cost, a.groups, c), count = sm.count[g];
-    long long rem = c - sm.cost[g];
-    const long long full = (long long)a.tiles * w4_cost(a.tokens);
-    const int tb = (int)min(rem / full, (long long)((count - 1) / a.tokens));
-    rem -= tb * full;
-    return ((long long)sm.pre[g] + tb) * a.tiles + min(rem / w4_cost(min(a.tokens, count - tb * a.tokens)), (long long)a.tiles);
+    const int c = sm.cost[a.groups], grid = gridDim.x;
+    if (b >= grid) return make_int2(sm.pre[a.groups], 0);
+    const int q = a.by_grid(c), r = (c - q * grid) * b, rq = a.by_grid(r), whole = q * b + rq, rest = r - rq * grid;
+    const int g = last_not_above(sm.cost, a.groups, whole), count = sm.count[g];
+    const int full = w4_cost(a.tokens), tb = min((whole - sm.cost[g]) / full, a.by_tokens(count - 1));
+    const int left = whole - sm.cost[g] - tb * full, w = w4_cost(min(a.tokens, count - tb * a.tokens));
+    // left < 8, rest < grid, tiles <= 4096
+    const int tile = (int)((uint32_t)(left * grid + rest) * (uint32_t)a.tiles / (uint32_t)(w * grid));
+    return tile < a.tiles ? make_int2(sm.pre[g] + tb, tile) : make_int2(sm.pre[g] + tb + 1, 0);
 }
 
-// This lane's weight rows of a unit: rows g and g + 8 of its fragment.
-template <bool kUp, int G>
-struct UnitRows {
-    const W4Ptrs *wa, *wb;
-    size_t ra, rb;
-
-    __device__ __forceinline__ UnitRows(const W4Args &a, int grp, int tile)
-    {
-        const W4Product &p = a.p;
-        const int g8 = (threadIdx.x & 31) >> 2;
-        const bool shared = grp >= p.E;
-        wa = shared ? &p.w_shared : &p.w;
-        wb = kUp ? (shared ? &p.up_shared : &p.up) : wa;
-        // rows past the end repeat the last one; their results are not stored
-        const int r_a = min(kUp ? tile * 8 + g8 : tile * 16 + g8, p.rows - 1);
-        const int r_b = kUp ? r_a : min(tile * 16 + g8 + 8, p.rows - 1);
-        const size_t e0 = shared ? 0 : (size_t)grp * p.rows;
-        ra = e0 + r_a;
-        rb = e0 + r_b;
+// The token blocks of a phase that begins in token block `first`, by one warp:
+// lane k takes block first + k, as many as there are up to the share's last
+// (`last`, inclusive) and as fit into shared memory. Also looks up the x rows.
+__device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, int first, int last)
+{
+    const W4Product &p = a.p;
+    const int lane = threadIdx.x & 31, tb = first + lane;
+    const bool in = tb <= last;
+    const int g = in ? last_not_above(sm.pre, a.groups, tb) : 0;
+    const int skip = in ? (tb - sm.pre[g]) * a.tokens : 0, n = in ? min(a.tokens, sm.count[g] - skip) : 0;
+    const int pairs = (n + 1) >> 1, row0 = in ? sm.start[g] + skip : 0;
+    int upto = pairs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
-};
+    const bool take = in && upto <= a.x_pairs;    // the first always fits
+    const unsigned m = __ballot_sync(0xffffffffu, take);
+    if (take) sm.ent[lane] = {g, row0, n, upto - pairs};
+    if (lane == __popc(m) - 1) {
+        sm.n_ent = lane + 1;
+        sm.used = upto;
+    }
+    if (take) {                                   // x rows; a token that is not there stands for zeros
+        int xi[kW4Tokens];
+#pragma unroll
+        for (int i = 0; i < kW4Tokens; ++i) {
+            xi[i] = row0 + i;
+            if (!p.x_by_row) xi[i] = g >= p.E ? xi[i] - p.P : p.perm && i < n ? p.perm[xi[i]] : xi[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kW4Tokens; ++i)
+            if (i < 2 * pairs) sm.row[2 * (upto - pairs) + i] = i < n && (unsigned)xi[i] < (unsigned)p.x_rows ? xi[i] : -1;
+    }
+}
 
-constexpr int aux_word(int G) { return G == 32 ? 8 : 4; }
+// This lane's four weight rows of a unit: rows g and g + 8 of each fragment, in
+// the order gate f, up f, gate f + 8, up f + 8 with `up` weights.
+template <bool kUp>
+__device__ __forceinline__ size_t unit_row(const W4Args &a, int grp, int tile, int i)
+{
+    const int g8 = (threadIdx.x & 31) >> 2;
+    int r = kUp ? tile * 16 + g8 + 8 * (i >> 1) : tile * 32 + g8 + 8 * i;
+    // rows past the end repeat an earlier one, a multiple of 8 rows before (or
+    // the last); their results are not stored
+    if (r >= a.p.rows) {
+        r -= (r - a.p.rows + 8) & ~7;
+        if (r < 0) r = a.p.rows - 1;
+    }
+    return (grp >= a.p.E ? 0 : (size_t)grp * a.p.rows) + r;
+}
+template <bool kUp>
+__device__ __forceinline__ const W4Ptrs &unit_stack(const W4Args &a, int grp, int i)
+{
+    const bool shared = grp >= a.p.E;
+    return kUp && (i & 1) ? (shared ? a.p.up_shared : a.p.up) : (shared ? a.p.w_shared : a.p.w);
+}
 
 // The copies ahead: a walk over (unit, 128-column block) steps.
 template <bool kUp, int G, bool kZeros>
 struct Copier {
     int ent, tile, left;                          // left: blocks of the unit still to copy
-    int a_jump;                                   // aux: from the end of a row to the next tile's row
-    const uint8_t *qa, *qb, *aux;                 // aux: lanes 0, 1 of a row scales of rows g, g + 8; 2, 3 zero points
+    const uint8_t *q[4], *s, *z;                  // s, z: of row t of the four
 
     __device__ __forceinline__ void unit(const W4Args &a, const W4Smem &sm, int block)
     {
-        const UnitRows<kUp, G> r(a, sm.ent[ent].grp, tile);
-        const int t = threadIdx.x & 3, pitch = a.p.cols / 2, gpr = a.p.cols / G;
-        qa = r.wa->q + r.ra * pitch + t * 16 + (size_t)block * 64;
-        qb = r.wb->q + r.rb * pitch + t * 16 + (size_t)block * 64;
-        const size_t at = (t & 1 ? r.rb : r.ra) * gpr + (size_t)block * (kW4Block / G);
-        const W4Ptrs *w = t & 1 ? r.wb : r.wa;
-        aux = t < 2 ? reinterpret_cast<const uint8_t *>(w->s + at) : kZeros ? w->z + at : nullptr;
+        constexpr int GB = kW4Block / G;
+        const int grp = sm.ent[ent].grp, t = threadIdx.x & 3, pitch = a.p.cols / 2, gpr = a.p.cols / G;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = unit_stack<kUp>(a, grp, i).q + unit_row<kUp>(a, grp, tile, i) * pitch + t * 16 + (size_t)block * 64;
+        const W4Ptrs &w = unit_stack<kUp>(a, grp, t);
+        const size_t at = unit_row<kUp>(a, grp, tile, t) * gpr + block * GB;
+        s = reinterpret_cast<const uint8_t *>(w.s + at);
+        if (kZeros) z = w.z + at;
         left = a.p.cols / kW4Block - block;
-        a_jump = a.s_jump * (t < 2 ? 2 : 1);
+    }
+    // The aligned word that holds n bytes at p: from its start, no byte past them.
+    template <int W>
+    __device__ __forceinline__ static void word(void *dst, const uint8_t *p, int n)
+    {
+        const uint32_t in = (uint32_t)reinterpret_cast<uintptr_t>(p) & (W - 1);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(p - in), "n"(W),
+                     "r"(in + n)
+                     : "memory");
     }
     // One step into `st`, which ends the unit's walk or goes on in it.
     __device__ __forceinline__ void step(const W4Args &a, const W4Smem &sm, W4Stage<G> &st, bool more)
     {
-        constexpr int GB = kW4Block / G, W = aux_word(G);
-        const int lane = threadIdx.x & 31, t = lane & 3;
-        cp_async16(smem_u32(&st.q[0][lane]), qa, 16);
-        cp_async16(smem_u32(&st.q[1][lane]), qb, 16);
-        if (kZeros || t < 2) {                    // the aligned word that holds them, no byte past the last one
-            const uint32_t in = (uint32_t)reinterpret_cast<uintptr_t>(aux) & (W - 1);
-            const uint32_t n = in + (t < 2 ? 2 * GB : GB);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
-                             smem_u32(reinterpret_cast<uint8_t *>(st.aux[lane >> 2]) + t * W)),
-                         "l"(aux - in), "n"(W), "r"(n)
+        constexpr int GB = kW4Block / G, W = G == 32 ? 8 : 4;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_u32(&st.q[i][lane])), "l"(q[i])
                          : "memory");
+            q[i] += 64;
         }
-        qa += 64;
-        qb += 64;
-        aux += t < 2 ? 2 * GB : GB;
+        word<W>(reinterpret_cast<uint8_t *>(st.s) + lane * W, s, 2 * GB);
+        s += 2 * GB;
+        if (kZeros) {
+            word<4>(reinterpret_cast<uint8_t *>(st.z) + lane * 4, z, GB);
+            z += GB;
+        }
         if (--left == 0 && more) {
             if (++tile < a.tiles - 1) {           // whole tiles of one matrix lie at equal distances
-                qa += a.q_jump;
-                qb += a.q_jump;
-                aux += a_jump;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] += a.q_jump;
+                s += 2 * a.s_jump;
+                if (kZeros) z += a.s_jump;
                 left = a.p.cols / kW4Block;
             } else {
                 if (tile == a.tiles) {
@@ -250,129 +309,113 @@ struct Copier {
     }
 };
 
-// Scales (FP32) and zero points of a step from its copied words. la, lb, lz,
-// lzb: low address bits of the values, which say where in the word they are.
-template <int G, bool kZeros>
-__device__ __forceinline__ void read_aux(const uint4 (&aux)[G == 32 ? 2 : 1], uint32_t la, uint32_t lb, uint32_t lza, uint32_t lzb,
-                                         float (&sa)[kW4Block / G], float (&sb)[kW4Block / G], int (&za)[kW4Block / G],
-                                         int (&zb)[kW4Block / G])
+// Scales (FP32) of a step's four rows, and zero points, from their copied words.
+// at: index of a row's first group in its array, whose low bits say where in
+// the word it is; they are the same for the four rows, which lie multiples of
+// eight rows apart.
+template <int G>
+__device__ __forceinline__ void read_scales(const uint4 *w, uint32_t at, float (&s)[4][kW4Block / G])
 {
-    if constexpr (G == 32) {
-        const uint4 s = aux[0];
-        sa[0] = bf16_lo(s.x); sa[1] = bf16_hi(s.x); sa[2] = bf16_lo(s.y); sa[3] = bf16_hi(s.y);
-        sb[0] = bf16_lo(s.z); sb[1] = bf16_hi(s.z); sb[2] = bf16_lo(s.w); sb[3] = bf16_hi(s.w);
-        if (kZeros) {
-            const uint4 z = aux[1];
-            const uint32_t a = lza & 4 ? z.y : z.x, b = lzb & 4 ? z.w : z.z;
+    const uint32_t lo[4] = {w[0].x, G == 32 ? w[0].z : w[0].y, G == 32 ? w[G == 32].x : w[0].z, G == 32 ? w[G == 32].z : w[0].w};
+    const uint32_t hi[4] = {w[0].y, w[0].w, w[G == 32].y, w[G == 32].w};      // groups of 32 only
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                za[i] = (a >> (8 * i)) & 15;
-                zb[i] = (b >> (8 * i)) & 15;
-            }
-        }
-    } else {
-        const uint4 w = aux[0];
-        if constexpr (G == 64) {
-            sa[0] = bf16_lo(w.x); sa[1] = bf16_hi(w.x); sb[0] = bf16_lo(w.y); sb[1] = bf16_hi(w.y);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (G == 128) {
+            s[i][0] = at & 1 ? bf16_hi(lo[i]) : bf16_lo(lo[i]);
         } else {
-            sa[0] = la & 2 ? bf16_hi(w.x) : bf16_lo(w.x);
-            sb[0] = lb & 2 ? bf16_hi(w.y) : bf16_lo(w.y);
+            s[i][0] = bf16_lo(lo[i]);
+            s[i][1] = bf16_hi(lo[i]);
         }
-        if (kZeros) {
-            const uint32_t a = w.z >> (8 * (lza & 3)), b = w.w >> (8 * (lzb & 3));
-#pragma unroll
-            for (int i = 0; i < kW4Block / G; ++i) {
-                za[i] = (a >> (8 * i)) & 15;
-                zb[i] = (b >> (8 * i)) & 15;
-            }
+        if constexpr (G == 32) {
+            s[i][2] = bf16_lo(hi[i]);
+            s[i][3] = bf16_hi(hi[i]);
         }
     }
 }
-
-// One step: a 128-column block of 16 rows times NT token pairs. dig, sums and
-// sx point to this lane's share of the first pair's block.
-template <int G, bool kZeros, int NT>
-__device__ __forceinline__ void w4_step(const uint4 qa, const uint4 qb, const float (&sa)[kW4Block / G],
-                                        const float (&sb)[kW4Block / G], const int (&za)[kW4Block / G],
-                                        const int (&zb)[kW4Block / G], const uint4 *dig, const int2 *sums,
-                                        const float *sx, int blocks, float (&acc)[NT][4])
+template <int G>
+__device__ __forceinline__ void read_zeros(const uint4 &w, uint32_t at, int (&z)[4][kW4Block / G])
 {
-    constexpr int GB = kW4Block / G;
-    uint32_t a[4][4];                             // operand bytes of each 32-column slice
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t wa = word_of(qa, j), wb = word_of(qb, j);
-        a[j][0] = wa & 0x0f0f0f0fu;
-        a[j][1] = wb & 0x0f0f0f0fu;
-        a[j][2] = (wa >> 4) & 0x0f0f0f0fu;
-        a[j][3] = (wb >> 4) & 0x0f0f0f0fu;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = G == 32 ? v[i] : v[i] >> (8 * (at & 3));
+#pragma unroll
+        for (int k = 0; k < kW4Block / G; ++k) z[i][k] = (b >> (8 * k)) & 15;
     }
+}
+
+// One step: a 128-column block of two fragments of 16 rows times NT token
+// pairs. dig, sums and sx point to this lane's share of the first pair's block.
+// acc[pair][fragment][half]: rows g and g + 8 of token t >> 1, its digits 0 and
+// 1 in even lanes, digit 2 in odd ones.
+template <int G, bool kZeros, int NT>
+__device__ __forceinline__ void w4_step(const uint4 (&q)[4], const float (&s)[4][kW4Block / G],
+                                        const int (&z)[4][kW4Block / G], const uint4 *dig, const int *sums,
+                                        const float *sx, int blocks, float (&acc)[NT][kW4Frags][2])
+{
+    constexpr int GB = kW4Block / G, GS = G / 32; // groups of a block; 32-column slices of a group
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const uint4 d0 = dig[n * blocks * 64], d1 = dig[n * blocks * 64 + 32];
         const float x = sx[n * blocks * 2];
-        int part[4];
+        int part[kW4Frags][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (j % (G / 32) == 0) {
-                const int2 c = sums[n * blocks * GB * 4 + (j / (G / 32)) * 4];
-                if (kZeros) {
-                    const int gi = j / (G / 32);
-                    part[0] = -za[gi] * c.x;
-                    part[1] = -za[gi] * c.y;
-                    part[2] = -zb[gi] * c.x;
-                    part[3] = -zb[gi] * c.y;
-                } else {                          // staged as -8 times the digit sum
-                    part[0] = part[2] = c.x;
-                    part[1] = part[3] = c.y;
-                }
-            }
+            const int gi = j / GS;
+            if (j % GS == 0)
+#pragma unroll
+                for (int f = 0; f < kW4Frags; ++f) part[f][0] = part[f][1] = part[f][2] = part[f][3] = 0;
             const uint4 &d = j < 2 ? d0 : d1;
-            mma_u8s8(part, a[j][0], a[j][1], a[j][2], a[j][3], j & 1 ? d.z : d.x, j & 1 ? d.w : d.y);
-            if (j % (G / 32) == G / 32 - 1) {
-                const int gi = j / (G / 32);
-                const float fa = sa[gi] * x, fb = sb[gi] * x;
-                acc[n][0] = fmaf(fa, (float)part[0], acc[n][0]);
-                acc[n][1] = fmaf(fa, (float)part[1], acc[n][1]);
-                acc[n][2] = fmaf(fb, (float)part[2], acc[n][2]);
-                acc[n][3] = fmaf(fb, (float)part[3], acc[n][3]);
+#pragma unroll
+            for (int f = 0; f < kW4Frags; ++f) {
+                const uint32_t wa = word_of(q[2 * f], j), wb = word_of(q[2 * f + 1], j);
+                mma_u8s8(part[f], wa & 0x0f0f0f0fu, wb & 0x0f0f0f0fu, (wa >> 4) & 0x0f0f0f0fu, (wb >> 4) & 0x0f0f0f0fu,
+                         j & 1 ? d.z : d.x, j & 1 ? d.w : d.y);
+            }
+            if (j % GS == GS - 1) {
+                const int c = sums[n * blocks * GB * 4 + gi * 4];     // of this lane's digits; times -8 without zero points
+#pragma unroll
+                for (int f = 0; f < kW4Frags; ++f)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int sum = part[f][2 * h] * 256 + part[f][2 * h + 1] + (kZeros ? -z[2 * f + h][gi] * c : c);
+                        acc[n][f][h] = fmaf(s[2 * f + h][gi] * x, (float)sum, acc[n][f][h]);
+                    }
             }
         }
     }
 }
 
 // The digits' sums of a token pair joined: lane (g, t) gets row g + 8 (t & 1)
-// of token t >> 1. Even lanes hold digits 0 and 1, odd lanes digit 2.
-__device__ __forceinline__ float join_digits(const float (&acc)[4])
+// of token t >> 1.
+__device__ __forceinline__ float join_digits(const float (&acc)[2])
 {
     const bool odd = threadIdx.x & 1;
-    const float a = odd ? acc[0] : fmaf(acc[0], 65536.f, acc[1] * 256.f);
-    const float b = odd ? acc[2] : fmaf(acc[2], 65536.f, acc[3] * 256.f);
-    const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-    return (odd ? b : a) + other;
+    const float mine = odd ? acc[1] : acc[0], other = __shfl_xor_sync(0xffffffffu, odd ? acc[0] : acc[1], 1);
+    return fmaf(odd ? other : mine, 256.f, (odd ? mine : other) * (1.f / 256.f));
 }
 
-// Stores the joined sums v[pair] of a unit.
+// Stores the joined sums v[pair][fragment] of a unit.
 template <bool kUp, class YT, int NT>
-__device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e, int tile, const float (&v)[NT])
+__device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e, int tile, const float (&v)[NT][kW4Frags])
 {
     const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
     const bool shared = e.grp >= p.E;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int i = nt * 2 + (t >> 1);
+    for (int n = 0; n < NT; ++n) {
+        const int i = n * 2 + (t >> 1);
         const size_t row = (size_t)e.row0 + i;
-        if (kUp) {
-            const float up = __shfl_xor_sync(0xffffffffu, v[nt], 1);
-            const int f = tile * 8 + g8;
-            if (i < e.n && !(t & 1) && f < p.rows)
-                store_val(static_cast<YT *>(p.y) + row * p.rows + f, silu_mul(v[nt], up));
+        if (kUp) {                                // even lanes hold the gates: they take feature f, odd lanes f + 8
+            const float o = __shfl_xor_sync(0xffffffffu, t & 1 ? v[n][0] : v[n][1], 1);
+            const float gate = t & 1 ? o : v[n][0], up = t & 1 ? v[n][1] : o;
+            const int f = tile * 16 + g8 + 8 * (t & 1);
+            if (i < e.n && f < p.rows) store_val(static_cast<YT *>(p.y) + row * p.rows + f, silu_mul(gate, up));
         } else {
-            const int r = tile * 16 + g8 + 8 * (t & 1);
-            if (i < e.n && r < p.rows) {
-                YT *y = shared ? static_cast<YT *>(p.y_shared) + (row - p.P) * p.rows
-                               : static_cast<YT *>(p.y) + row * p.rows;
-                store_val(y + r, v[nt]);
+            YT *y = shared ? static_cast<YT *>(p.y_shared) + (row - p.P) * p.rows : static_cast<YT *>(p.y) + row * p.rows;
+#pragma unroll
+            for (int f = 0; f < kW4Frags; ++f) {
+                const int r = tile * 32 + 16 * f + g8 + 8 * (t & 1);
+                if (i < e.n && r < p.rows) store_val(y + r, v[n][f]);
             }
         }
     }
@@ -402,7 +445,7 @@ template <int G, bool kZeros, class XT>
 __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, int pairs, uint4 *dig, int *sums, float *sx)
 {
     constexpr int GB = kW4Block / G, GL = G / 8;  // groups of a block; lanes of a group
-    constexpr int kAhead = 4, kItems = kW4Threads / 16;
+    constexpr int kAhead = 2, kItems = kW4Threads / 16;
     const W4Product &p = a.p;
     const int blocks = p.cols / kW4Block, items = pairs * 2 * blocks;
     const int l16 = threadIdx.x & 15, jj = l16 >> 2, t = l16 & 3;
@@ -410,7 +453,7 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
         float v[kAhead][8];                       // all loads first: their latencies overlap
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int it = it0 + k * kItems, slot = it / blocks, b = it - slot * blocks;
+            const int it = it0 + k * kItems, slot = a.by_blocks(it), b = it - slot * blocks;
             const int xi = it < items ? sm.row[slot] : -1;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
@@ -418,7 +461,7 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int it = it0 + k * kItems, slot = it / blocks, b = it - slot * blocks, tok = slot & 1;
+            const int it = it0 + k * kItems, slot = a.by_blocks(it), b = it - slot * blocks, tok = slot & 1;
             if (it - (int)(threadIdx.x >> 4) % 2 >= items) break;     // both halves of the warp are past the end
             uint32_t top = 0;                     // bits of the largest |x|; NaN and infinity are the largest
 #pragma unroll
@@ -447,9 +490,9 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
             for (int j = 0; j < 3; ++j) out[((tok * 4 + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
             out[((tok * 4 + 3) * 4 + t) * 2] = make_uint2(0, 0);
             if (l16 % GL == 0) {
-                int *c = sums + (at * GB + l16 / GL) * 8 + tok * 4;
+                int *c = sums + (at * GB + l16 / GL) * 4 + tok * 2;
                 const int f = kZeros ? 1 : -8;
-                *reinterpret_cast<int4 *>(c) = make_int4(f * sum[0], f * sum[1], f * sum[2], 0);
+                *reinterpret_cast<int2 *>(c) = make_int2(f * (256 * sum[0] + sum[1]), f * 256 * sum[2]);
             }
             // a block with an infinity or a NaN makes this token's results NaN, and no other's
             if (l16 == 0) sx[at * 2 + tok] = (top >> 23) == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((ex - 21u) << 23);
@@ -461,9 +504,8 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
 struct WarpRun {
     int s, s1, issued, stage;                     // step, end, steps copied, ring stage of this step
     int block;                                    // first block of the unit at hand
-    bool open;                                    // the last unit goes on in later warps; v holds its sums so far
+    bool open;                                    // the last unit goes on in later warps; its sums so far lie in the ring
     int ent, tile;                                // the unit at hand
-    float v[kW4Tiles];
 };
 
 // The units of one token block that are this warp's, for its NT token pairs.
@@ -475,37 +517,37 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
     const int blocks = a.p.cols / kW4Block;
     const W4Entry e = sm.ent[r.ent];
-    const int at = e.tile0 * blocks;
-    const uint4 *d0 = dig + at * 64 + lane;
-    const int2 *c0 = reinterpret_cast<const int2 *>(sums) + at * GB * 4 + t;
-    const float *x0 = sx + at * 2 + (t >> 1);
-    uint32_t ia = 0, ib = 0;                      // low bits of the group's index, which tell the place in its copied word
+    const int at0 = e.tile0 * blocks;
+    const uint4 *d0 = dig + at0 * 64 + lane;
+    const int *c0 = sums + at0 * GB * 4 + t;
+    const float *x0 = sx + at0 * 2 + (t >> 1);
+    uint32_t at = 0;                              // index of the first row's group at hand, modulo 2^32
     bool fresh = true;
     while (true) {
         if (fresh || r.tile == a.tiles - 1) {     // the last tile of a matrix may repeat rows
-            const UnitRows<kUp, G> w(a, e.grp, r.tile);
-            const uint32_t gpr = a.p.cols / G;
-            ia = (uint32_t)w.ra * gpr + r.block * GB;
-            ib = (uint32_t)w.rb * gpr + r.block * GB;
+            at = (uint32_t)unit_row<kUp>(a, e.grp, r.tile, 0) * (uint32_t)(a.p.cols / G) + r.block * GB;
             fresh = false;
         }
         const uint4 *d = d0 + r.block * 64;
-        const int2 *c = c0 + r.block * GB * 4;
+        const int *c = c0 + r.block * GB * 4;
         const float *x = x0 + r.block * 2;
-        float acc[NT][4];
+        float acc[NT][kW4Frags][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+            for (int f = 0; f < kW4Frags; ++f)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[n][f][i] = 0.f;
         const int n_steps = min(blocks - r.block, r.s1 - r.s);
         for (int i = 0; i < n_steps; ++i) {
             W4Stage<G> &st = ring[r.stage];
             cp_async_wait<kW4Stages - 2>();
             __syncwarp();                         // every lane's copies of this step; reads of the last one are done
-            const uint4 qa = st.q[0][lane], qb = st.q[1][lane];
-            float sa[GB], sb[GB];
-            int za[GB], zb[GB];
-            read_aux<G, kZeros>(st.aux[lane >> 2], 2 * ia, 2 * ib, ia, ib, sa, sb, za, zb);
+            const uint4 q[4] = {st.q[0][lane], st.q[1][lane], st.q[2][lane], st.q[3][lane]};
+            float s[4][GB];
+            int z[4][GB];
+            read_scales<G>(st.s[lane >> 2], at, s);
+            if (kZeros) read_zeros<G>(st.z[lane >> 2], at, z);
             // the stage used one step ago takes the copy kW4Stages - 1 steps ahead
             const int prev = r.stage == 0 ? kW4Stages - 1 : r.stage - 1;
             if (r.issued < r.s1) {
@@ -514,32 +556,37 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
             }
             cp_async_commit();                    // an empty group past the end keeps the count
             r.stage = r.stage + 1 == kW4Stages ? 0 : r.stage + 1;
-            w4_step<G, kZeros, NT>(qa, qb, sa, sb, za, zb, d, c, x, blocks, acc);
+            w4_step<G, kZeros, NT>(q, s, z, d, c, x, blocks, acc);
             d += 64;
             c += GB * 4;
             x += 2;
-            ia += GB;
-            ib += GB;
+            at += GB;
         }
         r.s += n_steps;
         const bool whole = r.block == 0, ends = r.block + n_steps == blocks;
         r.block = 0;
-        float v[NT];
+        float v[NT][kW4Frags];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) v[n] = join_digits(acc[n]);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int f = 0; f < kW4Frags; ++f) v[n][f] = join_digits(acc[n][f]);
         if (whole && ends) {
             store_unit<kUp, YT, NT>(a.p, e, r.tile, v);
         } else if (!whole) {                      // begun by an earlier warp
 #pragma unroll
-            for (int n = 0; n < NT; ++n) sm.head[warp][n][lane] = v[n];
-        } else {
-            r.open = true;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) r.v[n] = v[n];
+                for (int f = 0; f < kW4Frags; ++f) sm.head[warp][n][f][lane] = v[n][f];
+        } else {
+            r.open = true;                        // the warp's last step: its ring is free
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int f = 0; f < kW4Frags; ++f) reinterpret_cast<float *>(ring)[(n * kW4Frags + f) * 32 + lane] = v[n][f];
         }
         if (r.s >= r.s1) return;
-        ia += a.s_jump;
-        ib += a.s_jump;
+        at += a.s_jump;
         if (++r.tile == a.tiles) {
             r.tile = 0;
             ++r.ent;
@@ -559,8 +606,8 @@ w4_kernel(const __grid_constant__ W4Args a)
     const int blocks = p.cols / kW4Block;
     W4Stage<G> *ring = reinterpret_cast<W4Stage<G> *>(smem_raw + kW4Tables) + (threadIdx.x >> 5) * kW4Stages;
     uint4 *dig = reinterpret_cast<uint4 *>(smem_raw + kW4FixedSmem<G>);
-    int *sums = reinterpret_cast<int *>(dig + (size_t)a.x_tiles * blocks * 64);
-    float *sx = reinterpret_cast<float *>(sums + (size_t)a.x_tiles * blocks * GB * 8);
+    int *sums = reinterpret_cast<int *>(dig + (size_t)a.x_pairs * blocks * 64);
+    float *sx = reinterpret_cast<float *>(sums + (size_t)a.x_pairs * blocks * GB * 4);
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -580,7 +627,7 @@ w4_kernel(const __grid_constant__ W4Args a)
                 group_rows(p, g, &start, &count);
                 sm.start[g] = start;
                 sm.count[g] = count;
-                const int full = count / a.tokens, rest = count - full * a.tokens;
+                const int full = a.by_tokens(count), rest = count - full * a.tokens;
                 n_blocks[i] = full + (rest > 0);
                 cost[i] = full * w4_cost(a.tokens) + (rest ? w4_cost(rest) : 0);
             }
@@ -594,51 +641,42 @@ w4_kernel(const __grid_constant__ W4Args a)
             const int g = threadIdx.x * per + i;
             if (i >= per || g >= a.groups) break;
             sm.pre[g] = run;
-            sm.cost[g] = run_cost * a.tiles;
+            sm.cost[g] = (int)run_cost;
             run += n_blocks[i];
             run_cost += cost[i];
             if (g == a.groups - 1) {
-                sm.pre[a.groups] = run;
-                sm.cost[a.groups] = run_cost * a.tiles;
+                // ranges that overlap (which no dispatch makes) could count beyond 32 bits: then nothing is done
+                const bool fits = run_cost < 0x7fffffffLL;
+                sm.pre[a.groups] = fits ? run : 0;
+                sm.cost[a.groups] = fits ? (int)run_cost : 0;
             }
         }
     }
     __syncthreads();
-    // this CTA's share of the cost c: from c b / gridDim.x on, in parts that stay below 2^63
-    const long long c = sm.cost[a.groups];
-    auto at_share = [&](int b) { return unit_at(a, sm, c / gridDim.x * b + c % gridDim.x * b / gridDim.x); };
-    const long long u1 = at_share(blockIdx.x + 1);
-    for (long long u0 = at_share(blockIdx.x); u0 < u1;) {
-        // the phase's token blocks: every warp works them out, each writes its share
-        int n_ent = 0, used = 0;
-        long long phase_end;
-        {
-            int tb = (int)(u0 / a.tiles), g = last_not_above(sm.pre, a.groups, tb);
-            for (; n_ent < kW4Entries && (long long)tb * a.tiles < u1; ++n_ent, ++tb) {
-                while (sm.pre[g + 1] <= tb) ++g;
-                const int first = (tb - sm.pre[g]) * a.tokens, n = min(a.tokens, sm.count[g] - first);
-                const int pairs = (n + 1) / 2, row0 = sm.start[g] + first;
-                if (n_ent && used + pairs > a.x_tiles) break;
-                if (n_ent % kW4Warps == warp) {
-                    if (lane == 0) sm.ent[n_ent] = {g, row0, n, used};
-                    if (lane < 2 * pairs) {       // x rows; a token that is not there stands for zeros
-                        int xi = row0 + lane;
-                        if (lane < n && !p.x_by_row) xi = g >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
-                        sm.row[used * 2 + lane] = lane < n && (unsigned)xi < (unsigned)p.x_rows ? xi : -1;
-                    }
-                }
-                used += pairs;
-            }
-            phase_end = min((long long)tb * a.tiles, u1);
+    if (sm.cost[a.groups] == 0) return;           // no rows
+    if (warp == 0) {
+        if (lane < 2) reinterpret_cast<int2 *>(sm.share)[lane] = share_begin(a, sm, blockIdx.x + lane);
+        __syncwarp();
+        plan_phase(a, sm, sm.share[0], sm.share[2] - (sm.share[3] == 0));
+    }
+    __syncthreads();
+    const int2 u1 = make_int2(sm.share[2], sm.share[3]);
+    for (int2 u0 = make_int2(sm.share[0], sm.share[1]); u0.x < u1.x || (u0.x == u1.x && u0.y < u1.y);) {
+        const int n_ent = sm.n_ent, used = sm.used;
+        int units = n_ent * a.tiles - u0.y;
+        int2 next = make_int2(u0.x + n_ent, 0);
+        if (next.x > u1.x) {                      // the share ends inside the last token block
+            units -= a.tiles - u1.y;
+            next = u1;
         }
-        __syncthreads();
-        const int first_tile = (int)(u0 % a.tiles), steps = (int)(phase_end - u0) * blocks;
+        const int steps = units * blocks;
         const int s0 = (int)((long long)steps * warp / kW4Warps);
-        WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, s0 % blocks, false, 0, 0, {}};
+        const int unit0 = a.by_blocks(s0);
+        WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, s0 - unit0 * blocks, false, 0, 0};
         Copier<kUp, G, kZeros> cp{};
         if (r.s < r.s1) {
-            r.ent = (first_tile + s0 / blocks) / a.tiles;
-            r.tile = first_tile + s0 / blocks - r.ent * a.tiles;
+            r.ent = a.by_tiles(u0.y + unit0);
+            r.tile = u0.y + unit0 - r.ent * a.tiles;
             cp.ent = r.ent;
             cp.tile = r.tile;
             cp.unit(a, sm, r.block);
@@ -662,19 +700,31 @@ w4_kernel(const __grid_constant__ W4Args a)
         __syncthreads();
         if (r.open) {                             // the warp that began a shared unit adds it up
             const W4Entry e = sm.ent[r.ent];
-            const int end = ((r.s1 - 1) / blocks + 1) * blocks;       // the unit's last step + 1
+            const int end = a.by_blocks(r.s1 - 1) * blocks + blocks;     // the unit's last step + 1
+            float v[kW4Pairs][kW4Frags] = {};
+#pragma unroll
+            for (int n = 0; n < kW4Pairs; ++n)
+                if (2 * n < e.n)
+#pragma unroll
+                    for (int f = 0; f < kW4Frags; ++f) v[n][f] = reinterpret_cast<float *>(ring)[(n * kW4Frags + f) * 32 + lane];
             for (int w = warp + 1; w < kW4Warps; ++w) {
                 const int w0 = (int)((long long)steps * w / kW4Warps), w1 = (int)((long long)steps * (w + 1) / kW4Warps);
                 if (w0 >= end) break;
                 if (w0 == w1) continue;           // a warp without steps
 #pragma unroll
-                for (int k = 0; k < kW4Tiles; ++k)
-                    if (2 * k < e.n) r.v[k] += sm.head[w][k][lane];
+                for (int n = 0; n < kW4Pairs; ++n)
+                    if (2 * n < e.n)
+#pragma unroll
+                        for (int f = 0; f < kW4Frags; ++f) v[n][f] += sm.head[w][n][f][lane];
             }
-            store_unit<kUp, YT, kW4Tiles>(p, e, r.tile, r.v);
+            store_unit<kUp, YT, kW4Pairs>(p, e, r.tile, v);
         }
-        u0 = phase_end;
-        if (u0 < u1) __syncthreads();             // tables and digits are free for the next phase
+        u0 = next;
+        if (u0.x < u1.x || (u0.x == u1.x && u0.y < u1.y)) {
+            __syncthreads();                      // tables and digits are free again
+            if (warp == 0) plan_phase(a, sm, u0.x, u1.x - (u1.y == 0));
+            __syncthreads();
+        }
     }
 }
 
@@ -691,16 +741,22 @@ template <bool kUp, int G, bool kZeros, class XT, class YT>
 static kmoe_status run_w4(W4Args a, cudaStream_t st)
 {
     const size_t x_bytes = w4_x_bytes(a.p.cols, G);
-    a.x_tiles = (int)std::min<size_t>((kW4SmemMax - kW4FixedSmem<G>) / x_bytes, kW4Entries * kW4Tiles);
-    if (a.x_tiles < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
-    a.tokens = 2 * std::min(a.x_tiles, kW4Tiles);
-    constexpr int kTileRows = kUp ? 8 : 16;
+    a.x_pairs = (int)std::min<size_t>((kW4SmemMax - kW4FixedSmem<G>) / x_bytes, kW4Entries * kW4Pairs);
+    if (a.x_pairs < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
+    a.tokens = 2 * std::min(a.x_pairs, kW4Pairs);
+    constexpr int kTileRows = kUp ? 16 : 32;
+    a.tiles = (a.p.rows + kTileRows - 1) / kTileRows;
     a.q_jump = (kTileRows - 1) * (a.p.cols / 2);
     a.s_jump = (kTileRows - 1) * (a.p.cols / G);
+    const int blocks = a.p.cols / kW4Block;
+    a.by_blocks = DivideBy::make(blocks);
+    a.by_tiles = DivideBy::make(a.tiles);
+    a.by_tokens = DivideBy::make(a.tokens);
     // no more CTAs than units there can be: an expert with rows has at least one token block
     const long long most = ((long long)std::min(a.p.E, a.p.P) + (a.p.P + a.p.n_shared) / a.tokens + 1) * a.tiles;
     const int grid = (int)std::min<long long>(sm_count_w4(), most);
-    const size_t smem = kW4FixedSmem<G> + a.x_tiles * x_bytes;
+    a.by_grid = DivideBy::make(grid);
+    const size_t smem = kW4FixedSmem<G> + a.x_pairs * x_bytes;
     cudaFuncSetAttribute(w4_kernel<kUp, G, kZeros, XT, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     launch_pdl(w4_kernel<kUp, G, kZeros, XT, YT>, grid, kW4Threads, smem, st, a);
     return check_launch("w4");
@@ -719,11 +775,11 @@ static kmoe_status pick_w4(const W4Args &a, cudaStream_t st)
 
 kmoe_status launch_w4(const W4Product &p, cudaStream_t st)
 {
-    W4Args a{p, 0, p.E + (p.n_shared > 0 ? 1 : 0), 0, 0, 0, 0};
+    W4Args a{};
+    a.p = p;
+    a.groups = p.E + (p.n_shared > 0 ? 1 : 0);
     if (a.groups > kW4MaxGroups) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: too many experts");
-    const bool up = p.up.q != nullptr;
-    a.tiles = up ? (p.rows + 7) / 8 : (p.rows + 15) / 16;
-    if (up) return pick_w4<true, __nv_bfloat16, float>(a, st);
+    if (p.up.q != nullptr) return pick_w4<true, __nv_bfloat16, float>(a, st);
     if (p.x_f32) return pick_w4<false, float, __nv_bfloat16>(a, st);
     return p.y_dtype == KMOE_F32 ? pick_w4<false, __nv_bfloat16, float>(a, st)
                                  : pick_w4<false, __nv_bfloat16, __nv_bfloat16>(a, st);

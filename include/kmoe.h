@@ -299,7 +299,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * x device [N, cols] BF16; w: E matrices [rows, cols]; perm_token device [P]
  * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
  * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,
- * 128 <= cols <= 10240 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
+ * 128 <= cols <= 8192 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
  */
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,

@@ -72,7 +72,7 @@ def test_linear_w4_checks_its_arguments(lib):
     assert linear(lib, P=0, x=None, y=None) == OK
     for kw, code in ((dict(x_dtype=0), UNSUP), (dict(y_dtype=3), UNSUP), (dict(N=-1), BAD), (dict(P=-1), BAD),
                      (dict(rows=0), UNSUP), (dict(rows=65537), UNSUP), (dict(cols=200), UNSUP), (dict(cols=0), UNSUP),
-                     (dict(cols=10240 + 128), UNSUP), (dict(E=0, off=A), UNSUP), (dict(E=1025, off=A), UNSUP),
+                     (dict(cols=8192 + 128), UNSUP), (dict(E=0, off=A), UNSUP), (dict(E=1025, off=A), UNSUP),
                      (dict(E=2), BAD), (dict(N=3), BAD), (dict(x=None), BAD), (dict(y=None), BAD), (dict(y=OFF), BAD),
                      (dict(perm=OFF), BAD), (dict(off=OFF), BAD), (dict(w=w4(group=48)), UNSUP),
                      (dict(w=w4(codes=None)), BAD), (dict(w=w4(scales=OFF)), BAD), (dict(w=w4(zeros=OFF)), BAD)):
