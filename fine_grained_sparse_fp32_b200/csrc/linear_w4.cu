@@ -21,7 +21,7 @@
 // With `up` weights, rows 0-7 of a fragment are eight gate features and rows
 // 8-15 the same eight up features, and SiLU(gate) * up is written.
 //
-// A unit is two fragments (32 rows; 16 features) of one expert for up to 8
+// A unit is two fragments (32 rows; 16 features) of one expert for up to 4
 // tokens: the digits read for one fragment serve both. The units of all experts
 // that have rows are numbered through and every CTA (one per SM) takes a
 // contiguous share of them, in phases: as many units as the digits of their
@@ -45,16 +45,15 @@ using namespace sm100;
 constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Frags = 2;                       // row fragments of a unit
-constexpr int kW4Pairs = 4;                       // column fragments of two tokens (three digits each) of a unit
-constexpr int kW4Tokens = 2 * kW4Pairs;
+constexpr int kW4Pairs = 2;                       // column fragments of two tokens (three digits each) of a unit
 constexpr int kW4Stages = 3;                      // steps of a warp's copies in flight, plus the one in use
 constexpr int kW4MaxGroups = 1025;
 constexpr int kW4Entries = 32;                    // token blocks of a phase
+constexpr int kW4Known = 1024;                    // token blocks whose expert is looked up in a table
 constexpr int kW4SmemMax = 226 * 1024;
 
-// Instructions of a step by its tokens, in units of about 55: what the CTAs'
-// shares are cut by.
-__host__ __device__ constexpr int w4_cost(int tokens) { return 2 + (tokens + 1) / 2; }
+// Cost of a step by its tokens: what the CTAs' shares are cut by.
+__host__ __device__ constexpr int w4_cost(int tokens) { return 3 + (tokens + 1) / 2; }
 
 // Division by a number that the host knows: the high word of n * ceil(2^64 / d),
 // exact for n < 2^32 and 1 < d < 2^32.
@@ -92,30 +91,38 @@ struct W4Entry {
 // One step's copies of a warp: code bytes of rows g, g + 8 (gate, up) of both
 // fragments by lane, then for each g the words that hold the four rows' scales
 // (4 bytes; 8 with groups of 32) and the words that hold their zero points.
-template <int G>
+template <int G, bool kZeros>
 struct W4Stage {
     uint4 q[2 * kW4Frags][32];
     uint4 s[8][G == 32 ? 2 : 1];
-    uint4 z[8];
+    uint4 z[kZeros ? 8 : 1];
 };
 
-struct W4Smem {
+struct alignas(16) W4Smem {
     float head[kW4Warps][kW4Pairs][kW4Frags][32]; // sums of a unit that an earlier warp began
     long long scan_tmp[32];
     W4Entry ent[kW4Entries];
     int share[4];                                 // this CTA's first unit and the one behind its last: token block, tile
     int n_ent, used;                              // the phase's token blocks, their token pairs
-    int row[kW4Entries * kW4Tokens];              // x row of every staged token (two per pair), -1: none
-    int pre[kW4MaxGroups + 1];                    // token blocks of the experts before
-    int cost[kW4MaxGroups + 1];                   // and their cost
-    int start[kW4MaxGroups + 1], count[kW4MaxGroups + 1];     // rows of every expert
+    uint8_t pair_ent[kW4Entries * kW4Pairs];      // token block of every staged pair
+    uint16_t known[kW4Known];                     // expert of the first token blocks
 };
-// behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][32], digit sums int [pair][block][128 / G][4],
-// scales of the digits float [pair][block][2]
-__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G) { return (size_t)(cols / kW4Block) * (1024 + 16 * (kW4Block / G) + 8); }
-constexpr size_t kW4Tables = (sizeof(W4Smem) + 127) / 128 * 128;
-template <int G>
-constexpr size_t kW4FixedSmem = kW4Tables + sizeof(W4Stage<G>) * kW4Warps * kW4Stages;
+static_assert(sizeof(W4Smem) % 16 == 0, "what follows is 16-byte aligned");
+// Behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][6][4], digit sums int [pair][block][128 / G][4],
+// scales of the digits float [pair][block][2], and four tables of the experts.
+constexpr int kW4Digits = 2 * 6 * 4;              // 16-byte pieces of a token pair's block
+__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G)
+{
+    return (size_t)(cols / kW4Block) * (16 * kW4Digits + 16 * (kW4Block / G) + 8);
+}
+template <int G, bool kZeros>
+__host__ __device__ constexpr size_t w4_ring_bytes() { return sizeof(W4Stage<G, kZeros>) * kW4Warps * kW4Stages; }
+
+// The experts' tables in shared memory, groups + 1 entries each.
+struct W4Tables {
+    int *pre, *cost;                              // token blocks of the experts before, and their cost
+    int *start, *count;                           // rows of every expert
+};
 
 // Rows [start, start + count) of group g (expert or shared expert), cut to the batch.
 __device__ __forceinline__ void group_rows(const W4Product &p, int g, int *start, int *count)
@@ -174,30 +181,29 @@ __device__ __forceinline__ int last_not_above(const int *v, int n, int x)
 // The unit (token block, numbered through all experts, and tile) at which share
 // b of gridDim.x begins: the place b / gridDim.x of the total cost, in whole
 // units of cost and a rest over gridDim.x, so that everything fits into 32 bits.
-__device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Smem &sm, int b)
+__device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Tables &tab, int b)
 {
-    const int c = sm.cost[a.groups], grid = gridDim.x;
-    if (b >= grid) return make_int2(sm.pre[a.groups], 0);
+    const int c = tab.cost[a.groups], grid = gridDim.x;
+    if (b >= grid) return make_int2(tab.pre[a.groups], 0);
     const int q = a.by_grid(c), r = (c - q * grid) * b, rq = a.by_grid(r), whole = q * b + rq, rest = r - rq * grid;
-    const int g = last_not_above(sm.cost, a.groups, whole), count = sm.count[g];
-    const int full = w4_cost(a.tokens), tb = min((whole - sm.cost[g]) / full, a.by_tokens(count - 1));
-    const int left = whole - sm.cost[g] - tb * full, w = w4_cost(min(a.tokens, count - tb * a.tokens));
+    const int g = last_not_above(tab.cost, a.groups, whole), count = tab.count[g];
+    const int full = w4_cost(a.tokens), tb = min((whole - tab.cost[g]) / full, a.by_tokens(count - 1));
+    const int left = whole - tab.cost[g] - tb * full, w = w4_cost(min(a.tokens, count - tb * a.tokens));
     // left < 8, rest < grid, tiles <= 4096
     const int tile = (int)((uint32_t)(left * grid + rest) * (uint32_t)a.tiles / (uint32_t)(w * grid));
-    return tile < a.tiles ? make_int2(sm.pre[g] + tb, tile) : make_int2(sm.pre[g] + tb + 1, 0);
+    return tile < a.tiles ? make_int2(tab.pre[g] + tb, tile) : make_int2(tab.pre[g] + tb + 1, 0);
 }
 
 // The token blocks of a phase that begins in token block `first`, by one warp:
 // lane k takes block first + k, as many as there are up to the share's last
-// (`last`, inclusive) and as fit into shared memory. Also looks up the x rows.
-__device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, int first, int last)
+// (`last`, inclusive) and as fit into shared memory.
+__device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, const W4Tables &tab, int first, int last)
 {
-    const W4Product &p = a.p;
     const int lane = threadIdx.x & 31, tb = first + lane;
     const bool in = tb <= last;
-    const int g = in ? last_not_above(sm.pre, a.groups, tb) : 0;
-    const int skip = in ? (tb - sm.pre[g]) * a.tokens : 0, n = in ? min(a.tokens, sm.count[g] - skip) : 0;
-    const int pairs = (n + 1) >> 1, row0 = in ? sm.start[g] + skip : 0;
+    const int g = !in ? 0 : tb < kW4Known ? sm.known[tb] : last_not_above(tab.pre, a.groups, tb);
+    const int skip = in ? (tb - tab.pre[g]) * a.tokens : 0, n = in ? min(a.tokens, tab.count[g] - skip) : 0;
+    const int pairs = (n + 1) >> 1, row0 = in ? tab.start[g] + skip : 0;
     int upto = pairs;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -206,21 +212,13 @@ __device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, int firs
     }
     const bool take = in && upto <= a.x_pairs;    // the first always fits
     const unsigned m = __ballot_sync(0xffffffffu, take);
-    if (take) sm.ent[lane] = {g, row0, n, upto - pairs};
+    if (take) {
+        sm.ent[lane] = {g, row0, n, upto - pairs};
+        for (int i = upto - pairs; i < upto; ++i) sm.pair_ent[i] = lane;
+    }
     if (lane == __popc(m) - 1) {
         sm.n_ent = lane + 1;
         sm.used = upto;
-    }
-    if (take) {                                   // x rows; a token that is not there stands for zeros
-        int xi[kW4Tokens];
-#pragma unroll
-        for (int i = 0; i < kW4Tokens; ++i) {
-            xi[i] = row0 + i;
-            if (!p.x_by_row) xi[i] = g >= p.E ? xi[i] - p.P : p.perm && i < n ? p.perm[xi[i]] : xi[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kW4Tokens; ++i)
-            if (i < 2 * pairs) sm.row[2 * (upto - pairs) + i] = i < n && (unsigned)xi[i] < (unsigned)p.x_rows ? xi[i] : -1;
     }
 }
 
@@ -239,13 +237,6 @@ __device__ __forceinline__ size_t unit_row(const W4Args &a, int grp, int tile, i
     }
     return (grp >= a.p.E ? 0 : (size_t)grp * a.p.rows) + r;
 }
-template <bool kUp>
-__device__ __forceinline__ const W4Ptrs &unit_stack(const W4Args &a, int grp, int i)
-{
-    const bool shared = grp >= a.p.E;
-    return kUp && (i & 1) ? (shared ? a.p.up_shared : a.p.up) : (shared ? a.p.w_shared : a.p.w);
-}
-
 // The copies ahead: a walk over (unit, 128-column block) steps.
 template <bool kUp, int G, bool kZeros>
 struct Copier {
@@ -256,13 +247,17 @@ struct Copier {
     {
         constexpr int GB = kW4Block / G;
         const int grp = sm.ent[ent].grp, t = threadIdx.x & 3, pitch = a.p.cols / 2, gpr = a.p.cols / G;
+        const W4Product &p = a.p;
+        const bool shared = grp >= p.E, second = kUp && (t & 1);
+        // plain selects: the pointers come from the constant bank
+        const uint8_t *q0 = shared ? p.w_shared.q : p.w.q, *q1 = kUp ? (shared ? p.up_shared.q : p.up.q) : q0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            q[i] = unit_stack<kUp>(a, grp, i).q + unit_row<kUp>(a, grp, tile, i) * pitch + t * 16 + (size_t)block * 64;
-        const W4Ptrs &w = unit_stack<kUp>(a, grp, t);
+            q[i] = (i & 1 ? q1 : q0) + unit_row<kUp>(a, grp, tile, i) * pitch + t * 16 + (size_t)block * 64;
         const size_t at = unit_row<kUp>(a, grp, tile, t) * gpr + block * GB;
-        s = reinterpret_cast<const uint8_t *>(w.s + at);
-        if (kZeros) z = w.z + at;
+        const __nv_bfloat16 *s0 = second ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s);
+        s = reinterpret_cast<const uint8_t *>(s0 + at);
+        if (kZeros) z = (second ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at;
         left = a.p.cols / kW4Block - block;
     }
     // The aligned word that holds n bytes at p: from its start, no byte past them.
@@ -275,7 +270,7 @@ struct Copier {
                      : "memory");
     }
     // One step into `st`, which ends the unit's walk or goes on in it.
-    __device__ __forceinline__ void step(const W4Args &a, const W4Smem &sm, W4Stage<G> &st, bool more)
+    __device__ __forceinline__ void step(const W4Args &a, const W4Smem &sm, W4Stage<G, kZeros> &st, bool more)
     {
         constexpr int GB = kW4Block / G, W = G == 32 ? 8 : 4;
         const int lane = threadIdx.x & 31;
@@ -354,9 +349,10 @@ __device__ __forceinline__ void w4_step(const uint4 (&q)[4], const float (&s)[4]
                                         const float *sx, int blocks, float (&acc)[NT][kW4Frags][2])
 {
     constexpr int GB = kW4Block / G, GS = G / 32; // groups of a block; 32-column slices of a group
+    const int second = 1 - (threadIdx.x & 1);     // odd lanes hold digit 2 and a column without meaning
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const uint4 d0 = dig[n * blocks * 64], d1 = dig[n * blocks * 64 + 32];
+        const uint4 d0 = dig[n * blocks * kW4Digits], d1 = dig[n * blocks * kW4Digits + kW4Digits / 2];
         const float x = sx[n * blocks * 2];
         int part[kW4Frags][4];
 #pragma unroll
@@ -378,7 +374,7 @@ __device__ __forceinline__ void w4_step(const uint4 (&q)[4], const float (&s)[4]
                 for (int f = 0; f < kW4Frags; ++f)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int sum = part[f][2 * h] * 256 + part[f][2 * h + 1] + (kZeros ? -z[2 * f + h][gi] * c : c);
+                        const int sum = part[f][2 * h] * 256 + part[f][2 * h + 1] * second + (kZeros ? -z[2 * f + h][gi] * c : c);
                         acc[n][f][h] = fmaf(s[2 * f + h][gi] * x, (float)sum, acc[n][f][h]);
                     }
             }
@@ -454,7 +450,16 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int it = it0 + k * kItems, slot = a.by_blocks(it), b = it - slot * blocks;
-            const int xi = it < items ? sm.row[slot] : -1;
+            int xi = -1;                          // x row; a token that is not there stands for zeros
+            if (it < items) {
+                const W4Entry e = sm.ent[sm.pair_ent[slot >> 1]];
+                const int i = slot - 2 * e.tile0;
+                if (i < e.n) {
+                    xi = e.row0 + i;
+                    if (!p.x_by_row) xi = e.grp >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
+                    if ((unsigned)xi >= (unsigned)p.x_rows) xi = -1;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
             if (xi >= 0) load8(static_cast<const XT *>(p.x) + (size_t)xi * p.cols + b * kW4Block + l16 * 8, v[k]);
@@ -485,10 +490,9 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
                 for (int j = 0; j < 3; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
             if (it >= items) continue;
             const int at = (slot >> 1) * blocks + b;
-            uint2 *out = reinterpret_cast<uint2 *>(dig + (at * 2 + (jj >> 1)) * 32) + (jj & 1);
+            uint2 *out = reinterpret_cast<uint2 *>(dig + (at * 2 + (jj >> 1)) * (kW4Digits / 2)) + (jj & 1);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) out[((tok * 4 + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
-            out[((tok * 4 + 3) * 4 + t) * 2] = make_uint2(0, 0);
+            for (int j = 0; j < 3; ++j) out[((tok * 3 + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
             if (l16 % GL == 0) {
                 int *c = sums + (at * GB + l16 / GL) * 4 + tok * 2;
                 const int f = kZeros ? 1 : -8;
@@ -510,7 +514,7 @@ struct WarpRun {
 
 // The units of one token block that are this warp's, for its NT token pairs.
 template <bool kUp, int G, bool kZeros, class YT, int NT>
-__device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G> *ring, const uint4 *dig, const int *sums,
+__device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G, kZeros> *ring, const uint4 *dig, const int *sums,
                                           const float *sx, WarpRun &r, Copier<kUp, G, kZeros> &cp)
 {
     constexpr int GB = kW4Block / G;
@@ -518,7 +522,8 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
     const int blocks = a.p.cols / kW4Block;
     const W4Entry e = sm.ent[r.ent];
     const int at0 = e.tile0 * blocks;
-    const uint4 *d0 = dig + at0 * 64 + lane;
+    // column g of a pair's fragment: digit g & 3 of token g >> 2; there is no fourth digit, its column repeats the third
+    const uint4 *d0 = dig + at0 * kW4Digits + ((lane >> 4) * 3 + min((lane >> 2) & 3, 2)) * 4 + t;
     const int *c0 = sums + at0 * GB * 4 + t;
     const float *x0 = sx + at0 * 2 + (t >> 1);
     uint32_t at = 0;                              // index of the first row's group at hand, modulo 2^32
@@ -528,7 +533,7 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
             at = (uint32_t)unit_row<kUp>(a, e.grp, r.tile, 0) * (uint32_t)(a.p.cols / G) + r.block * GB;
             fresh = false;
         }
-        const uint4 *d = d0 + r.block * 64;
+        const uint4 *d = d0 + r.block * kW4Digits;
         const int *c = c0 + r.block * GB * 4;
         const float *x = x0 + r.block * 2;
         float acc[NT][kW4Frags][2];
@@ -540,7 +545,7 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
                 for (int i = 0; i < 2; ++i) acc[n][f][i] = 0.f;
         const int n_steps = min(blocks - r.block, r.s1 - r.s);
         for (int i = 0; i < n_steps; ++i) {
-            W4Stage<G> &st = ring[r.stage];
+            W4Stage<G, kZeros> &st = ring[r.stage];
             cp_async_wait<kW4Stages - 2>();
             __syncwarp();                         // every lane's copies of this step; reads of the last one are done
             const uint4 q[4] = {st.q[0][lane], st.q[1][lane], st.q[2][lane], st.q[3][lane]};
@@ -557,7 +562,7 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
             cp_async_commit();                    // an empty group past the end keeps the count
             r.stage = r.stage + 1 == kW4Stages ? 0 : r.stage + 1;
             w4_step<G, kZeros, NT>(q, s, z, d, c, x, blocks, acc);
-            d += 64;
+            d += kW4Digits;
             c += GB * 4;
             x += 2;
             at += GB;
@@ -604,10 +609,16 @@ w4_kernel(const __grid_constant__ W4Args a)
     constexpr int GB = kW4Block / G;
     const W4Product &p = a.p;
     const int blocks = p.cols / kW4Block;
-    W4Stage<G> *ring = reinterpret_cast<W4Stage<G> *>(smem_raw + kW4Tables) + (threadIdx.x >> 5) * kW4Stages;
-    uint4 *dig = reinterpret_cast<uint4 *>(smem_raw + kW4FixedSmem<G>);
-    int *sums = reinterpret_cast<int *>(dig + (size_t)a.x_pairs * blocks * 64);
-    float *sx = reinterpret_cast<float *>(sums + (size_t)a.x_pairs * blocks * GB * 4);
+    uint8_t *behind = smem_raw + sizeof(W4Smem);
+    W4Stage<G, kZeros> *ring = reinterpret_cast<W4Stage<G, kZeros> *>(behind) + (threadIdx.x >> 5) * kW4Stages;
+    uint4 *dig = reinterpret_cast<uint4 *>(behind + w4_ring_bytes<G, kZeros>());
+    int *sums = reinterpret_cast<int *>(dig + a.x_pairs * blocks * kW4Digits);
+    float *sx = reinterpret_cast<float *>(sums + a.x_pairs * blocks * GB * 4);
+    W4Tables tab;
+    tab.pre = reinterpret_cast<int *>(sx + a.x_pairs * blocks * 2);
+    tab.cost = tab.pre + a.groups + 1;
+    tab.start = tab.cost + a.groups + 1;
+    tab.count = tab.start + a.groups + 1;
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -625,8 +636,8 @@ w4_kernel(const __grid_constant__ W4Args a)
             if (i < per && g < a.groups) {
                 int start, count;
                 group_rows(p, g, &start, &count);
-                sm.start[g] = start;
-                sm.count[g] = count;
+                tab.start[g] = start;
+                tab.count[g] = count;
                 const int full = a.by_tokens(count), rest = count - full * a.tokens;
                 n_blocks[i] = full + (rest > 0);
                 cost[i] = full * w4_cost(a.tokens) + (rest ? w4_cost(rest) : 0);
@@ -640,24 +651,25 @@ w4_kernel(const __grid_constant__ W4Args a)
         for (int i = 0; i < 3; ++i) {
             const int g = threadIdx.x * per + i;
             if (i >= per || g >= a.groups) break;
-            sm.pre[g] = run;
-            sm.cost[g] = (int)run_cost;
+            tab.pre[g] = run;
+            tab.cost[g] = (int)run_cost;
+            for (int k = run; k < min(run + n_blocks[i], kW4Known); ++k) sm.known[k] = g;
             run += n_blocks[i];
             run_cost += cost[i];
             if (g == a.groups - 1) {
                 // ranges that overlap (which no dispatch makes) could count beyond 32 bits: then nothing is done
                 const bool fits = run_cost < 0x7fffffffLL;
-                sm.pre[a.groups] = fits ? run : 0;
-                sm.cost[a.groups] = fits ? (int)run_cost : 0;
+                tab.pre[a.groups] = fits ? run : 0;
+                tab.cost[a.groups] = fits ? (int)run_cost : 0;
             }
         }
     }
     __syncthreads();
-    if (sm.cost[a.groups] == 0) return;           // no rows
+    if (tab.cost[a.groups] == 0) return;           // no rows
     if (warp == 0) {
-        if (lane < 2) reinterpret_cast<int2 *>(sm.share)[lane] = share_begin(a, sm, blockIdx.x + lane);
+        if (lane < 2) reinterpret_cast<int2 *>(sm.share)[lane] = share_begin(a, tab, blockIdx.x + lane);
         __syncwarp();
-        plan_phase(a, sm, sm.share[0], sm.share[2] - (sm.share[3] == 0));
+        plan_phase(a, sm, tab, sm.share[0], sm.share[2] - (sm.share[3] == 0));
     }
     __syncthreads();
     const int2 u1 = make_int2(sm.share[2], sm.share[3]);
@@ -681,6 +693,7 @@ w4_kernel(const __grid_constant__ W4Args a)
             cp.tile = r.tile;
             cp.unit(a, sm, r.block);
         }
+#pragma unroll 1
         for (int i = 0; i < kW4Stages - 1; ++i) {
             if (r.issued < r.s1) {
                 ++r.issued;
@@ -693,9 +706,7 @@ w4_kernel(const __grid_constant__ W4Args a)
         while (r.s < r.s1) {
             const int nt = (sm.ent[r.ent].n + 1) / 2;
             if (nt == 1) run_entry<kUp, G, kZeros, YT, 1>(a, sm, ring, dig, sums, sx, r, cp);
-            else if (nt == 2) run_entry<kUp, G, kZeros, YT, 2>(a, sm, ring, dig, sums, sx, r, cp);
-            else if (nt == 3) run_entry<kUp, G, kZeros, YT, 3>(a, sm, ring, dig, sums, sx, r, cp);
-            else run_entry<kUp, G, kZeros, YT, 4>(a, sm, ring, dig, sums, sx, r, cp);
+            else run_entry<kUp, G, kZeros, YT, 2>(a, sm, ring, dig, sums, sx, r, cp);
         }
         __syncthreads();
         if (r.open) {                             // the warp that began a shared unit adds it up
@@ -722,7 +733,7 @@ w4_kernel(const __grid_constant__ W4Args a)
         u0 = next;
         if (u0.x < u1.x || (u0.x == u1.x && u0.y < u1.y)) {
             __syncthreads();                      // tables and digits are free again
-            if (warp == 0) plan_phase(a, sm, u0.x, u1.x - (u1.y == 0));
+            if (warp == 0) plan_phase(a, sm, tab, u0.x, u1.x - (u1.y == 0));
             __syncthreads();
         }
     }
@@ -741,7 +752,8 @@ template <bool kUp, int G, bool kZeros, class XT, class YT>
 static kmoe_status run_w4(W4Args a, cudaStream_t st)
 {
     const size_t x_bytes = w4_x_bytes(a.p.cols, G);
-    a.x_pairs = (int)std::min<size_t>((kW4SmemMax - kW4FixedSmem<G>) / x_bytes, kW4Entries * kW4Pairs);
+    const size_t fixed = sizeof(W4Smem) + w4_ring_bytes<G, kZeros>() + 4 * sizeof(int) * (a.groups + 1);
+    a.x_pairs = (int)std::min<size_t>((kW4SmemMax - fixed) / x_bytes, kW4Entries * kW4Pairs);
     if (a.x_pairs < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
     a.tokens = 2 * std::min(a.x_pairs, kW4Pairs);
     constexpr int kTileRows = kUp ? 16 : 32;
@@ -756,7 +768,7 @@ static kmoe_status run_w4(W4Args a, cudaStream_t st)
     const long long most = ((long long)std::min(a.p.E, a.p.P) + (a.p.P + a.p.n_shared) / a.tokens + 1) * a.tiles;
     const int grid = (int)std::min<long long>(sm_count_w4(), most);
     a.by_grid = DivideBy::make(grid);
-    const size_t smem = kW4FixedSmem<G> + a.x_pairs * x_bytes;
+    const size_t smem = fixed + a.x_pairs * x_bytes;
     cudaFuncSetAttribute(w4_kernel<kUp, G, kZeros, XT, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     launch_pdl(w4_kernel<kUp, G, kZeros, XT, YT>, grid, kW4Threads, smem, st, a);
     return check_launch("w4");
