@@ -49,6 +49,8 @@ constexpr int kW4Pairs = 2;                       // column fragments of two tok
 constexpr int kW4Stages = 3;                      // steps of a warp's copies in flight, plus the one in use
 constexpr int kW4MaxGroups = 1025;
 constexpr int kW4Entries = 32;                    // token blocks of a phase
+constexpr int kW4Perm = kW4Threads;               // rows whose token is looked up in a table
+constexpr int kW4Ahead = 3;                       // tokens' blocks a half-warp loads before it cuts the first into digits
 constexpr int kW4Known = 1024;                    // token blocks whose expert is looked up in a table
 constexpr int kW4SmemMax = 226 * 1024;
 
@@ -106,6 +108,7 @@ struct alignas(16) W4Smem {
     int n_ent, used;                              // the phase's token blocks, their token pairs
     uint8_t pair_ent[kW4Entries * kW4Pairs];      // token block of every staged pair
     uint16_t known[kW4Known];                     // expert of the first token blocks
+    int perm[kW4Perm];                            // token of the first rows
 };
 static_assert(sizeof(W4Smem) % 16 == 0, "what follows is 16-byte aligned");
 // Behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [pair][block][2][6][4], digit sums int [pair][block][128 / G][4],
@@ -154,17 +157,14 @@ __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
     }
     if (lane == 31) sm.scan_tmp[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        long long v = lane < kW4Warps ? sm.scan_tmp[lane] : 0;
+    long long v = lane < kW4Warps ? sm.scan_tmp[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < kW4Warps; o <<= 1) {
-            const long long n = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += n;
-        }
-        if (lane < kW4Warps) sm.scan_tmp[lane] = v;
+    for (int o = 1; o < kW4Warps; o <<= 1) {
+        const long long n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
     }
-    __syncthreads();
-    const long long before = incl - mine + (warp ? sm.scan_tmp[warp - 1] : 0);
+    const long long up = __shfl_sync(0xffffffffu, v, warp ? warp - 1 : 0);
+    const long long before = incl - mine + (warp ? up : 0);
     *count = (int)(before & 0x3fffffff);
     *cost = before >> 30;
 }
@@ -304,6 +304,37 @@ struct Copier {
     }
 };
 
+// Asks for the weights behind a warp's first copies to be brought into L2: up
+// to 16 KB, row by row. They arrive while the digits are made, when HBM would
+// otherwise wait.
+template <bool kUp>
+__device__ __forceinline__ void prefetch_units(const W4Args &a, const W4Smem &sm, int ent, int tile, int block, int steps)
+{
+    const W4Product &p = a.p;
+    const int lane = threadIdx.x & 31, blocks = p.cols / kW4Block;
+    block += kW4Stages - 1;
+    steps -= kW4Stages - 1;
+    for (int left = 8; left > 0 && steps > 0;) {
+        while (block >= blocks) {
+            block -= blocks;
+            if (++tile == a.tiles) {
+                tile = 0;
+                ++ent;
+            }
+        }
+        const int n = min(min(blocks - block, left), steps), grp = sm.ent[ent].grp;
+        const bool shared = grp >= p.E, second = kUp && lane >= 16;
+        const int r = kUp ? tile * 16 + (lane & 15) : tile * 32 + lane;
+        const uint8_t *q = second ? (shared ? p.up_shared.q : p.up.q) : (shared ? p.w_shared.q : p.w.q);
+        q += ((shared ? 0 : (size_t)grp * p.rows) + r) * (p.cols / 2) + (size_t)block * 64;
+        if (r < p.rows)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(n * 64) : "memory");
+        block += n;
+        left -= n;
+        steps -= n;
+    }
+}
+
 // Scales (FP32) of a step's four rows, and zero points, from their copied words.
 // at: index of a row's first group in its array, whose low bits say where in
 // the word it is; they are the same for the four rows, which lie multiples of
@@ -435,42 +466,53 @@ __device__ __forceinline__ void split_digits(const int (&v)[8], uint32_t (&w)[3]
     }
 }
 
-// Digits of the phase's tokens: 16 lanes take 128 columns of one token, eight
-// each. Pairs without a second token get zeros in its place.
-template <int G, bool kZeros, class XT>
-__device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, int pairs, uint4 *dig, int *sums, float *sx)
+// Eight columns of kW4Ahead staged tokens' blocks, from item it0 on (16 lanes
+// take the 128 columns of an item). A token that is not there stands for zeros.
+template <class XT>
+__device__ __forceinline__ void load_items(const W4Args &a, const W4Smem &sm, int it0, int items, float (&v)[kW4Ahead][8])
 {
-    constexpr int GB = kW4Block / G, GL = G / 8;  // groups of a block; lanes of a group
-    constexpr int kAhead = 2, kItems = kW4Threads / 16;
     const W4Product &p = a.p;
-    const int blocks = p.cols / kW4Block, items = pairs * 2 * blocks;
-    const int l16 = threadIdx.x & 15, jj = l16 >> 2, t = l16 & 3;
-    for (int it0 = threadIdx.x >> 4; it0 - (int)(threadIdx.x >> 4) < items; it0 += kItems * kAhead) {
-        float v[kAhead][8];                       // all loads first: their latencies overlap
+    const int blocks = p.cols / kW4Block;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int it = it0 + k * kItems, slot = a.by_blocks(it), b = it - slot * blocks;
-            int xi = -1;                          // x row; a token that is not there stands for zeros
-            if (it < items) {
-                const W4Entry e = sm.ent[sm.pair_ent[slot >> 1]];
-                const int i = slot - 2 * e.tile0;
-                if (i < e.n) {
-                    xi = e.row0 + i;
-                    if (!p.x_by_row) xi = e.grp >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
-                    if ((unsigned)xi >= (unsigned)p.x_rows) xi = -1;
-                }
+    for (int k = 0; k < kW4Ahead; ++k) {
+        const int it = it0 + k * (kW4Threads / 16), slot = a.by_blocks(it), b = it - slot * blocks;
+        int xi = -1;
+        if (it < items) {
+            const W4Entry e = sm.ent[sm.pair_ent[slot >> 1]];
+            const int i = slot - 2 * e.tile0;
+            if (i < e.n) {
+                xi = e.row0 + i;
+                if (!p.x_by_row) xi = e.grp >= p.E ? xi - p.P : !p.perm ? xi : xi < kW4Perm ? sm.perm[xi] : p.perm[xi];
+                if ((unsigned)xi >= (unsigned)p.x_rows) xi = -1;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-            if (xi >= 0) load8(static_cast<const XT *>(p.x) + (size_t)xi * p.cols + b * kW4Block + l16 * 8, v[k]);
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+        if (xi >= 0) load8(static_cast<const XT *>(p.x) + (size_t)xi * p.cols + b * kW4Block + (threadIdx.x & 15) * 8, v[k]);
+    }
+}
+
+// Digits of the phase's tokens; v holds the first items' values.
+template <int G, bool kZeros, class XT>
+__device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, int pairs, float (&v)[kW4Ahead][8], uint4 *dig,
+                                             int *sums, float *sx)
+{
+    constexpr int GB = kW4Block / G, GL = G / 8;  // groups of a block; lanes of a group
+    constexpr int kItems = kW4Threads / 16;
+    const int blocks = a.p.cols / kW4Block, items = pairs * 2 * blocks;
+    const int l16 = threadIdx.x & 15, jj = l16 >> 2, t = l16 & 3;
+#pragma unroll 1
+    for (int it0 = threadIdx.x >> 4;;) {
+#pragma unroll 1
+        for (int k = 0; k < kW4Ahead; ++k) {
             const int it = it0 + k * kItems, slot = a.by_blocks(it), b = it - slot * blocks, tok = slot & 1;
             if (it - (int)(threadIdx.x >> 4) % 2 >= items) break;     // both halves of the warp are past the end
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = k == 0 ? v[0][i] : k == 1 ? v[1][i] : v[2][i];
             uint32_t top = 0;                     // bits of the largest |x|; NaN and infinity are the largest
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             // exponent field of 2^E; below 2^-105 the digits stay at that scale (off by less than 2^-127)
@@ -478,7 +520,7 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
             const float mul = __uint_as_float((275u - ex) << 23);     // 2^(21 - E)
             int q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(v[k][i] * mul);
+            for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(x[i] * mul);
             uint32_t w[3][2];
             split_digits(q, w);
             int sum[3];
@@ -501,6 +543,9 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
             // a block with an infinity or a NaN makes this token's results NaN, and no other's
             if (l16 == 0) sx[at * 2 + tok] = (top >> 23) == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((ex - 21u) << 23);
         }
+        it0 += kItems * kW4Ahead;
+        if (it0 - (int)(threadIdx.x >> 4) % 2 >= items) break;
+        load_items<XT>(a, sm, it0, items, v);
     }
 }
 
@@ -625,6 +670,7 @@ w4_kernel(const __grid_constant__ W4Args a)
     if (a.p.status && blockIdx.x == 0 && threadIdx.x == 0) *a.p.status = 0;
 
     // rows, token blocks and cost of every expert, the latter as exclusive prefixes
+    if (p.perm && threadIdx.x < min(p.P, kW4Perm)) sm.perm[threadIdx.x] = p.perm[threadIdx.x];
     {
         const int per = (a.groups + kW4Threads - 1) / kW4Threads;     // 1 to 3
         int n_blocks[3], cost[3], run = 0;
@@ -684,6 +730,8 @@ w4_kernel(const __grid_constant__ W4Args a)
         const int steps = units * blocks;
         const int s0 = (int)((long long)steps * warp / kW4Warps);
         const int unit0 = a.by_blocks(s0);
+        float v[kW4Ahead][8];
+        load_items<XT>(a, sm, threadIdx.x >> 4, used * 2 * blocks, v);
         WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, s0 - unit0 * blocks, false, 0, 0};
         Copier<kUp, G, kZeros> cp{};
         if (r.s < r.s1) {
@@ -701,7 +749,8 @@ w4_kernel(const __grid_constant__ W4Args a)
             }
             cp_async_commit();
         }
-        stage_digits<G, kZeros, XT>(a, sm, used, dig, sums, sx);
+        prefetch_units<kUp>(a, sm, r.ent, r.tile, r.block, r.s1 - r.s);
+        stage_digits<G, kZeros, XT>(a, sm, used, v, dig, sums, sx);
         __syncthreads();
         while (r.s < r.s1) {
             const int nt = (sm.ent[r.ent].n + 1) / 2;
