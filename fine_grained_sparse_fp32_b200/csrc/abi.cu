@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 namespace kmoe {
@@ -72,6 +73,10 @@ static kmoe_status check_act_dtype(int t, const char *name)
     if (t != KMOE_F32 && t != KMOE_BF16) return fail(KMOE_ERR_UNSUPPORTED, "%s dtype %d: F32 or BF16 only", name, t);
     return KMOE_OK;
 }
+
+// From this many tokens 4-bit experts run on the tensor-core kernel.
+static const int kW4TcTokens = getenv("W4TC") ? atoi(getenv("W4TC")) : 128;
+static const int kW4TcLin = getenv("W4TCL") ? atoi(getenv("W4TCL")) : 64;
 
 // E4M3 weights with FP32 128 x 128 block scales (BF16 or FP8 activations).
 static bool fp8_weights(int w_dtype) { return w_dtype == KMOE_E4M3_B128 || w_dtype == KMOE_E4M3_B128_A8; }
@@ -280,12 +285,15 @@ static FfnPath ffn_path(int x_dtype, int w_dtype, int N, int d)
 }
 
 // Grouped FFN with 4-bit weights: H = SiLU(W_g x) * (W_u x) for routed and
-// shared rows in one launch, then both down projections in another. `status`
-// (NULL: left alone) is set to 0 by the first.
+// shared rows in one launch, then both down projections in another; below
+// kW4TcTokens tokens on the kernel for few tokens, with H in FP32, from there
+// on the tensor-core kernel, with H in BF16. The device status word is cleared
+// by the first launch if `clear` is set.
 static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E, int K, const int32_t *perm,
                               const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, void *h, void *y_perm,
-                              void *y_shared, int *status, cudaStream_t st)
+                              void *y_shared, int *status, bool clear, cudaStream_t st)
 {
+    const bool tc = N >= kW4TcTokens;
     W4Product a{};
     a.P = N * K;
     a.n_shared = s ? N : 0;
@@ -294,7 +302,7 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
     a.y_dtype = KMOE_BF16;
     W4Product b = a;
     a.x = x;
-    a.status = status;
+    a.status = clear ? status : nullptr;
     a.x_rows = N;
     a.perm = perm;
     a.rows = I;
@@ -307,9 +315,9 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
         a.up_shared = w4_ptrs(s[1]);
     }
     a.y = h;
-    KMOE_TRY(launch_w4(a, st));
+    KMOE_TRY(tc ? launch_w4_tc(a, status, wait_limit(), st) : launch_w4(a, st));
     b.x = h;
-    b.x_f32 = true;
+    b.x_f32 = !tc;
     b.x_rows = a.P + a.n_shared;
     b.x_by_row = true;
     b.rows = d;
@@ -319,7 +327,7 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
     if (s) b.w_shared = w4_ptrs(s[2]);
     b.y = y_perm;
     b.y_shared = y_shared;
-    return launch_w4(b, st);
+    return tc ? launch_w4_tc(b, status, wait_limit(), st) : launch_w4(b, st);
 }
 
 // `status` is the workspace status block: the status word, tickets, then
@@ -331,7 +339,7 @@ static kmoe_status run_ffn(const void *x, int x_dtype, int N, int d, int I, int 
     const int w_dtype = routed->dtype;
     if (w_dtype == KMOE_W4)
         return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm, offsets, routed->w4,
-                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, nullptr, st);
+                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, false, st);
     const ExpertPtrs r = ptrs(routed);
     ExpertPtrs sh{};
     if (shared) sh = ptrs(shared);
@@ -639,7 +647,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
     const FfnScratch f = take_ffn_scratch(c, N, d, K, I, routed->dtype);
     if (routed->dtype == KMOE_W4)   // these kernels clear the status word themselves: no memset in front of them
         return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm_token, offsets, routed->w4,
-                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, st);
+                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, true, st);
     KMOE_TRY(clear_status(status, st, kFfnStatusBytes));
     return run_ffn(x, x_dtype, N, d, I, E, K, perm_token, offsets, routed, shared, f, y_perm, y_shared, status, st);
 }
@@ -763,6 +771,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     a.group = w->group;
     a.y = y;
     a.y_dtype = y_dtype;
+    if (P >= kW4TcLin && N > 0) return launch_w4_tc(a, nullptr, wait_limit(), static_cast<cudaStream_t>(stream));
     return launch_w4(a, static_cast<cudaStream_t>(stream));
 }
 

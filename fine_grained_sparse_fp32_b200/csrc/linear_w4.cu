@@ -57,14 +57,6 @@ constexpr int kW4SmemMax = 226 * 1024;
 // Cost of a step by its tokens: what the CTAs' shares are cut by.
 __host__ __device__ constexpr int w4_cost(int tokens) { return 3 + (tokens + 1) / 2; }
 
-// Division by a number that the host knows: the high word of n * ceil(2^64 / d),
-// exact for n < 2^32 and 1 < d < 2^32.
-struct DivideBy {
-    unsigned long long m;     // 0 stands for d = 1
-    static DivideBy make(uint32_t d) { return {d > 1 ? ~0ull / d + 1 : 0}; }
-    __device__ __forceinline__ int operator()(int n) const { return m ? (int)__umul64hi((unsigned long long)(uint32_t)n, m) : n; }
-};
-
 struct W4Args {
     W4Product p;
     int tiles;              // units of one expert and token block
@@ -127,23 +119,6 @@ struct W4Tables {
     int *start, *count;                           // rows of every expert
 };
 
-// Rows [start, start + count) of group g (expert or shared expert), cut to the batch.
-__device__ __forceinline__ void group_rows(const W4Product &p, int g, int *start, int *count)
-{
-    if (g >= p.E) {
-        *start = p.P;
-        *count = p.n_shared;
-        return;
-    }
-    int a = 0, b = p.P;
-    if (p.offsets) {
-        a = max(p.offsets[g], 0);
-        b = min(p.offsets[g + 1], p.P);
-    }
-    *start = a;
-    *count = max(b - a, 0);
-}
-
 // Block-wide exclusive scan over threadIdx.x, of counts and costs at once.
 __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
 {
@@ -167,15 +142,6 @@ __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
     const long long before = incl - mine + (warp ? up : 0);
     *count = (int)(before & 0x3fffffff);
     *cost = before >> 30;
-}
-
-// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x).
-__device__ __forceinline__ int last_not_above(const int *v, int n, int x)
-{
-    int lo = 0;
-    for (int w = 1 << (31 - __clz(n)); w > 0; w >>= 1)
-        if (lo + w < n && v[lo + w] <= x) lo += w;
-    return lo;
 }
 
 // The unit (token block, numbered through all experts, and tile) at which share

@@ -51,10 +51,47 @@ struct W4Product {
     int y_dtype;
     int *status;                         // set to 0 (NULL: none)
 };
+// wait_limit: SM cycles before a pipeline wait of the tensor-core kernel gives
+// up and sets *err (the device status word; may be NULL) to 1.
 kmoe_status launch_w4(const W4Product &a, cudaStream_t st);
+kmoe_status launch_w4_tc(const W4Product &a, int *err, long long wait_limit, cudaStream_t st);
 
 // Routing by the rule of kmoe_routing. hist as in launch_topk.
 kmoe_status launch_route(const void *logits, int l_dtype, const float *bias, int N, int E, int K,
                          const kmoe_routing &r, int32_t *idx, float *w, cudaStream_t st, int32_t *hist = nullptr);
+
+// Division by a number that the host knows: the high word of n * ceil(2^64 / d),
+// exact for n < 2^32 and 1 < d < 2^32.
+struct DivideBy {
+    unsigned long long m;     // 0 stands for d = 1
+    static DivideBy make(uint32_t d) { return {d > 1 ? ~0ull / d + 1 : 0}; }
+    __device__ __forceinline__ int operator()(int n) const { return m ? (int)__umul64hi((unsigned long long)(uint32_t)n, m) : n; }
+};
+
+// Rows [start, start + count) of group g (expert or shared expert), cut to the batch.
+__device__ __forceinline__ void group_rows(const W4Product &p, int g, int *start, int *count)
+{
+    if (g >= p.E) {
+        *start = p.P;
+        *count = p.n_shared;
+        return;
+    }
+    int a = 0, b = p.P;
+    if (p.offsets) {
+        a = max(p.offsets[g], 0);
+        b = min(p.offsets[g + 1], p.P);
+    }
+    *start = a;
+    *count = max(b - a, 0);
+}
+
+// Largest j in [0, n) with v[j] <= x (v ascending, v[0] <= x).
+__device__ __forceinline__ int last_not_above(const int *v, int n, int x)
+{
+    int lo = 0;
+    for (int w = 1 << (31 - __clz(n)); w > 0; w >>= 1)
+        if (lo + w < n && v[lo + w] <= x) lo += w;
+    return lo;
+}
 
 }  // namespace kmoe
