@@ -21,9 +21,12 @@
 //                (warps 0-3 tile 0, 4-7 tile 1); SiLU(gate) * up or the output
 //   warps 8-15   unpack: 64 bytes of codes of a row and 128 columns into 64
 //                columns of tensor memory (8-11 tile 0, 12-15 tile 1)
-//   warp 16      loads: code tiles by TMA (64-byte swizzle: the unpackers' reads
-//                have no bank conflicts), token rows by TMA gather
-//   warp 17      one thread issues tcgen05.mma
+//   warp 16      loads code tiles by TMA (64-byte swizzle: the unpackers' reads
+//                have no bank conflicts)
+//   warp 17      issues tcgen05.mma
+//   warps 18-19  gather token rows with cp.async (a TMA gather of four rows
+//                costs its issuer 80 clocks: 32 of them for 64 tokens and 128
+//                columns bounded the kernel)
 // Tensor memory: sums 2 tiles x 2 buffers x 64 columns, unpacked weights
 // 2 tiles x 2 buffers x 64 columns.
 #include "sm100.cuh"
@@ -39,7 +42,7 @@ using namespace sm100;
 
 namespace w4tc {
 
-constexpr int kThreads = 18 * 32;
+constexpr int kThreads = 20 * 32;
 constexpr int kTokens = 64;                       // tokens of a unit
 constexpr int kRows = 128;                        // rows of an M tile
 constexpr int kCodeTile = kRows * 64;             // bytes of one tile's codes of a 128-column block
@@ -47,10 +50,11 @@ constexpr int kPanel = kTokens * 128;             // bytes of 64 columns of a to
 constexpr int kStages = 4;                        // 128-column blocks in flight: codes 16 KB, tokens 16 KB each
 constexpr int kMaxGroups = 1025;
 constexpr int kKnown = 2048;                      // token blocks whose expert is looked up in a table
-constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kGatherWarp = 18;
+constexpr int kGatherThreads = 64;
 
 struct Maps {
-    CUtensorMap w[2], w_shared[2], x;             // codes (gate, up with SwiGLU); x, one row high for the gather
+    CUtensorMap w[2], w_shared[2];                // codes (gate, up with SwiGLU)
 };
 
 struct Args {
@@ -127,6 +131,14 @@ __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
     __syncthreads();
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, BF16 inputs, FP32 accumulation.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
@@ -182,12 +194,13 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     Tail &T = *reinterpret_cast<Tail *>(toks + (size_t)kStages * 2 * kPanel);
     volatile int *abort = &T.abort;
     const W4Product &p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = p.cols / kW4Block;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // known to be uniform
+    const int lane = threadIdx.x & 31, blocks = p.cols / kW4Block;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&T.cfull[s], 1);
             mbar_init(&T.cempty[s], 8);           // one arrival per unpacking warp
-            mbar_init(&T.bfull[s], 1);
+            mbar_init(&T.bfull[s], kGatherThreads);
             mbar_init(&T.bempty[s], 1);
         }
         for (int c = 0; c < 2; ++c)
@@ -222,90 +235,122 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
 
     if (warp == kLoadWarp) {
         // ---------------------------------------------------------- loads
-        swp::fence_proxy_async_global();          // x (or H) may come from the kernel before
-        const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+        const uint64_t pol_w = policy_evict_first();
         uint32_t it = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
-            int idx[4];                           // x rows of tokens 4 lane .. + 3; row 0 for those that are not there
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 4 * lane + j;
-                int xi = -1;
-                if (i < U.n) {
-                    xi = U.row0 + i;
-                    if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
-                }
-                idx[j] = (unsigned)xi < (unsigned)p.x_rows ? xi : 0;
-            }
-            const int quads = (U.n + 3) / 4, r0 = kUp ? U.tile * kRows : U.tile * 2 * kRows;
-            const int y0 = (shared ? 0 : U.grp * p.rows) + r0, y1 = kUp ? y0 : y0 + kRows;
+            const int y0 = (shared ? 0 : U.grp * p.rows) + (kUp ? U.tile * kRows : U.tile * 2 * kRows);
+            const int y1 = kUp ? y0 : y0 + kRows;
             const CUtensorMap *m0 = shared ? &maps.w_shared[0] : &maps.w[0], *m1 = shared ? &maps.w_shared[1] : &maps.w[1];
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
-                const uint32_t par = ((it / kStages) & 1) ^ 1;
-                if (!all(wait(&T.cempty[s], par) && wait(&T.bempty[s], par))) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *C = codes + (size_t)s * 2 * kCodeTile, *B = toks + (size_t)s * 2 * kPanel;
-                if (lane == 0) {
+                ok = all(wait(&T.cempty[s], ((it / kStages) & 1) ^ 1));
+                if (!ok) break;
+                uint8_t *C = codes + (size_t)s * 2 * kCodeTile;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&T.cfull[s], 2 * kCodeTile);
                     tma_load_2d_hint(C, m0, &T.cfull[s], kb * 64, y0, pol_w);
                     tma_load_2d_hint(C + kCodeTile, m1, &T.cfull[s], kb * 64, y1, pol_w);
-                    mbar_arrive_expect_tx(&T.bfull[s], quads * 1024);
                 }
                 __syncwarp();
-                if (lane < quads)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tma_gather4_hint(B + h * kPanel + lane * 512, &maps.x, &T.bfull[s], kb * kW4Block + h * 64, idx[0],
-                                         idx[1], idx[2], idx[3], pol_x);
             }
         }
         if (!ok)                                  // let loads in flight land before the CTA exits
-            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
+            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
                 mbar_wait_drain(&T.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
-                mbar_wait_drain(&T.bfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
+    } else if (warp >= kGatherWarp) {
+        // --------------------------------------------------------- gather
+        // 16 threads take the 256 bytes of a row's 128 columns, 4 rows a pass.
+        const int th = threadIdx.x - kGatherWarp * 32, piece = th & 15;
+        const uint32_t panel = (uint32_t)(piece >> 3) * kPanel;
+        uint32_t it = 0;
+        bool ok = true;
+        auto landed = [&](uint32_t j) {           // this thread's copies of block j are in place: tell the MMA
+            fence_proxy_async();
+            mbar_arrive(&T.bfull[j % kStages]);
+        };
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+            const Unit U = unit_of(a, T, u);
+            const bool shared = U.grp >= p.E;
+            int row[kTokens / 4];                 // x rows; row 0 for tokens that are not there (their results are not used)
+#pragma unroll
+            for (int j = 0; j < kTokens / 4; ++j) {
+                const int i = 4 * j + (th >> 4);
+                int xi = 0;
+                if (i < U.n) {
+                    xi = U.row0 + i;
+                    if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
+                    if ((unsigned)xi >= (unsigned)p.x_rows) xi = 0;
+                }
+                row[j] = xi;
             }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            uint32_t it = 0, dn = 0;              // blocks; groups' sums per tile
-            bool ok = true;
-            for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-                const Unit U = unit_of(a, T, u);
-                const uint32_t idesc = idesc_bf16_f32(kRows, (U.n + 15) & ~15);
-                for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
-                    const int s = it % kStages, ab = it & 1;
-                    if (!wait(&T.bfull[s], (it / kStages) & 1)) { ok = false; break; }
-                    const uint32_t b0 = smem_u32(toks + (size_t)s * 2 * kPanel);
-                    const uint64_t bd[2] = {sw128_kmajor_desc(b0), sw128_kmajor_desc(b0 + kPanel)};
-                    for (int c = 0; c < 2 && ok; ++c) {
-                        if (!wait(&T.afull[c][ab], (it >> 1) & 1)) { ok = false; break; }
+            for (int kb = 0; kb < blocks; ++kb, ++it) {
+                const int s = it % kStages;
+                ok = all(wait(&T.bempty[s], ((it / kStages) & 1) ^ 1));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel;
+                const char *src = static_cast<const char *>(p.x) + kb * (kW4Block * 2) + piece * 16;
 #pragma unroll
-                        for (int gi = 0; gi < GB; ++gi) {
-                            const uint32_t d = dn + gi;
-                            if (ok && !wait(&T.dempty[c][d & 1], ((d >> 1) & 1) ^ 1)) ok = false;
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = gi * (G / 16); k < (gi + 1) * (G / 16); ++k)
-                                umma_bf16_ts(tmem + d_col(c, d & 1), tmem + a_col(c, ab) + k * 8, bd[k >> 2] + (uint64_t)((k & 3) * 2),
-                                             idesc, k != gi * (G / 16));
-                            umma_commit(&T.dfull[c][d & 1]);
-                        }
-                        if (ok) umma_commit(&T.aempty[c][ab]);
-                    }
-                    if (ok) umma_commit(&T.bempty[s]);
-                    dn += GB;
+                for (int j = 0; j < kTokens / 4; ++j) {
+                    const int i = 4 * j + (th >> 4);
+                    if (4 * j < U.n)
+                        cp_async16(dst + i * 128 + (((piece & 7) ^ (i & 7)) << 4), src + (size_t)row[j] * (p.cols * 2), 16);
+                }
+                cp_async_commit();
+                if (it > 0) {                     // one block behind, so that copies overlap
+                    cp_async_wait<1>();
+                    landed(it - 1);
                 }
             }
-            umma_commit(&T.drain);                // every MMA done before tensor memory is released
-            mbar_wait_drain(&T.drain, 0, kDefaultWaitLimit);
         }
+        cp_async_wait_all();
+        if (it > 0) landed(it - 1);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA
+        // The whole warp walks; one elected lane issues. Kept converged, the
+        // descriptors live in uniform registers and an MMA costs 11 clocks at 16
+        // tokens; issued under `lane == 0` each took 170.
+        uint32_t it = 0, dn = 0;                  // blocks; groups' sums per tile
+        bool ok = true;
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+            const Unit U = unit_of(a, T, u);
+            const uint32_t idesc = idesc_bf16_f32(kRows, (U.n + 15) & ~15);
+            for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
+                const int s = it % kStages, ab = it & 1;
+                ok = all(wait(&T.bfull[s], (it / kStages) & 1));
+                const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
+                const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    ok = ok && all(wait(&T.afull[c][ab], (it >> 1) & 1));
+#pragma unroll
+                    for (int gi = 0; gi < GB; ++gi) {
+                        const uint32_t d = dn + gi;
+                        ok = ok && all(wait(&T.dempty[c][d & 1], ((d >> 1) & 1) ^ 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t dt = tmem + d_col(c, d & 1), at = tmem + a_col(c, ab);
+#pragma unroll
+                            for (int k = gi * (G / 16); k < (gi + 1) * (G / 16); ++k)
+                                umma_bf16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc,
+                                             k != gi * (G / 16));
+                            umma_commit(&T.dfull[c][d & 1]);
+                            if (gi + 1 == GB) umma_commit(&T.aempty[c][ab]);
+                            if (gi + 1 == GB && c == 1) umma_commit(&T.bempty[s]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                dn += GB;
+            }
+        }
+        if (elect_one()) umma_commit(&T.drain);   // every MMA done before tensor memory is released
+        __syncwarp();
+        mbar_wait_drain(&T.drain, 0, kDefaultWaitLimit);
         __syncwarp();
     } else if (warp >= 8) {
         // --------------------------------------------------------- unpack
@@ -474,17 +519,19 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-static bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t rows, uint64_t cols, int elem,
-                     uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
+// Codes [rows, bytes] as boxes of 128 rows x 64 bytes, 64-byte swizzle; rows
+// behind the last read as zeros.
+static bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t bytes)
 {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * elem};
-    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint64_t dims[2] = {bytes, rows};
+    cuuint64_t strides[1] = {bytes};
+    cuuint32_t box[2] = {64, kRows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kUp, int G, bool kZeros, class YT>
@@ -524,15 +571,13 @@ kmoe_status launch_w4_tc(const W4Product &p, int *err, long long wait_limit, cud
     Maps m{};
     const uint64_t bytes = (uint64_t)p.cols / 2;
     auto codes = [&](CUtensorMap *map, const W4Ptrs &w, uint64_t rows) {
-        return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.q, rows, bytes, 1, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B);
+        return make_map(map, w.q, rows, bytes);
     };
     const bool shared = p.n_shared > 0;
     const uint64_t all_rows = (uint64_t)p.E * p.rows;
     const W4Ptrs &w1 = up ? p.up : p.w, &s0 = shared ? p.w_shared : p.w, &s1 = shared ? (up ? p.up_shared : p.w_shared) : w1;
     const bool ok = codes(&m.w[0], p.w, all_rows) && codes(&m.w[1], w1, all_rows) && codes(&m.w_shared[0], s0, p.rows) &&
-                    codes(&m.w_shared[1], s1, p.rows) &&
-                    make_map(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, p.x_rows, p.cols, 2, 64, 1,
-                             CU_TENSOR_MAP_SWIZZLE_128B);
+                    codes(&m.w_shared[1], s1, p.rows);
     if (!ok) return fail(KMOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
