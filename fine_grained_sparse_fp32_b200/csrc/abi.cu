@@ -74,10 +74,6 @@ static kmoe_status check_act_dtype(int t, const char *name)
     return KMOE_OK;
 }
 
-// From this many tokens 4-bit experts run on the tensor-core kernel.
-static const int kW4TcTokens = getenv("W4TC") ? atoi(getenv("W4TC")) : 128;
-static const int kW4TcLin = getenv("W4TCL") ? atoi(getenv("W4TCL")) : 64;
-
 // E4M3 weights with FP32 128 x 128 block scales (BF16 or FP8 activations).
 static bool fp8_weights(int w_dtype) { return w_dtype == KMOE_E4M3_B128 || w_dtype == KMOE_E4M3_B128_A8; }
 
@@ -190,10 +186,16 @@ static size_t h_bytes(int w_dtype)
 // (BF16-precision) activations: below kTcMinTokens tokens.
 static bool two_term(int w_dtype, int N) { return w_dtype == KMOE_E4M3_B128 && N < kTcMinTokens; }
 
+// From this many tokens 4-bit experts run on the tensor-core kernel.
+static const int kW4TcTokens = getenv("W4TC") ? atoi(getenv("W4TC")) : 128;
+static const int kW4TcLin = getenv("W4TCL") ? atoi(getenv("W4TCL")) : 64;
+
 // The grouped FFN's scratch after the status block: H [N*K + N, I] and, with
 // FP8 activations, H's scales [N*K + N, I / 128], x's codes [N, d] and x's
 // scales [N, d / 128]. In two-term mode H's two bytes per element are its
 // high and low code planes (each [N*K + N, I]) and x has low codes as well.
+// 4-bit weights on the tensor cores: H in FP32, x in FP16 in xq, and a power of
+// two for every row of both in xs and hs.
 struct FfnScratch {
     void *h;
     float *hs;
@@ -212,8 +214,17 @@ static FfnScratch take_ffn_scratch(Carver &c, int N, int d, int K, int I, int w_
         if (two_term(w_dtype, N)) f.xl = c.take<uint8_t>((size_t)N * d);
         f.xs = c.take<float>((size_t)N * (d / 128));
     }
+    if (w_dtype == KMOE_W4 && N >= kW4TcTokens) {
+        f.hs = c.take<float>(R);
+        f.xq = c.take<uint8_t>((size_t)N * d * 2);
+        f.xs = c.take<float>(N);
+    }
     return f;
 }
+
+// Rows of BF16 products from which moe_linear_w4 takes the tensor-core kernel
+// (its FP16 weights are not exact enough for FP32 results).
+static bool linear_w4_tc(int N, int P, int y_dtype) { return y_dtype == KMOE_BF16 && P >= kW4TcLin && N > 0; }
 
 // Bytes of a moe_grouped_ffn workspace: the status block, then the scratch.
 static size_t ffn_ws_bytes(int N, int d, int K, int I, int w_dtype)
@@ -285,12 +296,12 @@ static FfnPath ffn_path(int x_dtype, int w_dtype, int N, int d)
 }
 
 // Grouped FFN with 4-bit weights: H = SiLU(W_g x) * (W_u x) for routed and
-// shared rows in one launch, then both down projections in another; below
-// kW4TcTokens tokens on the kernel for few tokens, with H in FP32, from there
-// on the tensor-core kernel, with H in BF16. The device status word is cleared
-// by the first launch if `clear` is set.
+// shared rows in one launch, then both down projections in another, H in FP32;
+// below kW4TcTokens tokens on the kernel for few tokens, from there on the
+// tensor-core kernel. The device status word is cleared by the first launch if
+// `clear` is set.
 static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E, int K, const int32_t *perm,
-                              const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, void *h, void *y_perm,
+                              const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, const FfnScratch &f, void *y_perm,
                               void *y_shared, int *status, bool clear, cudaStream_t st)
 {
     const bool tc = N >= kW4TcTokens;
@@ -314,10 +325,10 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
         a.w_shared = w4_ptrs(s[0]);
         a.up_shared = w4_ptrs(s[1]);
     }
-    a.y = h;
-    KMOE_TRY(tc ? launch_w4_tc(a, status, wait_limit(), st) : launch_w4(a, st));
-    b.x = h;
-    b.x_f32 = !tc;
+    a.y = f.h;
+    KMOE_TRY(tc ? launch_w4_tc(a, f.xq, f.xs, status, wait_limit(), st) : launch_w4(a, st));
+    b.x = f.h;
+    b.x_f32 = true;
     b.x_rows = a.P + a.n_shared;
     b.x_by_row = true;
     b.rows = d;
@@ -327,7 +338,7 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
     if (s) b.w_shared = w4_ptrs(s[2]);
     b.y = y_perm;
     b.y_shared = y_shared;
-    return tc ? launch_w4_tc(b, status, wait_limit(), st) : launch_w4(b, st);
+    return tc ? launch_w4_tc(b, f.h, f.hs, status, wait_limit(), st) : launch_w4(b, st);
 }
 
 // `status` is the workspace status block: the status word, tickets, then
@@ -339,7 +350,7 @@ static kmoe_status run_ffn(const void *x, int x_dtype, int N, int d, int I, int 
     const int w_dtype = routed->dtype;
     if (w_dtype == KMOE_W4)
         return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm, offsets, routed->w4,
-                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, false, st);
+                          shared ? shared->w4 : nullptr, f, y_perm, y_shared, status, false, st);
     const ExpertPtrs r = ptrs(routed);
     ExpertPtrs sh{};
     if (shared) sh = ptrs(shared);
@@ -647,7 +658,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
     const FfnScratch f = take_ffn_scratch(c, N, d, K, I, routed->dtype);
     if (routed->dtype == KMOE_W4)   // these kernels clear the status word themselves: no memset in front of them
         return run_ffn_w4(static_cast<const __nv_bfloat16 *>(x), N, d, I, E, K, perm_token, offsets, routed->w4,
-                          shared ? shared->w4 : nullptr, f.h, y_perm, y_shared, status, true, st);
+                          shared ? shared->w4 : nullptr, f, y_perm, y_shared, status, true, st);
     KMOE_TRY(clear_status(status, st, kFfnStatusBytes));
     return run_ffn(x, x_dtype, N, d, I, E, K, perm_token, offsets, routed, shared, f, y_perm, y_shared, status, st);
 }
@@ -737,9 +748,18 @@ kmoe_status moe_route(const void *logits, int l_dtype, const float *bias, int N,
     return launch_route(logits, l_dtype, bias, N, E, K, *routing, topk_idx, topk_w, static_cast<cudaStream_t>(stream));
 }
 
+size_t moe_linear_w4_workspace_size(int N, int P, int cols, int y_dtype)
+{
+    if (N < 0 || P < 0 || cols < 128 || cols % 128 || !linear_w4_tc(N, P, y_dtype)) return 0;
+    Carver c(nullptr);
+    c.take<uint8_t>((size_t)N * cols * 2);
+    c.take<float>(N);
+    return c.used;
+}
+
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w, void *y, int y_dtype,
-                          void *stream)
+                          void *ws, size_t ws_bytes, void *stream)
 {
     clear_error();
     if (x_dtype != KMOE_BF16) return fail(KMOE_ERR_UNSUPPORTED, "4-bit weights: x must be BF16");
@@ -758,6 +778,9 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     KMOE_TRY(check_ptr(perm_token, "perm_token", true));
     KMOE_TRY(check_ptr(offsets, "offsets", true));
     KMOE_TRY(check_ptr(y, "y"));
+    const size_t need = moe_linear_w4_workspace_size(N, P, cols, y_dtype);
+    if (need) KMOE_TRY(check_ptr(ws, "ws"));
+    if (ws_bytes < need) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     W4Product a{};
     a.x = x;
     a.x_rows = N;
@@ -771,7 +794,11 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     a.group = w->group;
     a.y = y;
     a.y_dtype = y_dtype;
-    if (P >= kW4TcLin && N > 0) return launch_w4_tc(a, nullptr, wait_limit(), static_cast<cudaStream_t>(stream));
+    if (linear_w4_tc(N, P, y_dtype)) {
+        Carver c(ws);
+        void *x16 = c.take<uint8_t>((size_t)N * cols * 2);
+        return launch_w4_tc(a, x16, c.take<float>(N), nullptr, wait_limit(), static_cast<cudaStream_t>(stream));
+    }
     return launch_w4(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -1,38 +1,38 @@
 // Products with 4-bit weights on the 5th-generation tensor cores, for batches
-// whose experts see several tokens (linear_w4.cu is the kernel for few).
+// whose experts see many tokens (linear_w4.cu is the kernel for few).
 //
-//   y[p][r] = sum_G s[r][G] * ( sum_{c in G} (q[r][c] - z[r][G]) x[p][c] )
-// Weights are the M operand (128 rows), tokens the N operand (up to 64). A
-// code minus its zero point is a whole number below 16 in magnitude, exact in
-// BF16, so the weights are never rounded: the tensor cores sum one group's
-// products of BF16 codes and BF16 x in FP32, and the group scale, which belongs
-// to a row and so to one thread's lane of tensor memory, multiplies that sum as
-// it is added up in registers.
+//   y[p][r] = sum_c (q[r][c] - z[r][c / group]) s[r][c / group] x[p][c]
+// Weights are the M operand (128 rows), tokens the N operand (up to 128), both
+// in FP16 with FP32 sums. With powers of two taken out, FP16 holds more of both
+// than BF16 would: 2^-a times x, a from the largest value of its row, is exact
+// for every BF16 x within 2^30 of that value, and (q - z) times the row's
+// scale over the power of two below its largest scale is rounded to 2^-12 of
+// the weight (a BF16 weight would be off by 2^-9, the rounding of the result).
+// The powers of two come back in FP32 with the sums.
 //
-// Unpacking bounds this kernel (1.4 instructions a weight on the integer pipe),
-// so a CTA unpacks a weight once for up to 64 tokens, and unpacked weights take
-// no shared-memory bandwidth: the unpacking threads write them straight into
+// Unpacking bounds this kernel (13 instructions for 8 weights), so a weight is
+// unpacked once for up to 128 tokens, scale included, and the sums stay in
+// tensor memory for a unit's whole depth; and unpacked weights take no
+// shared-memory bandwidth: the unpacking threads write them straight into
 // tensor memory, from where the MMA reads its A operand. A unit is two M tiles
 // (256 rows of one expert, or 128 gate and the same 128 up features) and a
-// block of tokens; the tiles' phases alternate, so one is unpacked and added up
-// while the MMA works on the other. Units are dealt to the CTAs (one per SM)
-// in turn.
-//   warps 0-7    add up: tcgen05.ld of a group's sums, times the scale
-//                (warps 0-3 tile 0, 4-7 tile 1); SiLU(gate) * up or the output
+// block of tokens. Units are dealt to the CTAs (one per SM) in turn.
+//   warps 0-7    results: sums from tensor memory, SiLU(gate) * up or y (warps
+//                0-3 and 4-7 take turns in 16-token steps)
 //   warps 8-15   unpack: 64 bytes of codes of a row and 128 columns into 64
 //                columns of tensor memory (8-11 tile 0, 12-15 tile 1)
 //   warp 16      loads code tiles by TMA (64-byte swizzle: the unpackers' reads
 //                have no bank conflicts)
 //   warp 17      issues tcgen05.mma
 //   warps 18-19  gather token rows with cp.async (a TMA gather of four rows
-//                costs its issuer 80 clocks: 32 of them for 64 tokens and 128
-//                columns bounded the kernel)
-// Tensor memory: sums 2 tiles x 2 buffers x 64 columns, unpacked weights
-// 2 tiles x 2 buffers x 64 columns.
+//                costs its issuer 80 clocks, too much for 64 tokens)
+// Tensor memory: sums 2 tiles x 2 slots x 64 columns (a unit of more than 64
+// tokens takes both slots), unpacked weights 2 tiles x 2 buffers x 64 columns.
 #include "sm100.cuh"
 #include "swap_units.cuh"
 #include "w4.cuh"
 
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -43,11 +43,11 @@ using namespace sm100;
 namespace w4tc {
 
 constexpr int kThreads = 20 * 32;
-constexpr int kTokens = 64;                       // tokens of a unit
+constexpr int kTokens = 128;                      // tokens of a unit
 constexpr int kRows = 128;                        // rows of an M tile
 constexpr int kCodeTile = kRows * 64;             // bytes of one tile's codes of a 128-column block
 constexpr int kPanel = kTokens * 128;             // bytes of 64 columns of a token block
-constexpr int kStages = 4;                        // 128-column blocks in flight: codes 16 KB, tokens 16 KB each
+constexpr int kStages = 4;                        // 128-column blocks in flight: codes 16 KB, tokens 32 KB each
 constexpr int kMaxGroups = 1025;
 constexpr int kKnown = 2048;                      // token blocks whose expert is looked up in a table
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kGatherWarp = 18;
@@ -61,19 +61,52 @@ struct Args {
     W4Product p;
     int tiles, groups;                            // units of a token block; experts, the shared one included
     DivideBy by_tiles;
+    const void *x16;                              // x in FP16, rows x_pitch bytes apart
+    size_t x_pitch;
+    const float *x_scale;                         // its rows' powers of two
     int *err;
     long long wait_limit;
 };
 
 struct Tail {
     uint64_t cfull[kStages], cempty[kStages], bfull[kStages], bempty[kStages];
-    uint64_t afull[2][2], aempty[2][2], dfull[2][2], dempty[2][2], up_full, up_empty, drain;
+    uint64_t afull[2][2], aempty[2][2], dfull[2], dempty[2], drain;    // d: both tiles' sums in a slot
     uint32_t tmem_base;
     int abort, total;
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
+
+// mbar_wait by a whole warp: true in every lane, or false in every lane. Past
+// the first look the warp is suspended for up to 20 us at a time.
+__device__ __forceinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, long long limit)
+{
+    const long long t0 = clock64();
+    bool done = false, give_up = false;
+    while (!done && !give_up) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+            : "memory");
+        done = ok != 0;
+        if (!done && clock64() - t0 > limit) {
+            *abort = 1;
+            if (err) atomicCAS(err, kErrNone, kErrWaitTimeout);
+        }
+        give_up = !done && *abort;
+    }
+    return __all_sync(0xffffffffu, done);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, long long limit)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_slowly(bar, parity, abort, err, limit);
+}
 
 struct Unit {
     int grp, row0, n, tile;
@@ -86,7 +119,7 @@ __device__ __forceinline__ Unit unit_of(const Args &a, const Tail &T, int u)
     return {g, T.start[g] + first, min(T.size[g], T.count[g] - first), u - tb * a.tiles};
 }
 
-// Tokens of a block of a group with `count` rows: equal blocks of at most 64.
+// Tokens of a block of a group with `count` rows: equal blocks of at most 128.
 __device__ __forceinline__ int block_size(int count)
 {
     const int n = (count + kTokens - 1) / kTokens;
@@ -139,8 +172,8 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, BF16 inputs, FP32 accumulation.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+// D[tmem] (+)= A[tmem] * B[smem]^T, FP16 inputs, FP32 accumulation.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -161,18 +194,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// {128 + z, 128 + z} in BF16 (the low mantissa bits of 128.0 count ones).
-__device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z)
+// Instruction descriptor: FP16 A and B (both K-major), FP32 sums, M x N tile.
+__device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N)
 {
-    const uint32_t v = (0x4300u | z) * 0x00010001u;
-    return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// Columns 2i, 2i + 1 of a word as BF16 q - z: 128 + q (the code as mantissa
-// bits), minus 128 + z; exact.
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, __nv_bfloat162 zz)
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
+__device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// The eight columns of a word as FP16 weights, in column order. A code in the
+// low mantissa bits of 1024.0 counts ones, four bits further up sixteens: so
+// one shift serves the word. Codes minus zero points are exact, the product
+// with the scale is rounded.
+// z1 = -(1024 + z), z16 = -(64 + z), both twice; s = scale, twice.
+__device__ __forceinline__ void unpack_word(uint32_t word, __half2 z1, __half2 z16, __half2 s, uint32_t *out)
 {
-    const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    return as_u32(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), zz));
+    const __half2 sixteenth = as_half2(0x2c002c00u);
+    const uint32_t up = word >> 8;
+    out[0] = half2_bits(__hmul2(__hadd2(as_half2((word & 0x000f000fu) | 0x64006400u), z1), s));
+    out[1] = half2_bits(__hmul2(__hfma2(as_half2((word & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
+    out[2] = half2_bits(__hmul2(__hadd2(as_half2((up & 0x000f000fu) | 0x64006400u), z1), s));
+    out[3] = half2_bits(__hmul2(__hfma2(as_half2((up & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
+}
+
+// Exponent field of the largest magnitude among n scales (n a multiple of 2 at
+// a 4-byte boundary, or any n).
+__device__ __forceinline__ uint32_t scale_exponent(const __nv_bfloat16 *s, int n)
+{
+    uint32_t top = 0;
+    const uint16_t *v = reinterpret_cast<const uint16_t *>(s);
+    for (int i = 0; i < n; ++i) top = max(top, (uint32_t)(v[i] & 0x7fffu));
+    return max(top >> 7, 1u);
 }
 
 // This thread's row of M tile c of a unit, and its matrix.
@@ -183,9 +236,28 @@ __device__ __forceinline__ size_t tile_row(const Args &a, const Unit &u, int c, 
     return (u.grp >= a.p.E ? 0 : (size_t)u.grp * a.p.rows) + min(r, a.p.rows - 1);
 }
 
+// Tensor memory: sums of tile c in a slot, unpacked weights of tile c in a buffer.
+__device__ __forceinline__ uint32_t d_col(int c, int slot) { return c * 128 + slot * 64; }
+__device__ __forceinline__ uint32_t a_col(int c, int b) { return 256 + c * 128 + b * 64; }
+
+// Slots that units take in turn: a unit of up to 64 tokens takes the next one,
+// a larger one both. `phase` holds, for each slot, the parity of its uses.
+struct Slots {
+    uint32_t phase = 0;
+    int next = 0, first = 0, n = 1;
+    __device__ __forceinline__ void take(int tokens)
+    {
+        n = tokens > 64 ? 2 : 1;
+        first = n == 2 ? 0 : next;
+        if (n == 1) next ^= 1;
+    }
+    __device__ __forceinline__ uint32_t parity(int slot) const { return (phase >> slot) & 1; }
+    __device__ __forceinline__ void done() { phase ^= n == 2 ? 3u : 1u << first; }
+};
+
 template <bool kUp, int G, bool kZeros, class YT>
 __global__ void __launch_bounds__(kThreads, 1)
-kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
+w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
 {
     constexpr int GB = kW4Block / G;
     extern __shared__ uint8_t smem_raw[];
@@ -207,11 +279,11 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&T.afull[c][b], 4);
                 mbar_init(&T.aempty[c][b], 1);
-                mbar_init(&T.dfull[c][b], 1);
-                mbar_init(&T.dempty[c][b], 4);
             }
-        mbar_init(&T.up_full, 4);
-        mbar_init(&T.up_empty, 4);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&T.dfull[b], 1);
+            mbar_init(&T.dempty[b], 8);           // one arrival per result warp
+        }
         mbar_init(&T.drain, 1);
         T.abort = 0;
         fence_mbar_init();
@@ -228,10 +300,7 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     tc_fence_after();
     const int total = T.total;
     const uint32_t tmem = T.tmem_base;
-    auto all = [](bool ok) { return __all_sync(0xffffffffu, ok); };
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort, a.err, a.wait_limit); };
-    auto d_col = [](int c, int b) { return (uint32_t)(c * 128 + b * 64); };
-    auto a_col = [](int c, int b) { return (uint32_t)(256 + c * 128 + b * 64); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort, a.err, a.wait_limit); };
 
     if (warp == kLoadWarp) {
         // ---------------------------------------------------------- loads
@@ -246,7 +315,7 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const CUtensorMap *m0 = shared ? &maps.w_shared[0] : &maps.w[0], *m1 = shared ? &maps.w_shared[1] : &maps.w[1];
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
-                ok = all(wait(&T.cempty[s], ((it / kStages) & 1) ^ 1));
+                ok = wait(&T.cempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
                 uint8_t *C = codes + (size_t)s * 2 * kCodeTile;
                 if (elect_one()) {
@@ -288,15 +357,15 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             }
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
-                ok = all(wait(&T.bempty[s], ((it / kStages) & 1) ^ 1));
+                ok = wait(&T.bempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
                 const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel;
-                const char *src = static_cast<const char *>(p.x) + kb * (kW4Block * 2) + piece * 16;
+                const char *src = static_cast<const char *>(a.x16) + kb * (kW4Block * 2) + piece * 16;
 #pragma unroll
                 for (int j = 0; j < kTokens / 4; ++j) {
                     const int i = 4 * j + (th >> 4);
-                    if (4 * j < U.n)
-                        cp_async16(dst + i * 128 + (((piece & 7) ^ (i & 7)) << 4), src + (size_t)row[j] * (p.cols * 2), 16);
+                    if (4 * j >= U.n) break;
+                    cp_async16(dst + i * 128 + (((piece & 7) ^ (i & 7)) << 4), src + (size_t)row[j] * a.x_pitch, 16);
                 }
                 cp_async_commit();
                 if (it > 0) {                     // one block behind, so that copies overlap
@@ -312,41 +381,40 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         // The whole warp walks; one elected lane issues. Kept converged, the
         // descriptors live in uniform registers and an MMA costs 11 clocks at 16
         // tokens; issued under `lane == 0` each took 170.
-        uint32_t it = 0, dn = 0;                  // blocks; groups' sums per tile
+        uint32_t it = 0;
+        Slots sl;
         bool ok = true;
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
-            const uint32_t idesc = idesc_bf16_f32(kRows, (U.n + 15) & ~15);
+            const uint32_t idesc = idesc_f16_f32(kRows, (U.n + 15) & ~15);
+            sl.take(U.n);
+            for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dempty[sl.first + k], sl.parity(sl.first + k) ^ 1);
             for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
                 const int s = it % kStages, ab = it & 1;
-                ok = all(wait(&T.bfull[s], (it / kStages) & 1));
+                ok = wait(&T.bfull[s], (it / kStages) & 1);
                 const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
                 const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    ok = ok && all(wait(&T.afull[c][ab], (it >> 1) & 1));
-#pragma unroll
-                    for (int gi = 0; gi < GB; ++gi) {
-                        const uint32_t d = dn + gi;
-                        ok = ok && all(wait(&T.dempty[c][d & 1], ((d >> 1) & 1) ^ 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint32_t dt = tmem + d_col(c, d & 1), at = tmem + a_col(c, ab);
-#pragma unroll
-                            for (int k = gi * (G / 16); k < (gi + 1) * (G / 16); ++k)
-                                umma_bf16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc,
-                                             k != gi * (G / 16));
-                            umma_commit(&T.dfull[c][d & 1]);
-                            if (gi + 1 == GB) umma_commit(&T.aempty[c][ab]);
-                            if (gi + 1 == GB && c == 1) umma_commit(&T.bempty[s]);
-                        }
-                        __syncwarp();
-                    }
+                    ok = ok && wait(&T.afull[c][ab], (it >> 1) & 1);
                     if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t dt = tmem + d_col(c, sl.first), at = tmem + a_col(c, ab);
+#pragma unroll
+                        for (int k = 0; k < kW4Block / 16; ++k)
+                            umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
+                        umma_commit(&T.aempty[c][ab]);
+                        if (c == 1) umma_commit(&T.bempty[s]);
+                        if (c == 1 && kb + 1 == blocks) {
+                            umma_commit(&T.dfull[sl.first]);
+                            if (sl.n == 2) umma_commit(&T.dfull[1]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                dn += GB;
             }
+            sl.done();
         }
         if (elect_one()) umma_commit(&T.drain);   // every MMA done before tensor memory is released
         __syncwarp();
@@ -354,40 +422,54 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         __syncwarp();
     } else if (warp >= 8) {
         // --------------------------------------------------------- unpack
-        const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
+        const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         uint32_t it = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
-            const uint8_t *zr = nullptr;
-            if (kZeros) {
-                const bool shared = U.grp >= p.E;
-                const uint8_t *z = kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z);
-                zr = z + tile_row<kUp>(a, U, c, row) * (p.cols / G);
-            }
-            for (int kb = 0; kb < blocks; ++kb, ++it) {
-                const int s = it % kStages, ab = it & 1;
-                uint32_t z = 0x08080808u;
+            const bool shared = U.grp >= p.E;
+            const size_t at = tile_row<kUp>(a, U, c, row) * gpr;
+            const __nv_bfloat16 *sc = (kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at;
+            const uint8_t *zr = kZeros ? (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at : nullptr;
+            // scales over the power of two below the row's largest: 2^(127 - field) as FP32
+            const float over = __uint_as_float((254u - min(scale_exponent(sc, gpr), 253u)) << 23);
+            __nv_bfloat16 s_next[GB];             // loaded one block ahead
+            uint32_t z_next = 0x08080808u;
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int gi = 0; gi < GB; ++gi) s_next[gi] = sc[kb * GB + gi];
                 if (kZeros) {
-                    const uint8_t *at = zr + kb * GB;
-                    z = GB == 1 ? *at : GB == 2 ? *reinterpret_cast<const uint16_t *>(at) : *reinterpret_cast<const uint32_t *>(at);
+                    const uint8_t *z = zr + kb * GB;
+                    z_next = GB == 1 ? *z : GB == 2 ? *reinterpret_cast<const uint16_t *>(z) : *reinterpret_cast<const uint32_t *>(z);
                 }
-                if (!all(wait(&T.cfull[s], (it / kStages) & 1))) { ok = false; break; }
-                const uint8_t *src = codes + (size_t)s * 2 * kCodeTile + c * kCodeTile + row * 64;
+            };
+            fetch(0);
+            for (int kb = 0; kb < blocks; ++kb, ++it) {
+                const int st = it % kStages, ab = it & 1;
+                __half2 s[GB];
+#pragma unroll
+                for (int gi = 0; gi < GB; ++gi) s[gi] = __float2half2_rn(__bfloat162float(s_next[gi]) * over);
+                const uint32_t z = z_next;
+                if (kb + 1 < blocks) fetch(kb + 1);
+                ok = wait(&T.cfull[st], (it / kStages) & 1);
+                if (!ok) break;
+                const uint8_t *src = codes + (size_t)st * 2 * kCodeTile + c * kCodeTile + row * 64;
                 uint4 w[4];                       // w[t]: words of columns 8t of each 32-column slice
 #pragma unroll
                 for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint4 *>(src + ((t ^ ((row >> 1) & 3)) << 4));
-                if (!all(wait(&T.aempty[c][ab], ((it >> 1) & 1) ^ 1))) { ok = false; break; }
+                ok = wait(&T.aempty[c][ab], ((it >> 1) & 1) ^ 1);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {  // 32 columns: 16 columns of tensor memory
-                    const __nv_bfloat162 zz = zero_pair((z >> (8 * (jj / (G / 32)))) & 15u);
+                    const int gi = jj / (G / 32);
+                    const uint32_t zi = kZeros ? (z >> (8 * gi)) & 15u : 8u;
+                    const __half2 z1 = as_half2((0xe400u | zi) * 0x00010001u);             // -(1024 + z)
+                    const __half2 z16 = as_half2((0xd400u | zi << 4) * 0x00010001u);       // -(64 + z)
                     uint32_t r[16];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[4 * t + i] = code_pair(word_of(w[t], jj), i, zz);
+                    for (int t = 0; t < 4; ++t) unpack_word(word_of(w[t], jj), z1, z16, s[gi], r + 4 * t);
                     tmem_st16(tmem + lanes + a_col(c, ab) + jj * 16, r);
                 }
                 tmem_st_wait();
@@ -395,106 +477,73 @@ kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&T.afull[c][ab]);
-                    mbar_arrive(&T.cempty[s]);
+                    mbar_arrive(&T.cempty[st]);
                 }
             }
         }
     } else {
-        // --------------------------------------------------------- add up
-        const int c = warp >> 2, row = (warp & 3) * 32 + lane;
+        // -------------------------------------------------------- results
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        uint32_t dn = 0, un = 0;
+        Slots sl;
         bool ok = true;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++un) {
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
-            const __nv_bfloat16 *sc = kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s);
-            sc += tile_row<kUp>(a, U, c, row) * (p.cols / G);
-            float acc[kTokens];
+            sl.take(U.n);
+            // the rows' powers of two, and the tokens'
+            float row_scale[2];
 #pragma unroll
-            for (int i = 0; i < kTokens; ++i) acc[i] = 0.f;
-            __nv_bfloat16 nxt[GB];                // scales of the next block, loaded one block ahead
+            for (int c = 0; c < 2; ++c) {
+                const __nv_bfloat16 *sc = kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s);
+                row_scale[c] = __uint_as_float(min(scale_exponent(sc + tile_row<kUp>(a, U, c, row) * gpr, gpr), 253u) << 23);
+            }
+            float tok[kTokens / 32];              // of tokens lane + 32 j; 0 for one that is not there
 #pragma unroll
-            for (int gi = 0; gi < GB; ++gi) nxt[gi] = sc[gi];
-            for (int kb = 0; kb < blocks && ok; ++kb) {
-                float s[GB];
-#pragma unroll
-                for (int gi = 0; gi < GB; ++gi) s[gi] = __bfloat162float(nxt[gi]);
-                if (kb + 1 < blocks)
-#pragma unroll
-                    for (int gi = 0; gi < GB; ++gi) nxt[gi] = sc[(kb + 1) * GB + gi];
-#pragma unroll
-                for (int gi = 0; gi < GB; ++gi, ++dn) {
-                    if (ok && !all(wait(&T.dfull[c][dn & 1], (dn >> 1) & 1))) ok = false;
-                    if (!ok) continue;
-                    tc_fence_after();
-                    const uint32_t d = tmem + lanes + d_col(c, dn & 1);
-#pragma unroll
-                    for (int q = 0; q < kTokens / 16; ++q)
-                        if (q * 16 < U.n) {
-                            uint32_t v[16];
-                            tmem_ld16(d + q * 16, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[q * 16 + i] = fmaf(s[gi], __uint_as_float(v[i]), acc[q * 16 + i]);
-                        }
-                    // the up tile's last sums stay: their place takes the up values
-                    if (kUp && c && kb + 1 == blocks && gi + 1 == GB) continue;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&T.dempty[c][dn & 1]);
+            for (int j = 0; j < kTokens / 32; ++j) {
+                const int i = lane + 32 * j;
+                int xi = -1;
+                if (i < U.n) {
+                    xi = U.row0 + i;
+                    if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
                 }
+                tok[j] = (unsigned)xi < (unsigned)p.x_rows ? a.x_scale[xi] : 0.f;
             }
+            for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dfull[sl.first + k], sl.parity(sl.first + k));
             if (!ok) break;
-            const int last = (dn - 1) & 1;
-            if (kUp && c) {                       // up values to the gates' warps, in the same lanes of tensor memory
-                if (!all(wait(&T.up_empty, (un & 1) ^ 1))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < kTokens / 16; ++q)
-                    if (q * 16 < U.n) tmem_st16(tmem + lanes + d_col(1, last) + q * 16, reinterpret_cast<const uint32_t *>(acc) + q * 16);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&T.up_full);
-                continue;
-            }
-            uint32_t there[2] = {~0u, ~0u};       // a token that is not there stands for a row of zeros
-            if (p.perm && !p.x_by_row && !shared)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    there[h] = __ballot_sync(0xffffffffu, h * 32 + lane < U.n &&
-                                                              (unsigned)p.perm[U.row0 + h * 32 + lane] < (unsigned)p.x_rows);
-            const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + c * kRows + row;
+            tc_fence_after();
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
-            if (kUp) {
-                if (!all(wait(&T.up_full, un & 1))) break;
-                tc_fence_after();
-            }
 #pragma unroll
-            for (int q = 0; q < kTokens / 16; ++q)
-                if (q * 16 < U.n) {
-                    uint32_t v[16];
+            for (int q = 0; q < kTokens / 16; ++q) {
+                if (q * 16 >= U.n) break;
+                if ((q & 1) != half) continue;
+                uint32_t v0[16], v1[16];
+                tmem_ld16(tmem + lanes + d_col(0, sl.first) + q * 16, v0);
+                tmem_ld16(tmem + lanes + d_col(1, sl.first) + q * 16, v1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float f = __shfl_sync(0xffffffffu, tok[q >> 1], (q & 1) * 16 + i);
+                    const float o0 = f == 0.f ? 0.f : __uint_as_float(v0[i]) * row_scale[0] * f;
+                    const float o1 = f == 0.f ? 0.f : __uint_as_float(v1[i]) * row_scale[1] * f;
+                    if (q * 16 + i >= U.n) continue;
+                    YT *at = y + (size_t)(q * 16 + i) * p.rows;
                     if (kUp) {
-                        tmem_ld16(tmem + lanes + d_col(1, last) + q * 16, v);
-                        tmem_ld_wait();
+                        const int r = U.tile * kRows + row;
+                        if (r < p.rows) store_val(at + r, silu_mul(o0, o1));
+                    } else {
+                        const int r = U.tile * 2 * kRows + row;
+                        if (r < p.rows) store_val(at + r, o0);
+                        if (r + kRows < p.rows) store_val(at + r + kRows, o1);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float o = kUp ? silu_mul(acc[q * 16 + i], __uint_as_float(v[i])) : acc[q * 16 + i];
-                        if (!((there[q >> 1] >> ((q & 1) * 16 + i)) & 1)) o = 0.f;
-                        if (q * 16 + i < U.n && r < p.rows) store_val(y + (size_t)(q * 16 + i) * p.rows + r, o);
-                    }
-                }
-            if (kUp) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&T.dempty[1][last]);
-                    mbar_arrive(&T.up_empty);
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
+            sl.done();
         }
     }
     tc_fence_before();
@@ -537,8 +586,8 @@ static bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t b
 template <bool kUp, int G, bool kZeros, class YT>
 static kmoe_status run(const Maps &maps, const Args &a, int grid, cudaStream_t st)
 {
-    cudaFuncSetAttribute(kernel<kUp, G, kZeros, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    launch_pdl(kernel<kUp, G, kZeros, YT>, grid, kThreads, kSmem, st, maps, a);
+    cudaFuncSetAttribute(w4_tc_kernel<kUp, G, kZeros, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    launch_pdl(w4_tc_kernel<kUp, G, kZeros, YT>, grid, kThreads, kSmem, st, maps, a);
     return check_launch("w4_tc");
 }
 
@@ -555,10 +604,61 @@ static kmoe_status pick(const Maps &m, const Args &a, int grid, cudaStream_t st)
 
 }  // namespace w4tc
 
-kmoe_status launch_w4_tc(const W4Product &p, int *err, long long wait_limit, cudaStream_t st)
+// x (BF16 or FP32) in FP16 over a power of two per row: the largest magnitude
+// of a row lies in [2^14, 2^15). One warp per row, two passes (the second reads
+// L1). `out` may start where x starts, with rows the same bytes apart (H, FP32):
+// a step's values are read before any of its results is written.
+template <class XT>
+__global__ void __launch_bounds__(256) to_f16_kernel(const XT *x, int rows, int cols, __half *out, size_t out_pitch, float *scale)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const XT *src = x + (size_t)row * cols;
+    uint32_t top = 0;
+    for (int c = lane * 8; c < cols; c += 256) {
+        float v[8];
+        load8(src + c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const uint32_t ex = max(top >> 23, 15u);      // a row below 2^-112 stays at that scale
+    const float mul = __uint_as_float((268u - ex) << 23);             // 2^(14 - E)
+    __half *dst = out + (size_t)row * out_pitch;
+    for (int c0 = 0; c0 < cols; c0 += 256) {
+        const int c = c0 + lane * 8;
+        float v[8];
+        if (c < cols) load8(src + c, v);
+        __syncwarp();
+        if (c < cols) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 h = __floats2half2_rn(v[2 * i] * mul, v[2 * i + 1] * mul);
+                o[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncwarp();
+    }
+    if (lane == 0) scale[row] = __uint_as_float((ex - 14u) << 23);
+}
+
+kmoe_status launch_w4_tc(const W4Product &p, void *x16, float *x_scale, int *err, long long wait_limit, cudaStream_t st)
 {
     using namespace w4tc;
     Args a{};
+    a.x16 = x16;
+    a.x_pitch = (size_t)p.cols * (p.x_f32 ? 4 : 2);
+    a.x_scale = x_scale;
+    const int x_grid = (p.x_rows + 7) / 8;
+    __half *out = static_cast<__half *>(x16);
+    if (p.x_f32) launch_pdl(to_f16_kernel<float>, x_grid, 256, 0, st, static_cast<const float *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols * 2, x_scale);
+    else launch_pdl(to_f16_kernel<__nv_bfloat16>, x_grid, 256, 0, st, static_cast<const __nv_bfloat16 *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols, x_scale);
+    const kmoe_status conv = check_launch("to_f16");
+    if (conv != KMOE_OK) return conv;
     a.p = p;
     a.groups = p.E + (p.n_shared > 0 ? 1 : 0);
     if (a.groups > kMaxGroups) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: too many experts");
@@ -581,10 +681,9 @@ kmoe_status launch_w4_tc(const W4Product &p, int *err, long long wait_limit, cud
     if (!ok) return fail(KMOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long most = ((long long)std::min(p.E, p.P) + (p.P + p.n_shared) / 32 + 1) * a.tiles;
+    const long long most = ((long long)std::min(p.E, p.P) + (p.P + p.n_shared) / 64 + 1) * a.tiles;
     const int grid = (int)std::min<long long>(sms, most);
-    if (up) return pick<true, __nv_bfloat16>(m, a, grid, st);
-    return p.y_dtype == KMOE_F32 ? pick<false, float>(m, a, grid, st) : pick<false, __nv_bfloat16>(m, a, grid, st);
+    return up ? pick<true, float>(m, a, grid, st) : pick<false, __nv_bfloat16>(m, a, grid, st);
 }
 
 }  // namespace kmoe

@@ -51,10 +51,12 @@ struct W4Product {
     int y_dtype;
     int *status;                         // set to 0 (NULL: none)
 };
-// wait_limit: SM cycles before a pipeline wait of the tensor-core kernel gives
-// up and sets *err (the device status word; may be NULL) to 1.
 kmoe_status launch_w4(const W4Product &a, cudaStream_t st);
-kmoe_status launch_w4_tc(const W4Product &a, int *err, long long wait_limit, cudaStream_t st);
+// The tensor-core kernel; y is BF16 (H: FP32). x16 and x_scale: scratch for x in
+// FP16 ([x_rows, cols], for FP32 x its own memory) and a float for each of its
+// rows. wait_limit: SM cycles before a pipeline wait gives up and sets *err (the
+// device status word; may be NULL) to 1.
+kmoe_status launch_w4_tc(const W4Product &a, void *x16, float *x_scale, int *err, long long wait_limit, cudaStream_t st);
 
 // Routing by the rule of kmoe_routing. hist as in launch_topk.
 kmoe_status launch_route(const void *logits, int l_dtype, const float *bias, int N, int E, int K,

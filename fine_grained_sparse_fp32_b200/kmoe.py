@@ -24,7 +24,7 @@ FFN_STATUS_BYTES = (64 + 1088) * 4
 
 EXPORTS = ["moe_workspace_size", "moe_router_topk", "moe_permute", "moe_permute_noalloc", "moe_grouped_ffn",
            "moe_combine", "moe_forward", "moe_block_workspace_size", "moe_block_forward", "moe_quant_1x128",
-           "moe_route", "moe_linear_w4", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
+           "moe_route", "moe_linear_w4", "moe_linear_w4_workspace_size", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
            "moe_dequant_w4",
            "moe_device_status", "moe_set_wait_limit", "moe_last_error", "moe_abi_version"]
 
@@ -141,7 +141,9 @@ def load(path: str | None = None):
                                       ctypes.POINTER(Experts), ctypes.POINTER(Experts), vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_quant_1x128.argtypes = [vp, i, i, vp, vp, vp]
     lib.moe_route.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp]
-    lib.moe_linear_w4.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp]
+    lib.moe_linear_w4.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp, sz, vp]
+    lib.moe_linear_w4_workspace_size.restype = sz
+    lib.moe_linear_w4_workspace_size.argtypes = [i, i, i, i]
     lib.moe_forward_routed.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, ctypes.POINTER(Experts),
                                        ctypes.POINTER(Experts), vp, i, vp, vp, vp, vp, sz, vp]
     lib.moe_block_forward_routed.argtypes = [vp, i, i, i, i, i, vp, vp, vp, ctypes.c_float, vp, vp,
@@ -153,7 +155,7 @@ def load(path: str | None = None):
     lib.moe_set_wait_limit.argtypes = [ctypes.c_longlong]
     for f in ("moe_router_topk", "moe_permute", "moe_permute_noalloc", "moe_grouped_ffn", "moe_combine",
               "moe_forward", "moe_block_forward", "moe_quant_1x128", "moe_device_status", "moe_set_wait_limit",
-              "moe_route", "moe_linear_w4", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
+              "moe_route", "moe_linear_w4", "moe_linear_w4_workspace_size", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
               "moe_dequant_w4"):
         getattr(lib, f).restype = i
     if lib.moe_abi_version() != 3:
@@ -563,7 +565,11 @@ def moe_dequant_w4(w4: W4, dtype=torch.bfloat16, out=None, stream=None):
     return out
 
 
-def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat16, out=None, stream=None):
+def moe_linear_w4_workspace_size(N, P, cols, y_dtype=torch.bfloat16) -> int:
+    return int(load().moe_linear_w4_workspace_size(N, P, cols, _act_code(y_dtype, "y")))
+
+
+def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat16, out=None, ws=None, stream=None):
     """y[p] = W_e x[perm_token[p]] with 4-bit weights: one matrix for all rows, or (offsets [E + 1], from
     moe_permute) the matrix of the expert whose range holds p. x [N, cols] BF16; y [P, rows]."""
     if x.dim() != 2:
@@ -585,7 +591,13 @@ def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat
         out = torch.empty((P, w4.rows), dtype=y_dtype, device=dev)
     else:
         _dense(out, "out", tuple(_DTYPE_CODES), (P, w4.rows), dev)
+    code = _DTYPE_CODES[out.dtype]
+    if ws is None and code == KMOE_BF16:
+        need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.cols, code)
+        if need:
+            with torch.cuda.stream(stream):       # memory of the stream that uses it
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("moe_linear_w4", x, stream, x.data_ptr(), KMOE_BF16, N, P, w4.rows, w4.cols, w4.E,
           None if perm_token is None else perm_token.data_ptr(), None if offsets is None else offsets.data_ptr(),
-          w4._ref, out.data_ptr(), _DTYPE_CODES[out.dtype])
+          w4._ref, out.data_ptr(), code, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out

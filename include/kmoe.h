@@ -300,10 +300,13 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
  * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,
  * 128 <= cols <= 8192 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
+ * ws: device workspace of at least moe_linear_w4_workspace_size() bytes, which
+ * is 0 (ws may be NULL) for few rows and for FP32 y.
  */
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,
-                          void *y, int y_dtype, void *stream);
+                          void *y, int y_dtype, void *ws, size_t ws_bytes, void *stream);
+size_t moe_linear_w4_workspace_size(int N, int P, int cols, int y_dtype);
 
 /*
  * Weighted combine ("Kolibri 1 Deep Dive", section 1, the layer-output

@@ -65,7 +65,7 @@ def w4(group=128, codes=A, scales=A, zeros=None):
 
 def linear(lib, w=None, x_dtype=1, N=4, P=4, rows=16, cols=256, E=1, perm=None, off=None, x=A, y=A, y_dtype=1):
     w = w4() if w is None else w
-    return lib.moe_linear_w4(x, x_dtype, N, P, rows, cols, E, perm, off, ctypes.byref(w), y, y_dtype, None)
+    return lib.moe_linear_w4(x, x_dtype, N, P, rows, cols, E, perm, off, ctypes.byref(w), y, y_dtype, A, 1 << 40, None)
 
 
 def test_linear_w4_checks_its_arguments(lib):
@@ -77,7 +77,12 @@ def test_linear_w4_checks_its_arguments(lib):
                      (dict(perm=OFF), BAD), (dict(off=OFF), BAD), (dict(w=w4(group=48)), UNSUP),
                      (dict(w=w4(codes=None)), BAD), (dict(w=w4(scales=OFF)), BAD), (dict(w=w4(zeros=OFF)), BAD)):
         assert linear(lib, **kw) == code, kw
-    assert lib.moe_linear_w4(A, 1, 4, 4, 16, 256, 1, None, None, None, A, 1, None) == BAD
+    assert lib.moe_linear_w4(A, 1, 4, 4, 16, 256, 1, None, None, None, A, 1, A, 0, None) == BAD
+    need = kmoe.moe_linear_w4_workspace_size(5000, 5000, 256)
+    assert need >= 5000 * (256 * 2 + 4) and kmoe.moe_linear_w4_workspace_size(5000, 5000, 256, torch.float32) == 0
+    w = w4()
+    call = lambda ws, n: lib.moe_linear_w4(A, 1, 5000, 5000, 16, 256, 1, None, None, ctypes.byref(w), A, 1, ws, n, None)
+    assert call(A, need - 1) == kmoe.KMOE_ERR_WORKSPACE and call(None, need) == BAD
 
 
 def test_quant_w4_checks_its_arguments(lib):

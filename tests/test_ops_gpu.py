@@ -5,10 +5,11 @@ fixed point, for each 128 columns off by at most 2^-22 of their largest |x|; the
 and in FP32 follow, for each of the three digits of x, one scaled sum per group (at most cols / 32, each two
 roundings of 2^-24 and the addition's) and the joining of digits and of at most 16 column shares, all
 relative to S = sum |W| |x| (a digit's own sum of magnitudes is below 2 S): in all less than
-(cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-22 max|x|. For the FFN the errors of both sums go
-through SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|; the hardware exponential
-and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst; all of it goes through
-|W_d|.
+(cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-22 max|x|. Batches on the tensor cores (BF16 results)
+round each weight to FP16, 2^-11 S more, and have the same FP32 sums of cols / 16 partial sums. For the FFN
+the errors of both sums go through SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|;
+the hardware exponential and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst;
+all of it goes through |W_d|.
 """
 import numpy as np
 import pytest
@@ -155,20 +156,23 @@ def make_w4(g, lead, rows, cols, group, zeros):
     return kmoe.W4(codes, scales, z)
 
 
-def sums_bound(x, w, cols):
+def sums_bound(x, w, cols, tensor_cores=False):
     top = x.abs().unflatten(-1, (-1, 128)).amax(-1).repeat_interleave(128, -1)
-    return ((cols / 16 + cols / 32 + 8) * 2.0 ** -23 * x.abs() + 2.0 ** -22 * top) @ w.abs().t()
+    each = (cols / 16 + cols / 32 + 8) * 2.0 ** -23 + (2.0 ** -11 if tensor_cores else 0)
+    return (each * x.abs() + 2.0 ** -22 * top) @ w.abs().t()
 
 
-def check_linear(y, x, w, cols):
+def check_linear(y, x, w, cols, rows=None):
+    """rows: rows of the call (those of y, unless y is a part of them)."""
     ref = x @ w.t()
-    tol = sums_bound(x, w, cols) + (BF16 * ref.abs() if y.dtype == torch.bfloat16 else 0) + 1e-30
+    tc = kmoe.moe_linear_w4_workspace_size(rows or y.shape[0], rows or y.shape[0], cols, y.dtype) > 0
+    tol = sums_bound(x, w, cols, tc) + (BF16 * ref.abs() if y.dtype == torch.bfloat16 else 0) + 1e-30
     assert torch.isfinite(y).all()
     off = (y.double() - ref).abs() / tol
     assert off.max() <= 1, float(off.max())
 
 
-@pytest.mark.parametrize("N", [1, 3, 8, 9, 17, 32, 33, 70])
+@pytest.mark.parametrize("N", [1, 3, 8, 9, 17, 32, 33, 70, 129, 300])
 @pytest.mark.parametrize("rows,cols", [(1, 128), (15, 384), (16, 640), (100, 2560), (515, 256), (17, 8192)])
 def test_linear_w4_one_matrix(N, rows, cols):
     g = gen(N * 1000 + rows + cols)
@@ -184,20 +188,21 @@ def test_linear_w4_one_matrix(N, rows, cols):
 
 @pytest.mark.parametrize("N,E,K", [(1, 16, 4), (5, 16, 4), (64, 7, 3), (300, 3, 2), (130, 61, 8)])
 @pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
-def test_linear_w4_grouped_by_expert(N, E, K, group, zeros):
+@pytest.mark.parametrize("y_dtype", [torch.float32, torch.bfloat16])
+def test_linear_w4_grouped_by_expert(N, E, K, group, zeros, y_dtype):
     g = gen(N + E)
     rows, cols = 72, 384
     x = randn(g, N, cols).bfloat16()
     w = make_w4(g, E, rows, cols, group, zeros)
     idx = torch.rand((N, E), device="cuda", generator=g).topk(K, 1).indices.int()
     counts, offsets, perm, inv = kmoe.moe_permute(idx, E)
-    y = kmoe.moe_linear_w4(x, w, perm, offsets, y_dtype=torch.float32)
+    y = kmoe.moe_linear_w4(x, w, perm, offsets, y_dtype=y_dtype)
     v = plain_ops.w4_values(w.codes, w.scales, w.zeros)
     off = offsets.tolist()
     for e in range(E):
         at = slice(off[e], off[e + 1])
         if off[e] < off[e + 1]:
-            check_linear(y[at], x.double()[perm[at].long()], v[e], cols)
+            check_linear(y[at], x.double()[perm[at].long()], v[e], cols, rows=N * K)
 
 
 def test_linear_w4_leaves_uncovered_rows_and_reads_no_foreign_token():
@@ -222,29 +227,47 @@ def test_linear_w4_leaves_uncovered_rows_and_reads_no_foreign_token():
     assert (kmoe.moe_linear_w4(x[:0], w, perm, torch.tensor([0, 4, 7, 10], dtype=torch.int32, device="cuda")) == 0).all()
 
 
-def test_linear_w4_takes_wide_ranges_of_values():
+@pytest.mark.parametrize("N,y_dtype", [(5, torch.float32), (5, torch.bfloat16), (200, torch.bfloat16)])
+def test_linear_w4_takes_wide_ranges_of_values(N, y_dtype):
     """Large and tiny x and scales: sums stay in FP32 range and keep their relative accuracy."""
     g = gen(3)
-    x = (randn(g, 5, 512) * torch.tensor([1e-20, 1e-3, 1.0, 1e4, 1e15], device="cuda")[:, None]).bfloat16()
+    x = randn(g, N, 512) * torch.tensor([1e-20, 1e-3, 1.0, 1e4, 1e15], device="cuda").repeat(N // 5)[:, None]
+    x = x.bfloat16()
     w = make_w4(g, 1, 33, 512, 128, False)
-    w.scales.mul_(1e10)
-    y = kmoe.moe_linear_w4(x, kmoe.W4(w.codes[0], w.scales[0]), y_dtype=torch.float32)
+    w.scales.mul_(torch.logspace(-12, 10, 33, device="cuda")[None, :, None])
+    w.scales[0, :, 1] *= 2.0 ** -9                         # groups of one row that differ widely
+    w.scales[0, ::2, 2] *= 2.0 ** 7
+    y = kmoe.moe_linear_w4(x, kmoe.W4(w.codes[0], w.scales[0]), y_dtype=y_dtype)
     check_linear(y, x.double(), plain_ops.w4_values(w.codes[0], w.scales[0]), 512)
 
 
+@pytest.mark.parametrize("N", [6, 200])
+def test_linear_w4_keeps_non_finite_rows_to_themselves(N):
+    g = gen(6)
+    x = randn(g, N, 384).bfloat16()
+    x[1, 7], x[N - 1, 300] = float("nan"), float("inf")
+    w = make_w4(g, 1, 40, 384, 128, True)
+    y = kmoe.moe_linear_w4(x, kmoe.W4(w.codes[0], w.scales[0], w.zeros[0]))
+    fine = torch.ones(N, dtype=torch.bool, device="cuda")
+    fine[[1, N - 1]] = False
+    check_linear(y[fine], x[fine].double(), plain_ops.w4_values(w.codes[0], w.scales[0], w.zeros[0]), 384, rows=N)
+    assert not torch.isfinite(y[1]).any() and not torch.isfinite(y[N - 1]).all()
+
+
 # ------------------------------------------------------------- experts' FFN
-def ffn_ref(x, layer, e, group_cols):
-    """FP64 result and bound of expert e on rows x."""
+def ffn_ref(x, layer, e, tc):
+    """FP64 result and bound of expert e on rows x; tc: on the tensor cores."""
     z = lambda m: None if layer.get("z_" + m) is None else layer["z_" + m][e]
     wg, wu, wd = (plain_ops.w4_values(layer["w_" + m][e], layer["s_" + m][e], z(m)) for m in ("gate", "up", "down"))
     d, I = wg.shape[1], wg.shape[0]
     a, u = x @ wg.t(), x @ wu.t()
     h = a * torch.sigmoid(a) * u
-    dh = 1.1 * u.abs() * sums_bound(x, wg, d) + (a * torch.sigmoid(a)).abs() * sums_bound(x, wu, d) + 2.0 ** -20 * h.abs()
+    dh = 1.1 * u.abs() * sums_bound(x, wg, d, tc) + (a * torch.sigmoid(a)).abs() * sums_bound(x, wu, d, tc) \
+        + 2.0 ** -20 * h.abs()
     dh = dh + BF16 * (h.abs() + dh)
     y = h @ wd.t()
     hh = h.abs() + dh
-    return y, dh @ wd.abs().t() + sums_bound(hh, wd, I) + BF16 * y.abs() + 1e-30
+    return y, dh @ wd.abs().t() + sums_bound(hh, wd, I, tc) + BF16 * y.abs() + 1e-30
 
 
 def check_ffn(layer, N, K, E, seed, with_shared=True, handle=None):
@@ -262,7 +285,7 @@ def check_ffn(layer, N, K, E, seed, with_shared=True, handle=None):
             assert ys is None
             continue
         if rows.shape[0]:
-            ref, tol = ffn_ref(rows.double(), layer, e, cfg.w4_group)
+            ref, tol = ffn_ref(rows.double(), layer, e, N >= 128)
             off_by = ((got.double() - ref).abs() / tol).max()
             assert off_by <= 1, (e, float(off_by))
     return x, perm, offsets, y, ys
