@@ -75,6 +75,7 @@ struct Tail {
     int abort, total;
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
+    alignas(8) float tok[8][kTokens];             // result warps: the tokens' powers of two
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
@@ -218,13 +219,22 @@ __device__ __forceinline__ void unpack_word(uint32_t word, __half2 z1, __half2 z
     out[3] = half2_bits(__hmul2(__hfma2(as_half2((up & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
 }
 
-// Exponent field of the largest magnitude among n scales (n a multiple of 2 at
-// a 4-byte boundary, or any n).
+// Exponent field of the largest magnitude among the n scales of a row (which
+// start at a multiple of 8 bytes where n is a multiple of 4).
 __device__ __forceinline__ uint32_t scale_exponent(const __nv_bfloat16 *s, int n)
 {
     uint32_t top = 0;
-    const uint16_t *v = reinterpret_cast<const uint16_t *>(s);
-    for (int i = 0; i < n; ++i) top = max(top, (uint32_t)(v[i] & 0x7fffu));
+    if (n % 4 == 0) {
+        uint32_t two = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; i += 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(s + i);
+            two = __vmaxu2(two, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+        }
+        top = max(two & 0xffffu, two >> 16);
+    } else {
+        for (int i = 0; i < n; ++i) top = max(top, (uint32_t)(__bfloat16_as_ushort(s[i]) & 0x7fffu));
+    }
     return max(top >> 7, 1u);
 }
 
@@ -239,6 +249,23 @@ __device__ __forceinline__ size_t tile_row(const Args &a, const Unit &u, int c, 
 // Tensor memory: sums of tile c in a slot, unpacked weights of tile c in a buffer.
 __device__ __forceinline__ uint32_t d_col(int c, int slot) { return c * 128 + slot * 64; }
 __device__ __forceinline__ uint32_t a_col(int c, int b) { return 256 + c * 128 + b * 64; }
+
+// A row's sums of two neighbouring tokens, to y [token][row] in BF16. Lanes hold
+// neighbouring rows: each even lane takes the first token of two rows, each odd
+// lane the second, so that a lane stores 4 bytes.
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *at, int pitch, float first, float second, bool in, bool has_second)
+{
+    const bool odd = threadIdx.x & 1;
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? first : second, 1);
+    if (pitch & 1) {                              // rows of an odd pitch: a value at a time
+        if (!in) return;
+        at[0] = __float2bfloat16_rn(first);
+        if (has_second) at[pitch] = __float2bfloat16_rn(second);
+        return;
+    }
+    const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, second) : __floats2bfloat162_rn(first, other);
+    if (in && (!odd || has_second)) *reinterpret_cast<__nv_bfloat162 *>(odd ? at + pitch - 1 : at) = v;
+}
 
 // Slots that units take in turn: a unit of up to 64 tokens takes the next one,
 // a larger one both. `phase` holds, for each slot, the parity of its uses.
@@ -336,10 +363,6 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         const uint32_t panel = (uint32_t)(piece >> 3) * kPanel;
         uint32_t it = 0;
         bool ok = true;
-        auto landed = [&](uint32_t j) {           // this thread's copies of block j are in place: tell the MMA
-            fence_proxy_async();
-            mbar_arrive(&T.bfull[j % kStages]);
-        };
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
@@ -367,15 +390,10 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                     if (4 * j >= U.n) break;
                     cp_async16(dst + i * 128 + (((piece & 7) ^ (i & 7)) << 4), src + (size_t)row[j] * a.x_pitch, 16);
                 }
-                cp_async_commit();
-                if (it > 0) {                     // one block behind, so that copies overlap
-                    cp_async_wait<1>();
-                    landed(it - 1);
-                }
+                cp_async_arrive_noinc(&T.bfull[s]);       // once this thread's copies have landed
             }
         }
         cp_async_wait_all();
-        if (it > 0) landed(it - 1);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA
         // The whole warp walks; one elected lane issues. Kept converged, the
@@ -392,6 +410,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
                 const int s = it % kStages, ab = it & 1;
                 ok = wait(&T.bfull[s], (it / kStages) & 1);
+                fence_proxy_async();              // the gathered rows, for the tensor core
                 const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
                 const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
 #pragma unroll
@@ -498,45 +517,54 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 const __nv_bfloat16 *sc = kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s);
                 row_scale[c] = __uint_as_float(min(scale_exponent(sc + tile_row<kUp>(a, U, c, row) * gpr, gpr), 253u) << 23);
             }
-            float tok[kTokens / 32];              // of tokens lane + 32 j; 0 for one that is not there
+            float *tok = T.tok[warp];             // 0 for a token that is not there
+            bool there = true;
 #pragma unroll
             for (int j = 0; j < kTokens / 32; ++j) {
                 const int i = lane + 32 * j;
-                int xi = -1;
+                int xi = 0;
                 if (i < U.n) {
                     xi = U.row0 + i;
                     if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
                 }
-                tok[j] = (unsigned)xi < (unsigned)p.x_rows ? a.x_scale[xi] : 0.f;
+                const bool in = (unsigned)xi < (unsigned)p.x_rows;
+                there = there && in;
+                tok[i] = in ? a.x_scale[xi] : 0.f;
             }
+            there = __all_sync(0xffffffffu, there);
+            __syncwarp();
             for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dfull[sl.first + k], sl.parity(sl.first + k));
             if (!ok) break;
             tc_fence_after();
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
-#pragma unroll
-            for (int q = 0; q < kTokens / 16; ++q) {
-                if (q * 16 >= U.n) break;
-                if ((q & 1) != half) continue;
+            const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
+            for (int t0 = half * 16; t0 < U.n; t0 += 32) {
                 uint32_t v0[16], v1[16];
-                tmem_ld16(tmem + lanes + d_col(0, sl.first) + q * 16, v0);
-                tmem_ld16(tmem + lanes + d_col(1, sl.first) + q * 16, v1);
+                tmem_ld16(tmem + lanes + d_col(0, sl.first) + t0, v0);
+                tmem_ld16(tmem + lanes + d_col(1, sl.first) + t0, v1);
                 tmem_ld_wait();
+                YT *at = y + (size_t)t0 * p.rows + r;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float f = __shfl_sync(0xffffffffu, tok[q >> 1], (q & 1) * 16 + i);
-                    const float o0 = f == 0.f ? 0.f : __uint_as_float(v0[i]) * row_scale[0] * f;
-                    const float o1 = f == 0.f ? 0.f : __uint_as_float(v1[i]) * row_scale[1] * f;
-                    if (q * 16 + i >= U.n) continue;
-                    YT *at = y + (size_t)(q * 16 + i) * p.rows;
-                    if (kUp) {
-                        const int r = U.tile * kRows + row;
-                        if (r < p.rows) store_val(at + r, silu_mul(o0, o1));
-                    } else {
-                        const int r = U.tile * 2 * kRows + row;
-                        if (r < p.rows) store_val(at + r, o0);
-                        if (r + kRows < p.rows) store_val(at + r + kRows, o1);
+                for (int i = 0; i < 16; i += 2) {
+                    if (t0 + i >= U.n) break;
+                    const float2 f = *reinterpret_cast<const float2 *>(tok + t0 + i);
+                    float a0 = __uint_as_float(v0[i]) * row_scale[0] * f.x, b0 = __uint_as_float(v0[i + 1]) * row_scale[0] * f.y;
+                    float a1 = __uint_as_float(v1[i]) * row_scale[1] * f.x, b1 = __uint_as_float(v1[i + 1]) * row_scale[1] * f.y;
+                    if (!there) {                 // such tokens stand for zeros
+                        if (f.x == 0.f) a0 = a1 = 0.f;
+                        if (f.y == 0.f) b0 = b1 = 0.f;
                     }
+                    if constexpr (kUp) {
+                        if (r < p.rows) {
+                            at[0] = silu_mul(a0, a1);
+                            if (t0 + i + 1 < U.n) at[p.rows] = silu_mul(b0, b1);
+                        }
+                    } else {
+                        store_pair(at, p.rows, a0, b0, r < p.rows, t0 + i + 1 < U.n);
+                        store_pair(at + kRows, p.rows, a1, b1, r + kRows < p.rows, t0 + i + 1 < U.n);
+                    }
+                    at += 2 * p.rows;
                 }
             }
             tc_fence_before();
