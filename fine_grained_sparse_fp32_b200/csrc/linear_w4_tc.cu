@@ -18,7 +18,8 @@
 // (256 rows of one expert, or 128 gate and the same 128 up features) and a
 // block of tokens. Units are dealt to the CTAs (one per SM) in turn.
 //   warps 0-7    results: sums from tensor memory, SiLU(gate) * up or y (warps
-//                0-3 and 4-7 take turns in 16-token steps)
+//                0-3 and 4-7 take turns in units, so that one's loads and
+//                stores overlap the other's)
 //   warps 8-15   unpack: 64 bytes of codes of a row and 128 columns into 64
 //                columns of tensor memory (8-11 tile 0, 12-15 tile 1)
 //   warp 16      loads code tiles by TMA (64-byte swizzle: the unpackers' reads
@@ -70,12 +71,14 @@ struct Args {
 
 struct Tail {
     uint64_t cfull[kStages], cempty[kStages], bfull[kStages], bempty[kStages];
-    uint64_t afull[2][2], aempty[2][2], dfull[2], dempty[2], drain;    // d: both tiles' sums in a slot
+    uint64_t afull[2][2], aempty[2][2], dfull[2], dempty[2], drain;    // sums of a group's unit; a slot read
     uint32_t tmem_base;
     int abort, total;
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
-    alignas(8) float tok[8][kTokens];             // result warps: the tokens' powers of two
+    // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
+    alignas(16) float tok[8][kTokens];
+    alignas(16) __nv_bfloat16 turn[8][16 * 32];
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
@@ -250,25 +253,70 @@ __device__ __forceinline__ size_t tile_row(const Args &a, const Unit &u, int c, 
 __device__ __forceinline__ uint32_t d_col(int c, int slot) { return c * 128 + slot * 64; }
 __device__ __forceinline__ uint32_t a_col(int c, int b) { return 256 + c * 128 + b * 64; }
 
-// A row's sums of two neighbouring tokens, to y [token][row] in BF16. Lanes hold
-// neighbouring rows: each even lane takes the first token of two rows, each odd
-// lane the second, so that a lane stores 4 bytes.
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *at, int pitch, float first, float second, bool in, bool has_second)
+// 32 rows (one per lane) by 16 tokens of results to y [token][row] in BF16. They
+// turn in shared memory, so that a lane stores 16 bytes of a token's row: 4-byte
+// stores, four times as many, took up to 300 clocks each. at: the first token's
+// row of lane 0; left: rows from there to the end; n: tokens that are there.
+__device__ __forceinline__ void store_turned(__nv_bfloat16 *at, int pitch, int left, int n, __nv_bfloat16 *turn, const float (&o)[16])
 {
-    const bool odd = threadIdx.x & 1;
-    const float other = __shfl_xor_sync(0xffffffffu, odd ? first : second, 1);
-    if (pitch & 1) {                              // rows of an odd pitch: a value at a time
-        if (!in) return;
-        at[0] = __float2bfloat16_rn(first);
-        if (has_second) at[pitch] = __float2bfloat16_rn(second);
-        return;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) turn[i * 32 + lane] = __float2bfloat16_rn(o[i]);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = h * 8 + (lane >> 2), r = (lane & 3) * 8;
+        const uint4 v = *reinterpret_cast<const uint4 *>(turn + i * 32 + r);
+        __nv_bfloat16 *dst = at + (size_t)i * pitch + r;
+        if (i < n) {
+            if (r + 8 <= left && pitch % 8 == 0) {
+                *reinterpret_cast<uint4 *>(dst) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (r + k < left) dst[k] = __ushort_as_bfloat16((unsigned short)(w[k >> 1] >> (16 * (k & 1))));
+            }
+        }
     }
-    const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, second) : __floats2bfloat162_rn(first, other);
-    if (in && (!odd || has_second)) *reinterpret_cast<__nv_bfloat162 *>(odd ? at + pitch - 1 : at) = v;
+    __syncwarp();
+}
+
+// Results of 16 tokens (n of them there) from both tiles' sums v0, v1. at: the
+// first token's row r of y. All: every token is there and has an x row.
+template <bool kUp, bool kAll, class YT>
+__device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, int n, const float *tok, const float (&row_scale)[2],
+                                           __nv_bfloat16 *turn, const uint32_t (&v0)[16], const uint32_t (&v1)[16])
+{
+    float o0[16], o1[16];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float4 f4 = *reinterpret_cast<const float4 *>(tok + i);
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o0[i + k] = __uint_as_float(v0[i + k]) * row_scale[0] * f[k];
+            o1[i + k] = __uint_as_float(v1[i + k]) * row_scale[1] * f[k];
+            if (!kAll && f[k] == 0.f) o0[i + k] = o1[i + k] = 0.f;    // a token without an x row stands for zeros
+        }
+    }
+    if constexpr (kUp) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o0[i] = silu_mul(o0[i], o1[i]);
+        if (r < p.rows)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (kAll || i < n) at[(size_t)i * p.rows] = o0[i];
+    } else {
+        const int lane = threadIdx.x & 31, left = p.rows - (r - lane);
+        store_turned(at - lane, p.rows, left, n, turn, o0);
+        store_turned(at - lane + kRows, p.rows, left - kRows, n, turn, o1);
+    }
 }
 
 // Slots that units take in turn: a unit of up to 64 tokens takes the next one,
-// a larger one both. `phase` holds, for each slot, the parity of its uses.
+// a larger one both. `phase` holds, for each slot, the parity of its uses (the
+// MMA warp's: it waits for every use of a slot).
 struct Slots {
     uint32_t phase = 0;
     int next = 0, first = 0, n = 1;
@@ -309,7 +357,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&T.dfull[b], 1);
-            mbar_init(&T.dempty[b], 8);           // one arrival per result warp
+            mbar_init(&T.dempty[b], 4);           // one arrival per result warp of a group
         }
         mbar_init(&T.drain, 1);
         T.abort = 0;
@@ -366,7 +414,9 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
-            int row[kTokens / 4];                 // x rows; row 0 for tokens that are not there (their results are not used)
+            // x rows, in 16-byte pieces from x; row 0 for tokens that are not there (their results are not used)
+            uint32_t row[kTokens / 4];
+            const uint32_t pieces = (uint32_t)(a.x_pitch >> 4);
 #pragma unroll
             for (int j = 0; j < kTokens / 4; ++j) {
                 const int i = 4 * j + (th >> 4);
@@ -376,19 +426,20 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                     if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
                     if ((unsigned)xi >= (unsigned)p.x_rows) xi = 0;
                 }
-                row[j] = xi;
+                row[j] = (uint32_t)xi * pieces + piece;
             }
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
                 ok = wait(&T.bempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
-                const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel;
-                const char *src = static_cast<const char *>(a.x16) + kb * (kW4Block * 2) + piece * 16;
+                const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel + (th >> 4) * 128;
+                // the swizzle takes the row's low three bits: 4 (j & 1) + th / 16
+                const uint32_t dst0 = dst + (((piece & 7) ^ (th >> 4)) << 4), dst1 = dst + (((piece & 7) ^ (4 + (th >> 4))) << 4);
+                const uint4 *src = static_cast<const uint4 *>(a.x16) + kb * (kW4Block * 2 / 16);
 #pragma unroll
                 for (int j = 0; j < kTokens / 4; ++j) {
-                    const int i = 4 * j + (th >> 4);
                     if (4 * j >= U.n) break;
-                    cp_async16(dst + i * 128 + (((piece & 7) ^ (i & 7)) << 4), src + (size_t)row[j] * a.x_pitch, 16);
+                    cp_async16((j & 1 ? dst1 : dst0) + j * 512, src + row[j], 16);
                 }
                 cp_async_arrive_noinc(&T.bfull[s]);       // once this thread's copies have landed
             }
@@ -402,7 +453,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         uint32_t it = 0;
         Slots sl;
         bool ok = true;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        for (int u = blockIdx.x, turn = 0; u < total && ok; u += gridDim.x, turn ^= 1) {
             const Unit U = unit_of(a, T, u);
             const uint32_t idesc = idesc_f16_f32(kRows, (U.n + 15) & ~15);
             sl.take(U.n);
@@ -425,10 +476,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                             umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
                         umma_commit(&T.aempty[c][ab]);
                         if (c == 1) umma_commit(&T.bempty[s]);
-                        if (c == 1 && kb + 1 == blocks) {
-                            umma_commit(&T.dfull[sl.first]);
-                            if (sl.n == 2) umma_commit(&T.dfull[1]);
-                        }
+                        if (c == 1 && kb + 1 == blocks) umma_commit(&T.dfull[turn]);
                     }
                     __syncwarp();
                 }
@@ -504,12 +552,17 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         // -------------------------------------------------------- results
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        // A group waits on a barrier of its own: its units' sums follow one another
+        // there, and the next ones cannot be complete before it has read these,
+        // since three units never fit into two slots.
         Slots sl;
+        uint32_t mine = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        for (int u = blockIdx.x, turn = 0; u < total && ok; u += gridDim.x, turn ^= 1) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
             sl.take(U.n);
+            if (turn != half) continue;           // the other group's unit
             // the rows' powers of two, and the tokens'
             float row_scale[2];
 #pragma unroll
@@ -533,45 +586,30 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             }
             there = __all_sync(0xffffffffu, there);
             __syncwarp();
-            for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dfull[sl.first + k], sl.parity(sl.first + k));
+            ok = wait(&T.dfull[half], mine++ & 1);
             if (!ok) break;
             tc_fence_after();
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
-            for (int t0 = half * 16; t0 < U.n; t0 += 32) {
+            for (int t0 = 0; t0 < U.n; t0 += 16) {
                 uint32_t v0[16], v1[16];
                 tmem_ld16(tmem + lanes + d_col(0, sl.first) + t0, v0);
                 tmem_ld16(tmem + lanes + d_col(1, sl.first) + t0, v1);
                 tmem_ld_wait();
-                YT *at = y + (size_t)t0 * p.rows + r;
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    if (t0 + i >= U.n) break;
-                    const float2 f = *reinterpret_cast<const float2 *>(tok + t0 + i);
-                    float a0 = __uint_as_float(v0[i]) * row_scale[0] * f.x, b0 = __uint_as_float(v0[i + 1]) * row_scale[0] * f.y;
-                    float a1 = __uint_as_float(v1[i]) * row_scale[1] * f.x, b1 = __uint_as_float(v1[i + 1]) * row_scale[1] * f.y;
-                    if (!there) {                 // such tokens stand for zeros
-                        if (f.x == 0.f) a0 = a1 = 0.f;
-                        if (f.y == 0.f) b0 = b1 = 0.f;
-                    }
-                    if constexpr (kUp) {
-                        if (r < p.rows) {
-                            at[0] = silu_mul(a0, a1);
-                            if (t0 + i + 1 < U.n) at[p.rows] = silu_mul(b0, b1);
-                        }
-                    } else {
-                        store_pair(at, p.rows, a0, b0, r < p.rows, t0 + i + 1 < U.n);
-                        store_pair(at + kRows, p.rows, a1, b1, r + kRows < p.rows, t0 + i + 1 < U.n);
-                    }
-                    at += 2 * p.rows;
+                if (t0 + 16 >= U.n) {             // all of it in registers: the slot is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
                 }
+                // a whole step of tokens that are all there has no branch in it
+                if (t0 + 16 <= U.n && there)
+                    store_step<kUp, true>(p, y + (size_t)t0 * p.rows + r, r, 16, tok + t0, row_scale, T.turn[warp], v0, v1);
+                else
+                    store_step<kUp, false>(p, y + (size_t)t0 * p.rows + r, r, U.n - t0, tok + t0, row_scale, T.turn[warp], v0, v1);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
-            sl.done();
+            __syncwarp();                         // tok is read
         }
     }
     tc_fence_before();
