@@ -1,13 +1,13 @@
 """Routing and 4-bit operators on the GPU against plain 64-bit forms.
 
 Tolerances. A rounding to BF16 is off by at most 2^-8 of the value. A product with 4-bit weights takes x in
-fixed point, for each 128 columns off by at most 2^-22 of their largest |x|; the sums of a group are exact,
-and in FP32 follow, for each of the three digits of x, one scaled sum per group (at most cols / 32, each two
-roundings of 2^-24 and the addition's) and the joining of digits and of at most 16 column shares, all
-relative to S = sum |W| |x| (a digit's own sum of magnitudes is below 2 S): in all less than
-(cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-22 max|x|. Batches on the tensor cores (BF16 results)
-round each weight to FP16, 2^-11 S more, and have the same FP32 sums of cols / 16 partial sums. For the FFN
-the errors of both sums go through SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|;
+fixed point, for each 128 columns off by at most 2^-14 of their largest |x| (2^-22 for FP32 results, which take
+one digit more); the sums of a group are exact, and in FP32 follow, for each digit group of x, one scaled sum
+per group of weights (at most cols / 32, each two roundings of 2^-24 and the addition's) and the joining of
+digits and of at most 16 column shares, all relative to S = sum |W| |x| (a digit's own sum of magnitudes is
+below 2 S): in all less than (cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-14 (or 2^-22) max|x|.
+Batches on the tensor cores (BF16 results) round each weight to FP16, 2^-11 S, have x exact to 2^-30 of a row's
+largest value, and FP32 sums of cols / 16 partial sums. For the FFN the errors of both sums go through SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|;
 the hardware exponential and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst;
 all of it goes through |W_d|.
 """
@@ -156,17 +156,17 @@ def make_w4(g, lead, rows, cols, group, zeros):
     return kmoe.W4(codes, scales, z)
 
 
-def sums_bound(x, w, cols, tensor_cores=False):
+def sums_bound(x, w, cols, tensor_cores=False, y_dtype=torch.bfloat16):
     top = x.abs().unflatten(-1, (-1, 128)).amax(-1).repeat_interleave(128, -1)
     each = (cols / 16 + cols / 32 + 8) * 2.0 ** -23 + (2.0 ** -11 if tensor_cores else 0)
-    return (each * x.abs() + 2.0 ** -22 * top) @ w.abs().t()
+    return (each * x.abs() + (2.0 ** -22 if y_dtype == torch.float32 else 2.0 ** -14) * top) @ w.abs().t()
 
 
 def check_linear(y, x, w, cols, rows=None):
     """rows: rows of the call (those of y, unless y is a part of them)."""
     ref = x @ w.t()
     tc = kmoe.moe_linear_w4_workspace_size(rows or y.shape[0], rows or y.shape[0], cols, y.dtype) > 0
-    tol = sums_bound(x, w, cols, tc) + (BF16 * ref.abs() if y.dtype == torch.bfloat16 else 0) + 1e-30
+    tol = sums_bound(x, w, cols, tc, y.dtype) + (BF16 * ref.abs() if y.dtype == torch.bfloat16 else 0) + 1e-30
     assert torch.isfinite(y).all()
     off = (y.double() - ref).abs() / tol
     assert off.max() <= 1, float(off.max())
