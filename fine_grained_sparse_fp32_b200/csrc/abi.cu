@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 
 namespace kmoe {
@@ -186,16 +185,27 @@ static size_t h_bytes(int w_dtype)
 // (BF16-precision) activations: below kTcMinTokens tokens.
 static bool two_term(int w_dtype, int N) { return w_dtype == KMOE_E4M3_B128 && N < kTcMinTokens; }
 
-// From this many tokens 4-bit experts run on the tensor-core kernel.
-static const int kW4TcTokens = getenv("W4TC") ? atoi(getenv("W4TC")) : 128;
-static const int kW4TcLin = getenv("W4TCL") ? atoi(getenv("W4TCL")) : 64;
+// Whether P rows of a product with E matrices of `unit_rows` 256-row units (128
+// for gate and up) go to the tensor-core kernel. It unpacks a weight once for up
+// to 128 rows and costs nearly the same for one; the kernel for few tokens pays
+// for every four rows, more with small groups. Measured on the layer's FFN (384
+// experts): groups of 128, 8 rows an expert 243 us against 327 us here, 16 rows
+// 408 against 344; groups of 32, 4 rows 317 against 401, 8 rows 463 against 413.
+// One matrix has few units to deal out, and the more rows are needed the fewer
+// there are: 24 units (6144 x 2560) meet at 100 rows (31 us), 10 (2560 x 6144) at
+// 200 (65 us), 2 (512 x 2560) at 1200 (33 us).
+static bool w4_tensor_cores(int P, int E, int units, int group)
+{
+    const int rows = group == 32 ? 7 : group == 64 ? 9 : 12;
+    return (long long)P * units >= ((long long)rows * units * E + 2200);
+}
 
 // The grouped FFN's scratch after the status block: H [N*K + N, I] and, with
 // FP8 activations, H's scales [N*K + N, I / 128], x's codes [N, d] and x's
 // scales [N, d / 128]. In two-term mode H's two bytes per element are its
 // high and low code planes (each [N*K + N, I]) and x has low codes as well.
-// 4-bit weights on the tensor cores: H in FP32, x in FP16 in xq, and a power of
-// two for every row of both in xs and hs.
+// 4-bit weights: H in FP32; for the tensor cores x in FP16 in xq, and a power
+// of two for every row of both in xs and hs.
 struct FfnScratch {
     void *h;
     float *hs;
@@ -214,7 +224,7 @@ static FfnScratch take_ffn_scratch(Carver &c, int N, int d, int K, int I, int w_
         if (two_term(w_dtype, N)) f.xl = c.take<uint8_t>((size_t)N * d);
         f.xs = c.take<float>((size_t)N * (d / 128));
     }
-    if (w_dtype == KMOE_W4 && N >= kW4TcTokens) {
+    if (w_dtype == KMOE_W4) {
         f.hs = c.take<float>(R);
         f.xq = c.take<uint8_t>((size_t)N * d * 2);
         f.xs = c.take<float>(N);
@@ -222,9 +232,12 @@ static FfnScratch take_ffn_scratch(Carver &c, int N, int d, int K, int I, int w_
     return f;
 }
 
-// Rows of BF16 products from which moe_linear_w4 takes the tensor-core kernel
-// (its FP16 weights are not exact enough for FP32 results).
-static bool linear_w4_tc(int N, int P, int y_dtype) { return y_dtype == KMOE_BF16 && P >= kW4TcLin && N > 0; }
+// FP32 results stay on the kernel for few tokens: FP16 weights are not exact
+// enough for them.
+static bool linear_w4_tc(int N, int P, int rows, int E, int group, int y_dtype)
+{
+    return y_dtype == KMOE_BF16 && N > 0 && w4_tensor_cores(P, E, (rows + 255) / 256, group);
+}
 
 // Bytes of a moe_grouped_ffn workspace: the status block, then the scratch.
 static size_t ffn_ws_bytes(int N, int d, int K, int I, int w_dtype)
@@ -297,14 +310,13 @@ static FfnPath ffn_path(int x_dtype, int w_dtype, int N, int d)
 
 // Grouped FFN with 4-bit weights: H = SiLU(W_g x) * (W_u x) for routed and
 // shared rows in one launch, then both down projections in another, H in FP32;
-// below kW4TcTokens tokens on the kernel for few tokens, from there on the
-// tensor-core kernel. The device status word is cleared by the first launch if
-// `clear` is set.
+// on the kernel for few tokens or the one on the tensor cores. The device status
+// word is cleared by the first launch if `clear` is set.
 static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E, int K, const int32_t *perm,
                               const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, const FfnScratch &f, void *y_perm,
                               void *y_shared, int *status, bool clear, cudaStream_t st)
 {
-    const bool tc = N >= kW4TcTokens;
+    const bool tc = w4_tensor_cores(N * K, E, (I + 127) / 128, r[0].group);
     W4Product a{};
     a.P = N * K;
     a.n_shared = s ? N : 0;
@@ -748,9 +760,10 @@ kmoe_status moe_route(const void *logits, int l_dtype, const float *bias, int N,
     return launch_route(logits, l_dtype, bias, N, E, K, *routing, topk_idx, topk_w, static_cast<cudaStream_t>(stream));
 }
 
-size_t moe_linear_w4_workspace_size(int N, int P, int cols, int y_dtype)
+size_t moe_linear_w4_workspace_size(int N, int P, int rows, int cols, int E, int group, int y_dtype)
 {
-    if (N < 0 || P < 0 || cols < 128 || cols % 128 || !linear_w4_tc(N, P, y_dtype)) return 0;
+    if (N < 0 || P < 0 || rows < 1 || E < 1 || cols < 128 || cols % 128 || !linear_w4_tc(N, P, rows, E, group, y_dtype))
+        return 0;
     Carver c(nullptr);
     c.take<uint8_t>((size_t)N * cols * 2);
     c.take<float>(N);
@@ -778,7 +791,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     KMOE_TRY(check_ptr(perm_token, "perm_token", true));
     KMOE_TRY(check_ptr(offsets, "offsets", true));
     KMOE_TRY(check_ptr(y, "y"));
-    const size_t need = moe_linear_w4_workspace_size(N, P, cols, y_dtype);
+    const size_t need = moe_linear_w4_workspace_size(N, P, rows, cols, E, w->group, y_dtype);
     if (need) KMOE_TRY(check_ptr(ws, "ws"));
     if (ws_bytes < need) return fail(KMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     W4Product a{};
@@ -794,7 +807,7 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     a.group = w->group;
     a.y = y;
     a.y_dtype = y_dtype;
-    if (linear_w4_tc(N, P, y_dtype)) {
+    if (need) {
         Carver c(ws);
         void *x16 = c.take<uint8_t>((size_t)N * cols * 2);
         return launch_w4_tc(a, x16, c.take<float>(N), nullptr, wait_limit(), static_cast<cudaStream_t>(stream));

@@ -143,7 +143,7 @@ def load(path: str | None = None):
     lib.moe_route.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp]
     lib.moe_linear_w4.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp, sz, vp]
     lib.moe_linear_w4_workspace_size.restype = sz
-    lib.moe_linear_w4_workspace_size.argtypes = [i, i, i, i]
+    lib.moe_linear_w4_workspace_size.argtypes = [i, i, i, i, i, i, i]
     lib.moe_forward_routed.argtypes = [vp, i, i, i, i, i, i, vp, vp, vp, ctypes.POINTER(Experts),
                                        ctypes.POINTER(Experts), vp, i, vp, vp, vp, vp, sz, vp]
     lib.moe_block_forward_routed.argtypes = [vp, i, i, i, i, i, vp, vp, vp, ctypes.c_float, vp, vp,
@@ -565,8 +565,8 @@ def moe_dequant_w4(w4: W4, dtype=torch.bfloat16, out=None, stream=None):
     return out
 
 
-def moe_linear_w4_workspace_size(N, P, cols, y_dtype=torch.bfloat16) -> int:
-    return int(load().moe_linear_w4_workspace_size(N, P, cols, _act_code(y_dtype, "y")))
+def moe_linear_w4_workspace_size(N, P, rows, cols, E=1, group=128, y_dtype=torch.bfloat16) -> int:
+    return int(load().moe_linear_w4_workspace_size(N, P, rows, cols, E, group, _act_code(y_dtype, "y")))
 
 
 def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat16, out=None, ws=None, stream=None):
@@ -593,7 +593,7 @@ def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat
         _dense(out, "out", tuple(_DTYPE_CODES), (P, w4.rows), dev)
     code = _DTYPE_CODES[out.dtype]
     if ws is None and code == KMOE_BF16:
-        need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.cols, code)
+        need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.rows, w4.cols, w4.E, w4.group, code)
         if need:
             with torch.cuda.stream(stream):       # memory of the stream that uses it
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)

@@ -306,7 +306,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,
                           void *y, int y_dtype, void *ws, size_t ws_bytes, void *stream);
-size_t moe_linear_w4_workspace_size(int N, int P, int cols, int y_dtype);
+size_t moe_linear_w4_workspace_size(int N, int P, int rows, int cols, int E, int group, int y_dtype);
 
 /*
  * Weighted combine ("Kolibri 1 Deep Dive", section 1, the layer-output

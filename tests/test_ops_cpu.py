@@ -78,8 +78,10 @@ def test_linear_w4_checks_its_arguments(lib):
                      (dict(w=w4(codes=None)), BAD), (dict(w=w4(scales=OFF)), BAD), (dict(w=w4(zeros=OFF)), BAD)):
         assert linear(lib, **kw) == code, kw
     assert lib.moe_linear_w4(A, 1, 4, 4, 16, 256, 1, None, None, None, A, 1, A, 0, None) == BAD
-    need = kmoe.moe_linear_w4_workspace_size(5000, 5000, 256)
-    assert need >= 5000 * (256 * 2 + 4) and kmoe.moe_linear_w4_workspace_size(5000, 5000, 256, torch.float32) == 0
+    need = kmoe.moe_linear_w4_workspace_size(5000, 5000, 16, 256)
+    assert need >= 5000 * (256 * 2 + 4)
+    assert kmoe.moe_linear_w4_workspace_size(5000, 5000, 16, 256, y_dtype=torch.float32) == 0
+    assert kmoe.moe_linear_w4_workspace_size(4, 4, 16, 256) == 0
     w = w4()
     call = lambda ws, n: lib.moe_linear_w4(A, 1, 5000, 5000, 16, 256, 1, None, None, ctypes.byref(w), A, 1, ws, n, None)
     assert call(A, need - 1) == kmoe.KMOE_ERR_WORKSPACE and call(None, need) == BAD

@@ -7,8 +7,8 @@ per group of weights (at most cols / 32, each two roundings of 2^-24 and the add
 digits and of at most 16 column shares, all relative to S = sum |W| |x| (a digit's own sum of magnitudes is
 below 2 S): in all less than (cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-14 (or 2^-22) max|x|.
 Batches on the tensor cores (BF16 results) round each weight to FP16, 2^-11 S, have x exact to 2^-30 of a row's
-largest value, and FP32 sums of cols / 16 partial sums. For the FFN the errors of both sums go through SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|;
-the hardware exponential and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst;
+largest value, and FP32 sums of cols / 16 partial sums. For the FFN the errors of both sums go through
+SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|; the hardware exponential and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst;
 all of it goes through |W_d|.
 """
 import numpy as np
@@ -163,9 +163,10 @@ def sums_bound(x, w, cols, tensor_cores=False, y_dtype=torch.bfloat16):
 
 
 def check_linear(y, x, w, cols, rows=None):
-    """rows: rows of the call (those of y, unless y is a part of them)."""
+    """rows: rows of the call (those of y, unless y is a part of them). From seven rows on it may run on
+    the tensor cores."""
     ref = x @ w.t()
-    tc = kmoe.moe_linear_w4_workspace_size(rows or y.shape[0], rows or y.shape[0], cols, y.dtype) > 0
+    tc = y.dtype == torch.bfloat16 and (rows or y.shape[0]) >= 7
     tol = sums_bound(x, w, cols, tc, y.dtype) + (BF16 * ref.abs() if y.dtype == torch.bfloat16 else 0) + 1e-30
     assert torch.isfinite(y).all()
     off = (y.double() - ref).abs() / tol
@@ -186,7 +187,7 @@ def test_linear_w4_one_matrix(N, rows, cols):
         assert torch.equal(y, kmoe.moe_linear_w4(x, w, y_dtype=y_dtype))
 
 
-@pytest.mark.parametrize("N,E,K", [(1, 16, 4), (5, 16, 4), (64, 7, 3), (300, 3, 2), (130, 61, 8)])
+@pytest.mark.parametrize("N,E,K", [(1, 16, 4), (5, 16, 4), (64, 7, 3), (300, 3, 2), (130, 61, 8), (2500, 3, 2), (1300, 16, 5)])
 @pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
 @pytest.mark.parametrize("y_dtype", [torch.float32, torch.bfloat16])
 def test_linear_w4_grouped_by_expert(N, E, K, group, zeros, y_dtype):
@@ -227,7 +228,30 @@ def test_linear_w4_leaves_uncovered_rows_and_reads_no_foreign_token():
     assert (kmoe.moe_linear_w4(x[:0], w, perm, torch.tensor([0, 4, 7, 10], dtype=torch.int32, device="cuda")) == 0).all()
 
 
-@pytest.mark.parametrize("N,y_dtype", [(5, torch.float32), (5, torch.bfloat16), (200, torch.bfloat16)])
+def test_linear_w4_many_rows_uncovered_and_foreign():
+    """As above, at a size that runs on the tensor cores (and an odd number of weight rows)."""
+    g = gen(12)
+    N, cols, rows, P = 50, 256, 301, 4000
+    x = randn(g, N, cols).bfloat16()
+    w = make_w4(g, 3, rows, cols, 128, True)
+    assert kmoe.moe_linear_w4_workspace_size(N, P, rows, cols, 3, 128) > 0
+    perm = torch.randint(0, N, (P,), dtype=torch.int32, device="cuda", generator=g)
+    perm[[100, 2000]] = torch.tensor([-1, N], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([70, 150, 150, 3900], dtype=torch.int32, device="cuda")
+    out = torch.full((P, rows), 7.0, device="cuda", dtype=torch.bfloat16)
+    kmoe.moe_linear_w4(x, w, perm, offsets, out=out)
+    assert (out[:70] == 7).all() and (out[3900:] == 7).all() and (out[[100, 2000]] == 0).all()
+    xs = x.double()[perm.clamp(0, N - 1).long()]
+    xs[[100, 2000]] = 0
+    v = plain_ops.w4_values(w.codes, w.scales, w.zeros)
+    check_linear(out[70:150], xs[70:150], v[0], cols, rows=P)
+    check_linear(out[150:3900], xs[150:3900], v[2], cols, rows=P)
+    again = torch.full_like(out, 7.0)
+    kmoe.moe_linear_w4(x, w, perm, offsets, out=again)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("N,y_dtype", [(5, torch.float32), (5, torch.bfloat16), (2500, torch.bfloat16)])
 def test_linear_w4_takes_wide_ranges_of_values(N, y_dtype):
     """Large and tiny x and scales: sums stay in FP32 range and keep their relative accuracy."""
     g = gen(3)
@@ -241,7 +265,7 @@ def test_linear_w4_takes_wide_ranges_of_values(N, y_dtype):
     check_linear(y, x.double(), plain_ops.w4_values(w.codes[0], w.scales[0]), 512)
 
 
-@pytest.mark.parametrize("N", [6, 200])
+@pytest.mark.parametrize("N", [6, 2500])
 def test_linear_w4_keeps_non_finite_rows_to_themselves(N):
     g = gen(6)
     x = randn(g, N, 384).bfloat16()
@@ -285,13 +309,13 @@ def check_ffn(layer, N, K, E, seed, with_shared=True, handle=None):
             assert ys is None
             continue
         if rows.shape[0]:
-            ref, tol = ffn_ref(rows.double(), layer, e, N >= 128)
+            ref, tol = ffn_ref(rows.double(), layer, e, N * K >= 7 * E)
             off_by = ((got.double() - ref).abs() / tol).max()
             assert off_by <= 1, (e, float(off_by))
     return x, perm, offsets, y, ys
 
 
-@pytest.mark.parametrize("N", [1, 2, 9, 40, 130, 260, 700])
+@pytest.mark.parametrize("N", [1, 2, 9, 40, 130, 260, 700, 1500])
 @pytest.mark.parametrize("d,I,E,K,group,zeros", [(256, 128, 8, 2, 128, False), (384, 256, 5, 3, 32, True),
                                                  (1280, 128, 16, 6, 64, True), (512, 384, 4, 4, 64, False)])
 def test_grouped_ffn_w4(N, d, I, E, K, group, zeros):
