@@ -6,30 +6,56 @@
 // One warp per token. The 32 lanes are shared out evenly among the groups
 // (L = 32 / n_groups rounded down to a power of two, so a group's lanes are
 // neighbours), and lane j of a group holds its experts j, j + L, ... in
-// registers, in ascending order.
+// registers. Each keeps the two best of them in hand, so that a round of the
+// selection is two warp reductions, whatever the number of experts.
+//
+// The choice is the one that FP64 scores make, at the cost of FP32 ones. FP32
+// scores are off by at most D = 2^-20 max s + 2^-22 max |c| (the hardware
+// exponential and reciprocal, the sum; the error of s is s (1 - s) times that of
+// the exponential, or s times it, whose growth with the exponent s outweighs).
+// Where the K + 1 best are further than 2 D apart, and the last group that stays
+// further than 4 D from the first that goes, every exact score has the same
+// order. Any other token (about one in 300) is decided again in FP64. Without a
+// bias the order of scores is that of the logits, which are exact: equal ones
+// are equal in FP64 too, and only logits whose FP64 scores may round to the same
+// number go to FP64: closer than 1e-13, with scores below e^-600, or above 20
+// under a sigmoid.
 #include "permute_dev.cuh"
 #include "w4.cuh"
 
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
 namespace kmoe {
 
-constexpr int kRouteTokens = 8;       // tokens (warps) of a CTA
+constexpr int kRouteWarps = 8;        // tokens in work of a CTA
 
 struct RouteArgs {
     const float *bias;
     int N, E, K, n_groups, topk_groups, size, lanes;   // size: experts of a group; lanes: lanes of a group
     bool softmax, top2, renormalise;
     float scale;
+    int exact_places;                     // doubles of shared memory for a warp's FP64 choice
     int32_t *idx;
     float *w;
     int32_t *hist;
 };
 
-// FP64 value of a selection score: masked experts sort behind all others.
-constexpr double kMasked = -DBL_MAX, kGone = -INFINITY;
+// Whole-number keys in the order of floats; masked experts and empty places
+// come before every float.
+constexpr int kEmpty = INT_MIN, kMaskedKey = INT_MIN + 1;
+__device__ __forceinline__ int key_of(float v)
+{
+    const int b = __float_as_int(v + 0.f);        // -0 and +0 are equal
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float value_of(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
+// sigmoid for the choice: hardware exponential and reciprocal.
+__device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+
+// ------------------------------------------------- FP64 choice of one token
 __device__ __forceinline__ double warp_max(double v)
 {
 #pragma unroll
@@ -37,105 +63,264 @@ __device__ __forceinline__ double warp_max(double v)
     return v;
 }
 
-template <class LT, int NPL>
-__global__ void __launch_bounds__(32 * kRouteTokens)
-route_kernel(const LT *__restrict__ logits, const RouteArgs a)
+// One token's choice by FP64 scores, which lie in shared memory (c, one place
+// for each lane and expert). Lane k returns choice k and its score.
+template <class LT>
+__device__ __noinline__ int route_exact(const LT *lr, const RouteArgs &a, double *c, double *score_out)
 {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kRouteTokens + (threadIdx.x >> 5);
-    if (t >= a.N) return;
-    const int group = lane / a.lanes, sub = lane % a.lanes;
-    const int base = group * a.size;
-    const LT *lr = logits + (size_t)t * a.E;
-    double s[NPL], c[NPL];
-    uint64_t masked = 0;
-    static_assert(NPL <= 64, "mask bits");
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = sub + a.lanes * i;
-        const bool in = group < a.n_groups && e < a.size;
-        s[i] = in ? (double)to_f32(lr[base + e]) : -INFINITY;
-        c[i] = in && a.bias ? (double)a.bias[base + e] : 0.0;
-        if (isnan(s[i])) s[i] = -INFINITY;
-        if (s[i] == -INFINITY || isnan(c[i]) || c[i] == -INFINITY) masked |= 1ull << i;
+    constexpr double kMasked = -DBL_MAX, kGone = -INFINITY;
+    const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes, base = group * a.size;
+    const int per = group < a.n_groups ? (a.size - sub + a.lanes - 1) / a.lanes : 0;
+    auto logit = [&](int e) {
+        const double l = (double)to_f32(lr[e]);
+        return isnan(l) ? -INFINITY : l;
+    };
+    double top = -INFINITY, sum = 0;
+    if (a.softmax) {
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) top = fmax(top, logit(base + sub + a.lanes * i));
+        top = warp_max(top);
+    }
+    auto weight = [&](double l) {                 // before the division by `sum`
+        if (!a.softmax) return 1.0 / (1.0 + exp(-l));
+        return l == -INFINITY ? 0.0 : l == top ? 1.0 : exp(l - top);
+    };
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+        const double w = weight(logit(base + sub + a.lanes * i));
+        c[i * 32 + lane] = w;
+        sum += w;
     }
     if (a.softmax) {
-        double top = -INFINITY, sum = 0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) top = fmax(top, s[i]);
-        top = warp_max(top);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            s[i] = s[i] == -INFINITY ? 0.0 : s[i] == top ? 1.0 : exp(s[i] - top);
-            sum += s[i];
-        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = sum > 0 ? s[i] / sum : 0.0;
     } else {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = 1.0 / (1.0 + exp(-s[i]));
+        sum = 1.0;
     }
-    double m1 = kMasked, m2 = kMasked;            // the two largest unmasked of this lane, then of the group
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = sub + a.lanes * i;
-        const bool in = group < a.n_groups && e < a.size;
-        c[i] = !in ? kGone : (masked >> i & 1) ? kMasked : s[i] + c[i];
-        if ((masked >> i & 1)) s[i] = 0;
-        if (c[i] > m1) { m2 = m1; m1 = c[i]; }
-        else if (c[i] > m2) m2 = c[i];
+    double m1 = kMasked, m2 = kMasked;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+        const int e = base + sub + a.lanes * i;
+        const double b = a.bias ? (double)a.bias[e] : 0.0, w = c[i * 32 + lane];
+        const double v = logit(e) == -INFINITY || isnan(b) || b == -INFINITY ? kMasked
+                         : (a.softmax ? (sum > 0 ? w / sum : 0.0) : w) + b;
+        c[i * 32 + lane] = v;
+        m2 = fmax(m2, fmin(m1, v));
+        m1 = fmax(m1, v);
     }
+    bool stays = true;
     if (a.topk_groups < a.n_groups) {
         for (int o = 1; o < a.lanes; o <<= 1) {
             const double p1 = __shfl_xor_sync(0xffffffffu, m1, o), p2 = __shfl_xor_sync(0xffffffffu, m2, o);
-            m2 = fmax(fmin(m1, p1), m1 > p1 ? m2 : p2);
+            m2 = fmax(fmin(m1, p1), fmax(m2, p2));
             m1 = fmax(m1, p1);
         }
-        const double score = a.top2 && m2 != kMasked ? m1 + m2 : m1;
-        int before = 0;                           // groups that come before this one
+        const double mine = a.top2 && m2 != kMasked ? m1 + m2 : m1;
+        int before = 0;
         for (int g = 0; g < a.n_groups; ++g) {
-            const double o = __shfl_sync(0xffffffffu, score, g * a.lanes);
-            before += o > score || (o == score && g < group);
+            const double o = __shfl_sync(0xffffffffu, mine, g * a.lanes);
+            before += o > mine || (o == mine && g < group);
         }
-        if (before >= a.topk_groups)
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) c[i] = kGone;
+        stays = before < a.topk_groups;
     }
-    double sel = 0, sum = 0;                      // lane k keeps choice k
     int chosen = 0;
+    bool ok = false;
     for (int k = 0; k < a.K; ++k) {
-        double bc = kGone, bs = 0;
-        int be = INT_MAX;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (c[i] > bc) { bc = c[i]; be = base + sub + a.lanes * i; bs = s[i]; }
-        const double top = warp_max(bc);
-        const int e = __reduce_min_sync(0xffffffffu, bc == top ? be : INT_MAX);
-        const int owner = __ffs(__ballot_sync(0xffffffffu, bc == top && be == e)) - 1;
-        bs = __shfl_sync(0xffffffffu, bs, owner);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (base + sub + a.lanes * i == e && lane == owner) c[i] = kGone;
-        if (lane == k) { sel = bs; chosen = e; }
-        sum += bs;
+        double bc = kGone;
+        int bi = 0;
+        if (stays) {
+#pragma unroll 4
+            for (int i = 0; i < per; ++i) {
+                const double v = c[i * 32 + lane];
+                if (v > bc) { bc = v; bi = i; }
+            }
+        }
+        const double best = warp_max(bc);
+        const int be = base + sub + a.lanes * bi, e = __reduce_min_sync(0xffffffffu, bc == best ? be : INT_MAX);
+        if (bc == best && be == e) c[bi * 32 + lane] = kGone;
+        if (lane == k) { chosen = e; ok = best != kMasked; }
     }
-    if (lane < a.K) {
-        if (a.renormalise) sel = sum > 0 ? sel / sum : 0.0;
-        a.idx[(size_t)t * a.K + lane] = chosen;
-        a.w[(size_t)t * a.K + lane] = (float)(sel * (double)a.scale);
-        if (a.hist) atomicAdd(a.hist + (size_t)(t / kChunk) * a.E + chosen, 1);   // whole numbers: exact in any order
+    *score_out = lane < a.K && ok ? (sum > 0 ? weight(logit(chosen)) / sum : 0.0) : 0.0;
+    return chosen;
+}
+
+// ------------------------------------------------------------------ kernel
+// The two best of a lane's keys, ties to the lower index.
+template <int NPL>
+__device__ __forceinline__ void best_two(const int (&key)[NPL], uint64_t gone, int &m1, int &m2, int &i1, int &i2)
+{
+    m1 = m2 = kEmpty;
+    i1 = i2 = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int k = gone >> i & 1 ? kEmpty : key[i];
+        const bool first = k > m1, second = k > m2;
+        if (second) { m2 = first ? m1 : k; i2 = first ? i1 : i; }
+        if (first) { m1 = k; i1 = i; }
     }
 }
 
-template <class LT>
-static kmoe_status run_route(const LT *logits, const RouteArgs &a, cudaStream_t st)
+template <class LT, int NPL, bool kBias>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+route_kernel(const LT *__restrict__ logits, const RouteArgs a)
 {
-    const int grid = (a.N + kRouteTokens - 1) / kRouteTokens, npl = (a.size + a.lanes - 1) / a.lanes;
-#define KMOE_ROUTE(n) launch_pdl(route_kernel<LT, n>, grid, 32 * kRouteTokens, 0, st, logits, a)
+    extern __shared__ double exact_c[];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int group = lane / a.lanes, sub = lane % a.lanes, base = group * a.size;
+    const int per = group < a.n_groups ? (a.size - sub + a.lanes - 1) / a.lanes : 0;      // this lane's experts
+    float b[kBias ? NPL : 1], b_max = 0.f;
+    if (kBias) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            b[i] = i < per ? a.bias[base + sub + a.lanes * i] : 0.f;
+            if (b[i] > -INFINITY) b_max = fmaxf(b_max, fabsf(b[i]));
+        }
+        b_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b_max)));
+    }
+    const int step = gridDim.x * kRouteWarps;
+    for (int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < a.N; t += step) {
+        const LT *lr = logits + (size_t)t * a.E;
+        int key[NPL];
+        float s_max = 1.f, top = -INFINITY, sum = 0.f;
+        {
+            float l[NPL];
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) l[i] = i < per ? to_f32(lr[base + sub + a.lanes * i]) : -INFINITY;
+            if (a.softmax) {
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) top = fmaxf(top, l[i]);         // fmaxf drops NaN
+                top = value_of(__reduce_max_sync(0xffffffffu, key_of(top)));
+                if (kBias || !a.renormalise) {
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) {
+                        const float e = l[i] > -INFINITY ? (l[i] == top ? 1.f : __expf(l[i] - top)) : 0.f;
+                        sum += e;
+                        if (kBias) key[i] = __float_as_int(e);
+                    }
+                    sum = warp_sum(sum);
+                    s_max = sum > 0.f ? 1.f / sum : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const bool ok = l[i] > -INFINITY && (!kBias || b[kBias ? i : 0] > -INFINITY);
+                float c = l[i];
+                if (kBias) c = (a.softmax ? __int_as_float(key[i]) * s_max : quick_sigmoid(l[i])) + b[kBias ? i : 0];
+                key[i] = i >= per ? kEmpty : ok ? key_of(c) : kMaskedKey;
+            }
+        }
+        const float D = s_max * 0x1p-20f + (s_max + b_max) * 0x1p-22f + 1e-36f;
+        // whether two neighbours' order is not the exact one for sure (hi >= lo)
+        auto unsure = [&](float hi, float lo, float width) {
+            const float d = hi - lo;
+            if (kBias) return !(d > width);
+            return d != 0.f && (!(d > 1e-13f) || (a.softmax ? hi - top < -600.f : lo > 20.f || hi < -600.f));
+        };
+        int m1, m2, i1, i2;
+        best_two(key, 0, m1, m2, i1, i2);
+        bool again = false, stays = true;
+        if (a.topk_groups < a.n_groups) {
+            int g1 = m1, g2 = m2;
+            for (int o = 1; o < a.lanes; o <<= 1) {
+                const int p1 = __shfl_xor_sync(0xffffffffu, g1, o), p2 = __shfl_xor_sync(0xffffffffu, g2, o);
+                g2 = max(min(g1, p1), max(g2, p2));
+                g1 = max(g1, p1);
+            }
+            int mine = g1;                        // group score as a key
+            const bool sums = a.top2 && g1 > kMaskedKey;
+            if (sums) {
+                float v1 = value_of(g1), v2 = value_of(g2);
+                if (!kBias) {                     // logits: their scores, the softmax's up to its divisor
+                    v1 = a.softmax ? __expf(v1 - top) : quick_sigmoid(v1);
+                    v2 = a.softmax ? __expf(v2 - top) : quick_sigmoid(v2);
+                }
+                mine = key_of(g2 > kMaskedKey ? v1 + v2 : v1);
+            }
+            if (group >= a.n_groups) mine = kEmpty;
+            int before = 0;
+            for (int g = 0; g < a.n_groups; ++g) {
+                const int o = __shfl_sync(0xffffffffu, mine, g * a.lanes);
+                before += o > mine || (o == mine && g < group);
+            }
+            stays = group < a.n_groups && before < a.topk_groups;
+            const int last = __reduce_min_sync(0xffffffffu, stays ? mine : INT_MAX);
+            const int next = __reduce_max_sync(0xffffffffu, stays ? kEmpty : mine);
+            if (next > kMaskedKey) {              // (masked groups come last in order of their index)
+                const float hi = value_of(last), lo = value_of(next);
+                if (kBias || !a.top2) again = unsure(hi, lo, 4 * D);
+                else again = !(hi - lo > 4 * (0x1p-20f + 0x1p-22f));
+            }
+            if (!stays) m1 = m2 = kEmpty;
+        }
+        uint64_t gone = 0;
+        int chosen = 0, prev = INT_MAX;
+        for (int k = 0; k <= a.K; ++k) {
+            const int best = __reduce_max_sync(0xffffffffu, m1);
+            if (k > 0 && best > kMaskedKey) again |= unsure(value_of(prev), value_of(best), 2 * D);
+            if (k == a.K || best == kEmpty) break;
+            const int e = __reduce_min_sync(0xffffffffu, m1 == best ? base + sub + a.lanes * i1 : INT_MAX);
+            if (lane == k) chosen = e;
+            prev = best;
+            const bool owner = m1 == best && base + sub + a.lanes * i1 == e;
+            if (owner) {
+                gone |= 1ull << i1;
+                m1 = m2;
+                i1 = i2;
+                m2 = kEmpty;
+            }
+            // a lane whose two best are both gone looks for the next ones
+            if (__any_sync(0xffffffffu, owner && m1 == kEmpty)) {
+                int n1, n2, j1, j2;
+                best_two(key, gone, n1, n2, j1, j2);
+                if (owner) { m1 = n1; m2 = n2; i1 = j1; i2 = j2; }
+            }
+        }
+        float s = 0.f;                            // score of choice `lane`
+        if (!again && lane < a.K) {
+            const float l = to_f32(lr[chosen]);
+            const bool ok = l > -INFINITY && (!kBias || a.bias[chosen] > -INFINITY);
+            if (ok && !a.softmax) s = sigmoidf_(l);
+            if (ok && a.softmax) s = (l == top ? 1.f : expf(l - top)) / (a.renormalise ? 1.f : sum);
+        }
+        const float total = warp_sum(s);          // 0 from lanes without a choice
+        if (again || (a.renormalise && total < 1e-30f)) {     // scores that FP32 cannot weigh against each other, too
+            double exact;
+            chosen = route_exact(lr, a, exact_c + (threadIdx.x >> 5) * a.exact_places, &exact);
+            if (a.renormalise) {
+                double all = lane < a.K ? exact : 0.0;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                exact = all > 0 ? exact / all : 0.0;
+            }
+            s = (float)exact;
+        } else if (a.renormalise) {
+            s /= total;
+        }
+        if (lane < a.K) {
+            a.idx[(size_t)t * a.K + lane] = chosen;
+            a.w[(size_t)t * a.K + lane] = s * a.scale;
+            if (a.hist) atomicAdd(a.hist + (size_t)(t / kChunk) * a.E + chosen, 1);   // whole numbers: exact in any order
+        }
+    }
+}
+
+template <class LT, bool kBias>
+static kmoe_status run_route(const LT *logits, RouteArgs a, cudaStream_t st)
+{
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // a few tokens for each warp, so that the bias is read once for them
+    const int grid = std::min((a.N + kRouteWarps - 1) / kRouteWarps, sms * 8), npl = (a.size + a.lanes - 1) / a.lanes;
+    a.exact_places = npl * 32;
+    const int smem = kRouteWarps * a.exact_places * (int)sizeof(double);
+#define KMOE_ROUTE(n)                                                                                                 \
+    do {                                                                                                              \
+        if (smem > 48 << 10)                                                                                          \
+            cudaFuncSetAttribute(route_kernel<LT, n, kBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);      \
+        launch_pdl(route_kernel<LT, n, kBias>, grid, 32 * kRouteWarps, smem, st, logits, a);                          \
+    } while (0)
     if (npl <= 2) KMOE_ROUTE(2);
     else if (npl <= 4) KMOE_ROUTE(4);
     else if (npl <= 8) KMOE_ROUTE(8);
@@ -167,8 +352,12 @@ kmoe_status launch_route(const void *logits, int l_dtype, const float *bias, int
     a.idx = idx;
     a.w = w;
     a.hist = hist;
-    if (l_dtype == KMOE_F32) return run_route(static_cast<const float *>(logits), a, st);
-    return run_route(static_cast<const __nv_bfloat16 *>(logits), a, st);
+    if (l_dtype == KMOE_F32) {
+        const float *l = static_cast<const float *>(logits);
+        return bias ? run_route<float, true>(l, a, st) : run_route<float, false>(l, a, st);
+    }
+    const __nv_bfloat16 *l = static_cast<const __nv_bfloat16 *>(logits);
+    return bias ? run_route<__nv_bfloat16, true>(l, a, st) : run_route<__nv_bfloat16, false>(l, a, st);
 }
 
 }  // namespace kmoe

@@ -109,7 +109,7 @@ def test_route_ties_masks_and_non_finite_logits(score):
     inf, nan = float("inf"), float("nan")
     E, K = 64, 6
     g = gen(5)
-    logits = randn(g, 12, E)
+    logits = randn(g, 14, E)
     logits[0] = 0.25                                         # all equal: lowest indices
     logits[1] = -inf                                         # nothing left: experts 0.., weight 0
     logits[2, 3:] = -inf                                     # fewer than K left
@@ -122,6 +122,8 @@ def test_route_ties_masks_and_non_finite_logits(score):
     logits[9] = 1.0 + torch.randint(0, 3, (E,), device="cuda", generator=g) * 2.0 ** -23   # neighbours in FP32
     logits[10, :60] = -inf
     logits[11] = -88.0 - torch.rand(E, device="cuda", generator=g)
+    logits[12] = -700.0 - torch.arange(E, device="cuda")     # scores that are 0 in FP64 from somewhere on
+    logits[13] = -torch.arange(E, device="cuda") * 40.0
     bias = torch.rand(E, device="cuda", generator=g) * 0.1
     off = bias.clone()
     off[torch.arange(0, E, 3)] = -inf
