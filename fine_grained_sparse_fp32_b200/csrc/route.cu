@@ -29,7 +29,7 @@
 
 namespace kmoe {
 
-constexpr int kRouteWarps = 8;        // tokens in work of a CTA
+constexpr int kRouteWarps = 8, kRouteCtas = 4;       // tokens in work of a CTA, CTAs of an SM
 
 struct RouteArgs {
     const float *bias;
@@ -42,18 +42,30 @@ struct RouteArgs {
     int32_t *hist;
 };
 
-// Whole-number keys in the order of floats; masked experts and empty places
-// come before every float.
-constexpr int kEmpty = INT_MIN, kMaskedKey = INT_MIN + 1;
-__device__ __forceinline__ int key_of(float v)
+// Whole-number keys in the order of floats. Masked experts and empty places
+// have the key of -inf, chosen ones and groups that go one below every float.
+constexpr int kGoneKey = INT_MIN, kMaskedKey = (int)(0xff800000u ^ 0x7fffffffu);
+__device__ __forceinline__ int key_of(float v)    // v is not -0
 {
-    const int b = __float_as_int(v + 0.f);        // -0 and +0 are equal
+    const int b = __float_as_int(v);
     return b ^ ((b >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float value_of(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// sigmoid for the choice: hardware exponential and reciprocal.
-__device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// Hardware exponential and reciprocal, for the choice: results below 2^-126
+// become 0, which D allows for.
+__device__ __forceinline__ float quick_exp(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+__device__ __forceinline__ float quick_sigmoid(float l)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + quick_exp(-l)));
+    return y;
+}
 
 // ------------------------------------------------- FP64 choice of one token
 __device__ __forceinline__ double warp_max(double v)
@@ -149,19 +161,21 @@ __device__ __noinline__ int route_exact(const LT *lr, const RouteArgs &a, double
 template <int NPL>
 __device__ __forceinline__ void best_two(const int (&key)[NPL], uint64_t gone, int &m1, int &m2, int &i1, int &i2)
 {
-    m1 = m2 = kEmpty;
+    m1 = m2 = kGoneKey;
     i1 = i2 = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        const int k = gone >> i & 1 ? kEmpty : key[i];
+        const int k = gone >> i & 1 ? kGoneKey : key[i];
         const bool first = k > m1, second = k > m2;
         if (second) { m2 = first ? m1 : k; i2 = first ? i1 : i; }
         if (first) { m1 = k; i1 = i; }
     }
 }
 
+// Four CTAs an SM (64 registers): at 2 (120 registers) 65536 tokens took 127
+// us, not 111.
 template <class LT, int NPL, bool kBias>
-__global__ void __launch_bounds__(32 * kRouteWarps)
+__global__ void __launch_bounds__(32 * kRouteWarps, NPL <= 16 ? kRouteCtas : 2)
 route_kernel(const LT *__restrict__ logits, const RouteArgs a)
 {
     extern __shared__ double exact_c[];
@@ -174,28 +188,28 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
     if (kBias) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            b[i] = i < per ? a.bias[base + sub + a.lanes * i] : 0.f;
+            b[i] = fmaxf(i < per ? a.bias[base + sub + a.lanes * i] : 0.f, -INFINITY);    // NaN becomes -inf
             if (b[i] > -INFINITY) b_max = fmaxf(b_max, fabsf(b[i]));
         }
         b_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b_max)));
     }
     const int step = gridDim.x * kRouteWarps;
     for (int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < a.N; t += step) {
-        const LT *lr = logits + (size_t)t * a.E;
+        const LT *lr = logits + (size_t)t * a.E, *mine_of = lr + base + sub;
         int key[NPL];
         float s_max = 1.f, top = -INFINITY, sum = 0.f;
         {
             float l[NPL];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) l[i] = i < per ? to_f32(lr[base + sub + a.lanes * i]) : -INFINITY;
+            for (int i = 0; i < NPL; ++i) l[i] = i < per ? to_f32(mine_of[a.lanes * i]) : -INFINITY;
             if (a.softmax) {
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) top = fmaxf(top, l[i]);         // fmaxf drops NaN
-                top = value_of(__reduce_max_sync(0xffffffffu, key_of(top)));
+                top = value_of(__reduce_max_sync(0xffffffffu, key_of(top + 0.f)));
                 if (kBias || !a.renormalise) {
 #pragma unroll
                     for (int i = 0; i < NPL; ++i) {
-                        const float e = l[i] > -INFINITY ? (l[i] == top ? 1.f : __expf(l[i] - top)) : 0.f;
+                        const float e = l[i] > -INFINITY ? (l[i] == top ? 1.f : quick_exp(l[i] - top)) : 0.f;
                         sum += e;
                         if (kBias) key[i] = __float_as_int(e);
                     }
@@ -205,10 +219,12 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
             }
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                const bool ok = l[i] > -INFINITY && (!kBias || b[kBias ? i : 0] > -INFINITY);
-                float c = l[i];
-                if (kBias) c = (a.softmax ? __int_as_float(key[i]) * s_max : quick_sigmoid(l[i])) + b[kBias ? i : 0];
-                key[i] = i >= per ? kEmpty : ok ? key_of(c) : kMaskedKey;
+                float c = fmaxf(l[i], -INFINITY) + 0.f;                       // no NaN, no -0
+                if (kBias) {
+                    c = (a.softmax ? __int_as_float(key[i]) * s_max : quick_sigmoid(l[i])) + b[kBias ? i : 0];
+                    c = l[i] > -INFINITY ? c : -INFINITY;
+                }
+                key[i] = key_of(c);
             }
         }
         const float D = s_max * 0x1p-20f + (s_max + b_max) * 0x1p-22f + 1e-36f;
@@ -220,7 +236,7 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         };
         int m1, m2, i1, i2;
         best_two(key, 0, m1, m2, i1, i2);
-        bool again = false, stays = true;
+        bool again = false;
         if (a.topk_groups < a.n_groups) {
             int g1 = m1, g2 = m2;
             for (int o = 1; o < a.lanes; o <<= 1) {
@@ -233,56 +249,66 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
             if (sums) {
                 float v1 = value_of(g1), v2 = value_of(g2);
                 if (!kBias) {                     // logits: their scores, the softmax's up to its divisor
-                    v1 = a.softmax ? __expf(v1 - top) : quick_sigmoid(v1);
-                    v2 = a.softmax ? __expf(v2 - top) : quick_sigmoid(v2);
+                    v1 = a.softmax ? (v1 == top ? 1.f : quick_exp(v1 - top)) : quick_sigmoid(v1);
+                    v2 = a.softmax ? (v2 == top ? 1.f : quick_exp(v2 - top)) : quick_sigmoid(v2);
                 }
-                mine = key_of(g2 > kMaskedKey ? v1 + v2 : v1);
+                mine = key_of((g2 > kMaskedKey ? v1 + v2 : v1) + 0.f);
             }
-            if (group >= a.n_groups) mine = kEmpty;
+            if (group >= a.n_groups) mine = kGoneKey;
             int before = 0;
             for (int g = 0; g < a.n_groups; ++g) {
                 const int o = __shfl_sync(0xffffffffu, mine, g * a.lanes);
                 before += o > mine || (o == mine && g < group);
             }
-            stays = group < a.n_groups && before < a.topk_groups;
+            const bool stays = group < a.n_groups && before < a.topk_groups;
             const int last = __reduce_min_sync(0xffffffffu, stays ? mine : INT_MAX);
-            const int next = __reduce_max_sync(0xffffffffu, stays ? kEmpty : mine);
+            const int next = __reduce_max_sync(0xffffffffu, stays ? kGoneKey : mine);
             if (next > kMaskedKey) {              // (masked groups come last in order of their index)
                 const float hi = value_of(last), lo = value_of(next);
                 if (kBias || !a.top2) again = unsure(hi, lo, 4 * D);
                 else again = !(hi - lo > 4 * (0x1p-20f + 0x1p-22f));
             }
-            if (!stays) m1 = m2 = kEmpty;
+            if (!stays) m1 = m2 = kGoneKey;
         }
         uint64_t gone = 0;
-        int chosen = 0, prev = INT_MAX;
-        for (int k = 0; k <= a.K; ++k) {
+        int chosen = 0;
+        float prev = INFINITY, gap = INFINITY;    // gap: between neighbours in the order
+        for (int k = 0;; ++k) {
             const int best = __reduce_max_sync(0xffffffffu, m1);
-            if (k > 0 && best > kMaskedKey) again |= unsure(value_of(prev), value_of(best), 2 * D);
-            if (k == a.K || best == kEmpty) break;
-            const int e = __reduce_min_sync(0xffffffffu, m1 == best ? base + sub + a.lanes * i1 : INT_MAX);
+            const float v = value_of(best);
+            if (best > kMaskedKey) {
+                if (kBias) gap = fminf(gap, prev - v);
+                else if (k > 0) again |= unsure(prev, v, 0.f);
+            }
+            if (k == a.K) break;
+            if (best <= kMaskedKey) {             // fewer than K experts to choose from: masked ones in order
+                again = true;
+                break;
+            }
+            const int mine = base + sub + a.lanes * i1;
+            const int e = __reduce_min_sync(0xffffffffu, m1 == best ? mine : INT_MAX);
             if (lane == k) chosen = e;
-            prev = best;
-            const bool owner = m1 == best && base + sub + a.lanes * i1 == e;
+            prev = v;
+            const bool owner = m1 == best && mine == e;
             if (owner) {
                 gone |= 1ull << i1;
                 m1 = m2;
                 i1 = i2;
-                m2 = kEmpty;
+                m2 = kGoneKey;
             }
             // a lane whose two best are both gone looks for the next ones
-            if (__any_sync(0xffffffffu, owner && m1 == kEmpty)) {
+            if (__any_sync(0xffffffffu, owner && m1 == kGoneKey)) {
                 int n1, n2, j1, j2;
                 best_two(key, gone, n1, n2, j1, j2);
                 if (owner) { m1 = n1; m2 = n2; i1 = j1; i2 = j2; }
             }
         }
+        if (kBias) again |= !(gap > 2 * D);
         float s = 0.f;                            // score of choice `lane`
         if (!again && lane < a.K) {
             const float l = to_f32(lr[chosen]);
-            const bool ok = l > -INFINITY && (!kBias || a.bias[chosen] > -INFINITY);
-            if (ok && !a.softmax) s = sigmoidf_(l);
-            if (ok && a.softmax) s = (l == top ? 1.f : expf(l - top)) / (a.renormalise ? 1.f : sum);
+            if (!a.softmax) s = sigmoidf_(l);
+            else s = (l == top ? 1.f : expf(l - top)) / (a.renormalise ? 1.f : sum);
         }
         const float total = warp_sum(s);          // 0 from lanes without a choice
         if (again || (a.renormalise && total < 1e-30f)) {     // scores that FP32 cannot weigh against each other, too
@@ -311,8 +337,9 @@ static kmoe_status run_route(const LT *logits, RouteArgs a, cudaStream_t st)
 {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // a few tokens for each warp, so that the bias is read once for them
-    const int grid = std::min((a.N + kRouteWarps - 1) / kRouteWarps, sms * 8), npl = (a.size + a.lanes - 1) / a.lanes;
+    // each warp takes the same number of tokens, so that the bias is read once for them
+    const int ctas = (a.N + kRouteWarps - 1) / kRouteWarps, room = sms * kRouteCtas, each = (ctas + room - 1) / room;
+    const int grid = (ctas + each - 1) / each, npl = (a.size + a.lanes - 1) / a.lanes;
     a.exact_places = npl * 32;
     const int smem = kRouteWarps * a.exact_places * (int)sizeof(double);
 #define KMOE_ROUTE(n)                                                                                                 \
