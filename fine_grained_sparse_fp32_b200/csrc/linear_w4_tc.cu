@@ -406,8 +406,12 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 mbar_wait_drain(&T.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
     } else if (warp >= kGatherWarp) {
         // --------------------------------------------------------- gather
-        // 16 threads take the 256 bytes of a row's 128 columns, 4 rows a pass.
-        const int th = threadIdx.x - kGatherWarp * 32, piece = th & 15;
+        // 16 threads take the 256 bytes of a row's 128 columns: warp w the rows
+        // 4j + 2w and the next one. Lane k holds where the k-th and the (32 + k)-th
+        // of the warp's rows start and hands them out: held by every thread for
+        // itself, 32 places and a copy each were unrolled, and the fetching of
+        // those instructions took 60 clocks a copy.
+        const int w = warp - kGatherWarp, piece = lane & 15, second = lane >> 4, r8 = 2 * w + second;
         const uint32_t panel = (uint32_t)(piece >> 3) * kPanel;
         uint32_t it = 0;
         bool ok = true;
@@ -415,31 +419,37 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
             // x rows, in 16-byte pieces from x; row 0 for tokens that are not there (their results are not used)
-            uint32_t row[kTokens / 4];
+            uint32_t row[2];
             const uint32_t pieces = (uint32_t)(a.x_pitch >> 4);
 #pragma unroll
-            for (int j = 0; j < kTokens / 4; ++j) {
-                const int i = 4 * j + (th >> 4);
+            for (int h = 0; h < 2; ++h) {
+                const int k = 32 * h + lane, i = 4 * (k >> 1) + 2 * w + (k & 1);
                 int xi = 0;
                 if (i < U.n) {
                     xi = U.row0 + i;
                     if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
                     if ((unsigned)xi >= (unsigned)p.x_rows) xi = 0;
                 }
-                row[j] = (uint32_t)xi * pieces + piece;
+                row[h] = (uint32_t)xi * pieces;
             }
+            const int passes = (U.n + 3) / 4;
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
                 ok = wait(&T.bempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
-                const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel + (th >> 4) * 128;
-                // the swizzle takes the row's low three bits: 4 (j & 1) + th / 16
-                const uint32_t dst0 = dst + (((piece & 7) ^ (th >> 4)) << 4), dst1 = dst + (((piece & 7) ^ (4 + (th >> 4))) << 4);
-                const uint4 *src = static_cast<const uint4 *>(a.x16) + kb * (kW4Block * 2 / 16);
+                const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel + r8 * 128;
+                // the swizzle takes the row's low three bits: 4 (j & 1) + r8
+                const uint32_t dst0 = dst + (((piece & 7) ^ r8) << 4), dst1 = dst + (((piece & 7) ^ (4 + r8)) << 4);
+                const uint4 *src = static_cast<const uint4 *>(a.x16) + kb * (kW4Block * 2 / 16) + piece;
+#pragma unroll 1
+                for (int j0 = 0; j0 < passes; j0 += 8) {
+                    const uint32_t held = j0 < 16 ? row[0] : row[1];
+                    uint32_t from[8];
 #pragma unroll
-                for (int j = 0; j < kTokens / 4; ++j) {
-                    if (4 * j >= U.n) break;
-                    cp_async16((j & 1 ? dst1 : dst0) + j * 512, src + row[j], 16);
+                    for (int j = 0; j < 8; ++j) from[j] = __shfl_sync(0xffffffffu, held, (2 * (j0 + j) + second) & 31);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < passes) cp_async16((j & 1 ? dst1 : dst0) + (j0 + j) * 512, src + from[j], 16);
                 }
                 cp_async_arrive_noinc(&T.bfull[s]);       // once this thread's copies have landed
             }
