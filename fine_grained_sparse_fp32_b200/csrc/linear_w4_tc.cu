@@ -10,7 +10,8 @@
 // the weight (a BF16 weight would be off by 2^-9, the rounding of the result).
 // The powers of two come back in FP32 with the sums.
 //
-// Unpacking bounds this kernel (13 instructions for 8 weights), so a weight is
+// Unpacking costs this kernel most of its instructions (13 for 8 weights, 9
+// without zero points), so a weight is
 // unpacked once for up to 128 tokens, scale included, and the sums stay in
 // tensor memory for a unit's whole depth; and unpacked weights take no
 // shared-memory bandwidth: the unpacking threads write them straight into
@@ -220,6 +221,22 @@ __device__ __forceinline__ void unpack_word(uint32_t word, __half2 z1, __half2 z
     out[1] = half2_bits(__hmul2(__hfma2(as_half2((word & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
     out[2] = half2_bits(__hmul2(__hadd2(as_half2((up & 0x000f000fu) | 0x64006400u), z1), s));
     out[3] = half2_bits(__hmul2(__hfma2(as_half2((up & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
+}
+
+// The same without zero points (8 stands for 0), in 9 instructions: a code in
+// the low bits of a half is that many times 2^-24, or 2^-20 four bits further
+// up, and one FMA takes it to (q - 8) s, rounded once. 8 s and both multipliers
+// are exact. For 2^24 s to be an FP16 number, s lies below 2^-8, which the
+// token's factor gives back; weights below 2^-14 of that are off by 2^-25, that
+// is 2^-17 of the row's largest scale.
+constexpr float kSymFactor = 512.f;
+__device__ __forceinline__ void unpack_word_sym(uint32_t word, __half2 s24, __half2 s20, __half2 minus8, uint32_t *out)
+{
+    const uint32_t up = word >> 8;
+    out[0] = half2_bits(__hfma2(as_half2(word & 0x000f000fu), s24, minus8));
+    out[1] = half2_bits(__hfma2(as_half2(word & 0x00f000f0u), s20, minus8));
+    out[2] = half2_bits(__hfma2(as_half2(up & 0x000f000fu), s24, minus8));
+    out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus8));
 }
 
 // Exponent field of the largest magnitude among the n scales of a row (which
@@ -524,9 +541,16 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             fetch(0);
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int st = it % kStages, ab = it & 1;
-                __half2 s[GB];
+                __half2 s[GB], s20[GB], minus8[GB];       // without zero points: 2^24 s, 2^20 s, -8 s
 #pragma unroll
-                for (int gi = 0; gi < GB; ++gi) s[gi] = __float2half2_rn(__bfloat162float(s_next[gi]) * over);
+                for (int gi = 0; gi < GB; ++gi) {
+                    const float f = __bfloat162float(s_next[gi]) * over;      // magnitude below 2
+                    s[gi] = __float2half2_rn(kZeros ? f : f * 0x1p15f);
+                    if (!kZeros) {
+                        s20[gi] = __float2half2_rn(f * 0x1p11f);
+                        minus8[gi] = __float2half2_rn(f * -0x1p-6f);
+                    }
+                }
                 const uint32_t z = z_next;
                 if (kb + 1 < blocks) fetch(kb + 1);
                 ok = wait(&T.cfull[st], (it / kStages) & 1);
@@ -541,12 +565,15 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {  // 32 columns: 16 columns of tensor memory
                     const int gi = jj / (G / 32);
-                    const uint32_t zi = kZeros ? (z >> (8 * gi)) & 15u : 8u;
+                    const uint32_t zi = (z >> (8 * gi)) & 15u;
                     const __half2 z1 = as_half2((0xe400u | zi) * 0x00010001u);             // -(1024 + z)
                     const __half2 z16 = as_half2((0xd400u | zi << 4) * 0x00010001u);       // -(64 + z)
                     uint32_t r[16];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) unpack_word(word_of(w[t], jj), z1, z16, s[gi], r + 4 * t);
+                    for (int t = 0; t < 4; ++t) {
+                        if constexpr (kZeros) unpack_word(word_of(w[t], jj), z1, z16, s[gi], r + 4 * t);
+                        else unpack_word_sym(word_of(w[t], jj), s[gi], s20[gi], minus8[gi], r + 4 * t);
+                    }
                     tmem_st16(tmem + lanes + a_col(c, ab) + jj * 16, r);
                 }
                 tmem_st_wait();
@@ -592,7 +619,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 }
                 const bool in = (unsigned)xi < (unsigned)p.x_rows;
                 there = there && in;
-                tok[i] = in ? a.x_scale[xi] : 0.f;
+                tok[i] = in ? a.x_scale[xi] * (kZeros ? 1.f : kSymFactor) : 0.f;
             }
             there = __all_sync(0xffffffffu, there);
             __syncwarp();
