@@ -19,8 +19,8 @@
 // (256 rows of one expert, or 128 gate and the same 128 up features) and a
 // block of tokens. Units are dealt to the CTAs (one per SM) in turn.
 //   warps 0-7    results: sums from tensor memory, SiLU(gate) * up or y (warps
-//                0-3 and 4-7 take turns in units, so that one's loads and
-//                stores overlap the other's)
+//                0-3 and 4-7 take turns in steps of 16 tokens, so that a slot is
+//                soon free)
 //   warps 8-15   unpack: 64 bytes of codes of a row and 128 columns into 64
 //                columns of tensor memory (8-11 tile 0, 12-15 tile 1)
 //   warp 16      loads code tiles by TMA (64-byte swizzle: the unpackers' reads
@@ -72,9 +72,9 @@ struct Args {
 
 struct Tail {
     uint64_t cfull[kStages], cempty[kStages], bfull[kStages], bempty[kStages];
-    uint64_t afull[2][2], aempty[2][2], dfull[2], dempty[2], drain;    // sums of a group's unit; a slot read
+    uint64_t afull[2], aempty[2], dfull[2], dempty[2], drain;          // dfull: every second unit's sums; dempty: a slot read
     uint32_t tmem_base;
-    int abort, total;
+    int abort, total, sums[kThreads / 32];
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
     // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
@@ -131,40 +131,50 @@ __device__ __forceinline__ int block_size(int count)
     return n > 1 ? (((count + n - 1) / n) + 3) & ~3 : kTokens;
 }
 
-// Tables of the groups; one warp adds up the blocks.
+// Tables of the groups. Each thread has one group of a step, its number of
+// blocks is added up over the warp, and then over the warps before.
 __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
 {
-    for (int g = threadIdx.x; g < a.groups; g += kThreads) {
-        int start, count;
-        group_rows(a.p, g, &start, &count);
-        T.start[g] = start;
-        T.count[g] = count;
-        T.size[g] = block_size(count);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        int run = 0;
-        for (int g0 = 0; g0 < a.groups; g0 += 32) {
-            const int g = g0 + threadIdx.x;
-            const int n = g < a.groups ? (T.count[g] + T.size[g] - 1) / T.size[g] : 0;
-            int incl = n;
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int run = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        int n = 0;
+        if (g < a.groups) {
+            int start, count;
+            group_rows(a.p, g, &start, &count);
+            const int size = block_size(count);
+            T.start[g] = start;
+            T.count[g] = count;
+            T.size[g] = size;
+            n = (count + size - 1) / size;
+        }
+        int incl = n;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if ((int)threadIdx.x >= o) incl += v;
-            }
-            const int before = run + incl - n;
-            if (g < a.groups) {
-                T.pre[g] = before;
-                for (int k = before; k < min(before + n, kKnown); ++k) T.known[k] = g;
-            }
-            run += __shfl_sync(0xffffffffu, incl, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
-        if (threadIdx.x == 0) {
-            T.pre[a.groups] = run;
-            // ranges that overlap (which no dispatch makes) could count beyond the units' 32 bits: then nothing is done
-            T.total = (long long)run * a.tiles < 0x7fffffffLL ? run * a.tiles : 0;
+        if (lane == 31) T.sums[warp] = incl;
+        __syncthreads();
+        int before = run + incl - n;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int v = T.sums[w];
+            before += w < warp ? v : 0;
+            run += v;
         }
+        if (g < a.groups) {
+            T.pre[g] = before;
+            for (int k = before; k < min(before + n, kKnown); ++k) T.known[k] = g;
+        }
+        __syncthreads();                          // sums are read
+    }
+    if (threadIdx.x == 0) {
+        T.pre[a.groups] = run;
+        // ranges that overlap (which no dispatch makes) could count beyond the units' 32 bits: then nothing is done
+        T.total = (long long)run * a.tiles < 0x7fffffffLL ? run * a.tiles : 0;
     }
     __syncthreads();
 }
@@ -367,14 +377,11 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             mbar_init(&T.bfull[s], kGatherThreads);
             mbar_init(&T.bempty[s], 1);
         }
-        for (int c = 0; c < 2; ++c)
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&T.afull[c][b], 4);
-                mbar_init(&T.aempty[c][b], 1);
-            }
         for (int b = 0; b < 2; ++b) {
+            mbar_init(&T.afull[b], 8);            // one arrival per unpacking warp
+            mbar_init(&T.aempty[b], 1);
             mbar_init(&T.dfull[b], 1);
-            mbar_init(&T.dempty[b], 4);           // one arrival per result warp of a group
+            mbar_init(&T.dempty[b], 8);           // one arrival per result warp
         }
         mbar_init(&T.drain, 1);
         T.abort = 0;
@@ -487,26 +494,25 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dempty[sl.first + k], sl.parity(sl.first + k) ^ 1);
             for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
                 const int s = it % kStages, ab = it & 1;
-                ok = wait(&T.bfull[s], (it / kStages) & 1);
+                ok = wait(&T.bfull[s], (it / kStages) & 1) && wait(&T.afull[ab], (it >> 1) & 1);
+                if (!ok) break;
                 fence_proxy_async();              // the gathered rows, for the tensor core
+                tc_fence_after();
                 const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
                 const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
+                if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    ok = ok && wait(&T.afull[c][ab], (it >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+                    for (int c = 0; c < 2; ++c) {
                         const uint32_t dt = tmem + d_col(c, sl.first), at = tmem + a_col(c, ab);
 #pragma unroll
                         for (int k = 0; k < kW4Block / 16; ++k)
                             umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
-                        umma_commit(&T.aempty[c][ab]);
-                        if (c == 1) umma_commit(&T.bempty[s]);
-                        if (c == 1 && kb + 1 == blocks) umma_commit(&T.dfull[turn]);
                     }
-                    __syncwarp();
+                    umma_commit(&T.aempty[ab]);
+                    umma_commit(&T.bempty[s]);
+                    if (kb + 1 == blocks) umma_commit(&T.dfull[turn]);
                 }
+                __syncwarp();
             }
             sl.done();
         }
@@ -559,7 +565,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 uint4 w[4];                       // w[t]: words of columns 8t of each 32-column slice
 #pragma unroll
                 for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint4 *>(src + ((t ^ ((row >> 1) & 3)) << 4));
-                ok = wait(&T.aempty[c][ab], ((it >> 1) & 1) ^ 1);
+                ok = wait(&T.aempty[ab], ((it >> 1) & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -580,7 +586,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&T.afull[c][ab]);
+                    mbar_arrive(&T.afull[ab]);
                     mbar_arrive(&T.cempty[st]);
                 }
             }
@@ -589,17 +595,16 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         // -------------------------------------------------------- results
         const int half = warp >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        // A group waits on a barrier of its own: its units' sums follow one another
-        // there, and the next ones cannot be complete before it has read these,
-        // since three units never fit into two slots.
+        // Units take turns in two barriers: a unit's sums can be complete before the
+        // last one's are read, but the next but one's cannot, since three units
+        // never fit into two slots.
         Slots sl;
-        uint32_t mine = 0;
+        uint32_t nth = 0;
         bool ok = true;
-        for (int u = blockIdx.x, turn = 0; u < total && ok; u += gridDim.x, turn ^= 1) {
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
             sl.take(U.n);
-            if (turn != half) continue;           // the other group's unit
             // the rows' powers of two, and the tokens'
             float row_scale[2];
 #pragma unroll
@@ -623,23 +628,25 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             }
             there = __all_sync(0xffffffffu, there);
             __syncwarp();
-            ok = wait(&T.dfull[half], mine++ & 1);
+            ok = wait(&T.dfull[nth & 1], (nth >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
-            for (int t0 = 0; t0 < U.n; t0 += 16) {
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
+            };
+            if (16 * half >= U.n) release();      // nothing to read
+            for (int t0 = 16 * half; t0 < U.n; t0 += 32) {
                 uint32_t v0[16], v1[16];
                 tmem_ld16(tmem + lanes + d_col(0, sl.first) + t0, v0);
                 tmem_ld16(tmem + lanes + d_col(1, sl.first) + t0, v1);
                 tmem_ld_wait();
-                if (t0 + 16 >= U.n) {             // all of it in registers: the slot is free
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
-                }
+                if (t0 + 32 >= U.n) release();    // all of it in registers
                 // a whole step of tokens that are all there has no branch in it
                 if (t0 + 16 <= U.n && there)
                     store_step<kUp, true>(p, y + (size_t)t0 * p.rows + r, r, 16, tok + t0, row_scale, T.turn[warp], v0, v1);
