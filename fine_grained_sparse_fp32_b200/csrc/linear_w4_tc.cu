@@ -77,6 +77,7 @@ struct Tail {
     int abort, total, sums[kThreads / 32];
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
+    uint8_t field[4][2][kRows];                   // exponent fields of the rows' largest scales, of units in turn
     // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
     alignas(16) float tok[8][kTokens];
     alignas(16) __nv_bfloat16 turn[8][16 * 32];
@@ -174,7 +175,7 @@ __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
     if (threadIdx.x == 0) {
         T.pre[a.groups] = run;
         // ranges that overlap (which no dispatch makes) could count beyond the units' 32 bits: then nothing is done
-        T.total = (long long)run * a.tiles < 0x7fffffffLL ? run * a.tiles : 0;
+        T.total = (long long)run * a.tiles < 0x7fff0000LL ? run * a.tiles : 0;
     }
     __syncthreads();
 }
@@ -249,24 +250,22 @@ __device__ __forceinline__ void unpack_word_sym(uint32_t word, __half2 s24, __ha
     out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus8));
 }
 
-// Exponent field of the largest magnitude among the n scales of a row (which
-// start at a multiple of 8 bytes where n is a multiple of 4).
-__device__ __forceinline__ uint32_t scale_exponent(const __nv_bfloat16 *s, int n)
+// A block's scales of a row (GB of them: 2, 4 or 8 bytes, aligned to that), as
+// they lie in memory.
+template <int GB>
+__device__ __forceinline__ uint2 load_scales(const __nv_bfloat16 *s)
 {
-    uint32_t top = 0;
-    if (n % 4 == 0) {
-        uint32_t two = 0;
-#pragma unroll 4
-        for (int i = 0; i < n; i += 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(s + i);
-            two = __vmaxu2(two, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
-        }
-        top = max(two & 0xffffu, two >> 16);
-    } else {
-        for (int i = 0; i < n; ++i) top = max(top, (uint32_t)(__bfloat16_as_ushort(s[i]) & 0x7fffu));
-    }
-    return max(top >> 7, 1u);
+    if constexpr (GB == 4) return *reinterpret_cast<const uint2 *>(s);
+    else if constexpr (GB == 2) return make_uint2(*reinterpret_cast<const uint32_t *>(s), 0u);
+    else return make_uint2(*reinterpret_cast<const uint16_t *>(s), 0u);
 }
+// The largest magnitudes so far (two halves of 15 bits) with some scales' among them.
+__device__ __forceinline__ uint32_t larger_scale(uint32_t top, uint2 s)
+{
+    return __vmaxu2(top, __vmaxu2(s.x & 0x7fff7fffu, s.y & 0x7fff7fffu));
+}
+// Exponent field of the largest magnitude: 1 to 253.
+__device__ __forceinline__ uint32_t scale_field(uint32_t top) { return min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u); }
 
 // This thread's row of M tile c of a unit, and its matrix.
 template <bool kUp>
@@ -524,33 +523,48 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         // --------------------------------------------------------- unpack
         const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        uint32_t it = 0;
+        uint32_t it = 0, nth = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const __nv_bfloat16 *sc = nullptr, *sc_after = nullptr;      // this unit's scales and the next one's
+        const uint8_t *zr = nullptr, *zr_after = nullptr;
+        auto rows_of = [&](int u) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
             const size_t at = tile_row<kUp>(a, U, c, row) * gpr;
-            const __nv_bfloat16 *sc = (kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at;
-            const uint8_t *zr = kZeros ? (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at : nullptr;
+            sc_after = (kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at;
+            if (kZeros) zr_after = (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at;
+        };
+        uint32_t top = 0;                         // of the next unit's scales, read along with this one's blocks
+        uint2 s_next{};                           // loaded one block ahead
+        uint32_t z_next = 0x08080808u;
+        auto fetch = [&](int kb) {
+            s_next = load_scales<GB>(sc + kb * GB);
+            if (kZeros) {
+                const uint8_t *z = zr + kb * GB;
+                z_next = GB == 1 ? *z : GB == 2 ? *reinterpret_cast<const uint16_t *>(z) : *reinterpret_cast<const uint32_t *>(z);
+            }
+        };
+        if (blockIdx.x < total) {
+            rows_of(blockIdx.x);
+            for (int kb = 0; kb < blocks; ++kb) top = larger_scale(top, load_scales<GB>(sc_after + kb * GB));
+        }
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             // scales over the power of two below the row's largest: 2^(127 - field) as FP32
-            const float over = __uint_as_float((254u - min(scale_exponent(sc, gpr), 253u)) << 23);
-            __nv_bfloat16 s_next[GB];             // loaded one block ahead
-            uint32_t z_next = 0x08080808u;
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int gi = 0; gi < GB; ++gi) s_next[gi] = sc[kb * GB + gi];
-                if (kZeros) {
-                    const uint8_t *z = zr + kb * GB;
-                    z_next = GB == 1 ? *z : GB == 2 ? *reinterpret_cast<const uint16_t *>(z) : *reinterpret_cast<const uint32_t *>(z);
-                }
-            };
+            const uint32_t field = scale_field(top);
+            const float over = __uint_as_float((254u - field) << 23);
+            sc = sc_after;
+            zr = zr_after;
             fetch(0);
+            const bool more = u + (int)gridDim.x < total;
+            if (more) rows_of(u + gridDim.x);
+            top = 0;
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int st = it % kStages, ab = it & 1;
                 __half2 s[GB], s20[GB], minus8[GB];       // without zero points: 2^24 s, 2^20 s, -8 s
 #pragma unroll
                 for (int gi = 0; gi < GB; ++gi) {
-                    const float f = __bfloat162float(s_next[gi]) * over;      // magnitude below 2
+                    const uint32_t two = gi < 2 ? s_next.x : s_next.y;
+                    const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // magnitude below 2
                     s[gi] = __float2half2_rn(kZeros ? f : f * 0x1p15f);
                     if (!kZeros) {
                         s20[gi] = __float2half2_rn(f * 0x1p11f);
@@ -559,6 +573,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 }
                 const uint32_t z = z_next;
                 if (kb + 1 < blocks) fetch(kb + 1);
+                const uint2 s_after = more ? load_scales<GB>(sc_after + kb * GB) : uint2{};
                 ok = wait(&T.cfull[st], (it / kStages) & 1);
                 if (!ok) break;
                 const uint8_t *src = codes + (size_t)st * 2 * kCodeTile + c * kCodeTile + row * 64;
@@ -568,6 +583,9 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 ok = wait(&T.aempty[ab], ((it >> 1) & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
+                // for the results. The block two before is done, so at the earliest the
+                // last unit but one, whose sums took the place of the last but three's.
+                if (kb == 0) T.field[nth & 3][c][row] = (uint8_t)field;
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {  // 32 columns: 16 columns of tensor memory
                     const int gi = jj / (G / 32);
@@ -589,11 +607,12 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                     mbar_arrive(&T.afull[ab]);
                     mbar_arrive(&T.cempty[st]);
                 }
+                top = larger_scale(top, s_after);
             }
         }
     } else {
         // -------------------------------------------------------- results
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         // Units take turns in two barriers: a unit's sums can be complete before the
         // last one's are read, but the next but one's cannot, since three units
@@ -601,36 +620,41 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         Slots sl;
         uint32_t nth = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
+        float f_after[kTokens / 32];              // the next unit's tokens' powers of two; 0 for one without an x row
+        auto factors_of = [&](int u) {
             const Unit U = unit_of(a, T, u);
-            const bool shared = U.grp >= p.E;
-            sl.take(U.n);
-            // the rows' powers of two, and the tokens'
-            float row_scale[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const __nv_bfloat16 *sc = kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s);
-                row_scale[c] = __uint_as_float(min(scale_exponent(sc + tile_row<kUp>(a, U, c, row) * gpr, gpr), 253u) << 23);
-            }
-            float *tok = T.tok[warp];             // 0 for a token that is not there
-            bool there = true;
 #pragma unroll
             for (int j = 0; j < kTokens / 32; ++j) {
                 const int i = lane + 32 * j;
                 int xi = 0;
                 if (i < U.n) {
                     xi = U.row0 + i;
-                    if (!p.x_by_row) xi = shared ? xi - p.P : p.perm ? p.perm[xi] : xi;
+                    if (!p.x_by_row) xi = U.grp >= p.E ? xi - p.P : p.perm ? p.perm[xi] : xi;
                 }
-                const bool in = (unsigned)xi < (unsigned)p.x_rows;
-                there = there && in;
-                tok[i] = in ? a.x_scale[xi] * (kZeros ? 1.f : kSymFactor) : 0.f;
+                f_after[j] = (unsigned)xi < (unsigned)p.x_rows ? a.x_scale[xi] : 0.f;
+            }
+        };
+        if (blockIdx.x < total) factors_of(blockIdx.x);
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
+            const Unit U = unit_of(a, T, u);
+            const bool shared = U.grp >= p.E;
+            sl.take(U.n);
+            float *tok = T.tok[warp];             // 0 for a token that is not there
+            bool there = true;
+#pragma unroll
+            for (int j = 0; j < kTokens / 32; ++j) {
+                tok[lane + 32 * j] = f_after[j] * (kZeros ? 1.f : kSymFactor);
+                there = there && f_after[j] != 0.f;
             }
             there = __all_sync(0xffffffffu, there);
             __syncwarp();
+            if (u + (int)gridDim.x < total) factors_of(u + gridDim.x);
             ok = wait(&T.dfull[nth & 1], (nth >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
+            float row_scale[2];                   // the rows' powers of two
+#pragma unroll
+            for (int c = 0; c < 2; ++c) row_scale[c] = __uint_as_float((uint32_t)T.field[nth & 3][c][row] << 23);
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
