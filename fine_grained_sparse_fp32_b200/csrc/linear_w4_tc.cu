@@ -7,11 +7,11 @@
 // than BF16 would: 2^-a times x, a from the largest value of its row, is exact
 // for every BF16 x within 2^30 of that value, and (q - z) times the row's
 // scale over the power of two below its largest scale is rounded to 2^-12 of
-// the weight (a BF16 weight would be off by 2^-9, the rounding of the result).
+// the weight and of the zero point's share (a BF16 weight would be off by 2^-9,
+// the rounding of the result).
 // The powers of two come back in FP32 with the sums.
 //
-// Unpacking costs this kernel most of its instructions (13 for 8 weights, 9
-// without zero points), so a weight is
+// Unpacking costs this kernel most of its instructions (9 for 8 weights), so a weight is
 // unpacked once for up to 128 tokens, scale included, and the sums stay in
 // tensor memory for a unit's whole depth; and unpacked weights take no
 // shared-memory bandwidth: the unpacking threads write them straight into
@@ -219,35 +219,22 @@ __device__ __forceinline__ constexpr uint32_t idesc_f16_f32(int M, int N)
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
 __device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
 
-// The eight columns of a word as FP16 weights, in column order. A code in the
-// low mantissa bits of 1024.0 counts ones, four bits further up sixteens: so
-// one shift serves the word. Codes minus zero points are exact, the product
-// with the scale is rounded.
-// z1 = -(1024 + z), z16 = -(64 + z), both twice; s = scale, twice.
-__device__ __forceinline__ void unpack_word(uint32_t word, __half2 z1, __half2 z16, __half2 s, uint32_t *out)
-{
-    const __half2 sixteenth = as_half2(0x2c002c00u);
-    const uint32_t up = word >> 8;
-    out[0] = half2_bits(__hmul2(__hadd2(as_half2((word & 0x000f000fu) | 0x64006400u), z1), s));
-    out[1] = half2_bits(__hmul2(__hfma2(as_half2((word & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
-    out[2] = half2_bits(__hmul2(__hadd2(as_half2((up & 0x000f000fu) | 0x64006400u), z1), s));
-    out[3] = half2_bits(__hmul2(__hfma2(as_half2((up & 0x00f000f0u) | 0x64006400u), sixteenth, z16), s));
-}
-
-// The same without zero points (8 stands for 0), in 9 instructions: a code in
-// the low bits of a half is that many times 2^-24, or 2^-20 four bits further
-// up, and one FMA takes it to (q - 8) s, rounded once. 8 s and both multipliers
-// are exact. For 2^24 s to be an FP16 number, s lies below 2^-8, which the
-// token's factor gives back; weights below 2^-14 of that are off by 2^-25, that
-// is 2^-17 of the row's largest scale.
-constexpr float kSymFactor = 512.f;
-__device__ __forceinline__ void unpack_word_sym(uint32_t word, __half2 s24, __half2 s20, __half2 minus8, uint32_t *out)
+// The eight columns of a word as FP16 weights, in column order and in 9
+// instructions: a code in the low bits of a half is that many times 2^-24, or
+// 2^-20 four bits further up (so one shift serves the word), and one FMA takes it
+// to (q - z) s, rounded once. s24 = 2^24 s and s20 = 2^20 s are exact, and so is
+// minus_z = -z s for z = 8; a zero point of 9 to 15 can lose the last of its
+// product's 12 bits, 2^-12 of z s. For s24 to be an FP16 number, s lies below
+// 2^-8, which the token's factor gives back; weights below 2^-14 of that are off
+// by 2^-25, that is 2^-17 of the row's largest scale.
+constexpr float kTokenFactor = 512.f;
+__device__ __forceinline__ void unpack_word(uint32_t word, __half2 s24, __half2 s20, __half2 minus_z, uint32_t *out)
 {
     const uint32_t up = word >> 8;
-    out[0] = half2_bits(__hfma2(as_half2(word & 0x000f000fu), s24, minus8));
-    out[1] = half2_bits(__hfma2(as_half2(word & 0x00f000f0u), s20, minus8));
-    out[2] = half2_bits(__hfma2(as_half2(up & 0x000f000fu), s24, minus8));
-    out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus8));
+    out[0] = half2_bits(__hfma2(as_half2(word & 0x000f000fu), s24, minus_z));
+    out[1] = half2_bits(__hfma2(as_half2(word & 0x00f000f0u), s20, minus_z));
+    out[2] = half2_bits(__hfma2(as_half2(up & 0x000f000fu), s24, minus_z));
+    out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus_z));
 }
 
 // A block's scales of a row (GB of them: 2, 4 or 8 bytes, aligned to that), as
@@ -536,7 +523,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         };
         uint32_t top = 0;                         // of the next unit's scales, read along with this one's blocks
         uint2 s_next{};                           // loaded one block ahead
-        uint32_t z_next = 0x08080808u;
+        uint32_t z_next = 0;
         auto fetch = [&](int kb) {
             s_next = load_scales<GB>(sc + kb * GB);
             if (kZeros) {
@@ -560,18 +547,16 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             top = 0;
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int st = it % kStages, ab = it & 1;
-                __half2 s[GB], s20[GB], minus8[GB];       // without zero points: 2^24 s, 2^20 s, -8 s
+                __half2 s24[GB], s20[GB], minus_z[GB];
 #pragma unroll
                 for (int gi = 0; gi < GB; ++gi) {
                     const uint32_t two = gi < 2 ? s_next.x : s_next.y;
-                    const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // magnitude below 2
-                    s[gi] = __float2half2_rn(kZeros ? f : f * 0x1p15f);
-                    if (!kZeros) {
-                        s20[gi] = __float2half2_rn(f * 0x1p11f);
-                        minus8[gi] = __float2half2_rn(f * -0x1p-6f);
-                    }
+                    const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
+                    const float z = kZeros ? (float)((z_next >> (8 * gi)) & 15u) : 8.f;
+                    s24[gi] = __float2half2_rn(f * 0x1p15f);
+                    s20[gi] = __float2half2_rn(f * 0x1p11f);
+                    minus_z[gi] = __float2half2_rn(f * z * -0x1p-9f);
                 }
-                const uint32_t z = z_next;
                 if (kb + 1 < blocks) fetch(kb + 1);
                 const uint2 s_after = more ? load_scales<GB>(sc_after + kb * GB) : uint2{};
                 ok = wait(&T.cfull[st], (it / kStages) & 1);
@@ -589,15 +574,9 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {  // 32 columns: 16 columns of tensor memory
                     const int gi = jj / (G / 32);
-                    const uint32_t zi = (z >> (8 * gi)) & 15u;
-                    const __half2 z1 = as_half2((0xe400u | zi) * 0x00010001u);             // -(1024 + z)
-                    const __half2 z16 = as_half2((0xd400u | zi << 4) * 0x00010001u);       // -(64 + z)
                     uint32_t r[16];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if constexpr (kZeros) unpack_word(word_of(w[t], jj), z1, z16, s[gi], r + 4 * t);
-                        else unpack_word_sym(word_of(w[t], jj), s[gi], s20[gi], minus8[gi], r + 4 * t);
-                    }
+                    for (int t = 0; t < 4; ++t) unpack_word(word_of(w[t], jj), s24[gi], s20[gi], minus_z[gi], r + 4 * t);
                     tmem_st16(tmem + lanes + a_col(c, ab) + jj * 16, r);
                 }
                 tmem_st_wait();
@@ -643,7 +622,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             bool there = true;
 #pragma unroll
             for (int j = 0; j < kTokens / 32; ++j) {
-                tok[lane + 32 * j] = f_after[j] * (kZeros ? 1.f : kSymFactor);
+                tok[lane + 32 * j] = f_after[j] * kTokenFactor;
                 there = there && f_after[j] != 0.f;
             }
             there = __all_sync(0xffffffffu, there);
