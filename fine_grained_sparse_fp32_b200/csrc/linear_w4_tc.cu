@@ -180,6 +180,13 @@ __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
     __syncthreads();
 }
 
+// Asks L2 for bytes that lie at p, but for parts of 16 at the ends.
+__device__ __forceinline__ void prefetch_l2(const void *p, size_t bytes)
+{
+    const uintptr_t from = (reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15), to = (reinterpret_cast<uintptr_t>(p) + bytes) & ~uintptr_t(15);
+    if (to > from) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+}
+
 // One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one()
 {
@@ -397,6 +404,21 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const bool shared = U.grp >= p.E;
             const int y0 = (shared ? 0 : U.grp * p.rows) + (kUp ? U.tile * kRows : U.tile * 2 * kRows);
             const int y1 = kUp ? y0 : y0 + kRows;
+            // The next unit's scales and zero points, whose rows the unpackers read a few
+            // bytes at a time, and each 32 bytes anew from memory otherwise.
+            if (u + (int)gridDim.x < total) {
+                const Unit V = unit_of(a, T, u + gridDim.x);
+                const bool vs = V.grp >= p.E;
+                const int r0 = V.tile * (kUp ? 1 : 2) * kRows, n = min(p.rows - r0, (kUp ? 1 : 2) * kRows), gpr = p.cols / G;
+                const size_t at = ((vs ? 0 : (size_t)V.grp * p.rows) + r0) * gpr;
+                if (elect_one()) {
+                    prefetch_l2((vs ? p.w_shared.s : p.w.s) + at, (size_t)n * gpr * 2);
+                    if (kUp) prefetch_l2((vs ? p.up_shared.s : p.up.s) + at, (size_t)n * gpr * 2);
+                    if (kZeros) prefetch_l2((vs ? p.w_shared.z : p.w.z) + at, (size_t)n * gpr);
+                    if (kZeros && kUp) prefetch_l2((vs ? p.up_shared.z : p.up.z) + at, (size_t)n * gpr);
+                }
+                __syncwarp();
+            }
             const CUtensorMap *m0 = shared ? &maps.w_shared[0] : &maps.w[0], *m1 = shared ? &maps.w_shared[1] : &maps.w[1];
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
@@ -552,10 +574,10 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 for (int gi = 0; gi < GB; ++gi) {
                     const uint32_t two = gi < 2 ? s_next.x : s_next.y;
                     const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
-                    const float z = kZeros ? (float)((z_next >> (8 * gi)) & 15u) : 8.f;
+                    const uint32_t z = kZeros ? (z_next >> (8 * gi)) & 15u : 8u;
                     s24[gi] = __float2half2_rn(f * 0x1p15f);
-                    s20[gi] = __float2half2_rn(f * 0x1p11f);
-                    minus_z[gi] = __float2half2_rn(f * z * -0x1p-9f);
+                    s20[gi] = __hmul2(s24[gi], as_half2(0x2c002c00u));                          // 2^-4
+                    minus_z[gi] = __hmul2(s24[gi], as_half2((0x8000u | z) * 0x00010001u));      // -z 2^-24
                 }
                 if (kb + 1 < blocks) fetch(kb + 1);
                 const uint2 s_after = more ? load_scales<GB>(sc_after + kb * GB) : uint2{};
