@@ -189,15 +189,16 @@ static bool two_term(int w_dtype, int N) { return w_dtype == KMOE_E4M3_B128 && N
 // for gate and up) go to the tensor-core kernel. It unpacks a weight once for up
 // to 128 rows and costs nearly the same for one; the kernel for few tokens pays
 // for every four rows, more with small groups. Measured on the layer's FFN (384
-// experts): groups of 128, 8 rows an expert 243 us against 327 us here, 16 rows
-// 408 against 344; groups of 32, 4 rows 317 against 401, 8 rows 463 against 413.
-// One matrix has few units to deal out, and the more rows are needed the fewer
-// there are: 24 units (6144 x 2560) meet at 100 rows (31 us), 10 (2560 x 6144) at
-// 200 (65 us), 2 (512 x 2560) at 1200 (33 us).
+// experts), with even and uneven experts, the two meet at 510 and 380 tokens for
+// groups of 128 (240 and 206 us), 320 and 170 for groups of 64 (261 and 175 us),
+// 125 and about 90 for groups of 32 (250 us); the rule lies between. One matrix
+// has few units to deal out, and the more rows are needed the fewer there are:
+// 24 units (6144 x 2560) meet at 35 rows (20 us), 10 (2560 x 6144) at 130 (56
+// us), 2 (512 x 2560) at 1000 (30 us).
 static bool w4_tensor_cores(int P, int E, int units, int group)
 {
-    const int rows = group == 32 ? 7 : group == 64 ? 9 : 12;
-    return (long long)P * units >= ((long long)rows * units * E + 2200);
+    const int rows = group == 32 ? 1 : group == 64 ? 3 : 6;
+    return (long long)P * units >= ((long long)rows * units * E + 1100);
 }
 
 // The grouped FFN's scratch after the status block: H [N*K + N, I] and, with

@@ -244,19 +244,53 @@ __device__ __forceinline__ void unpack_word(uint32_t word, __half2 s24, __half2 
     out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus_z));
 }
 
-// A block's scales of a row (GB of them: 2, 4 or 8 bytes, aligned to that), as
-// they lie in memory.
-template <int GB>
-__device__ __forceinline__ uint2 load_scales(const __nv_bfloat16 *s)
+// A few blocks' scales and zero points of a row, read at once: a load whose lanes
+// read a row each takes 32 clocks of the load unit, however few
+// bytes it brings (groups of 32, 1024 tokens: one load a block took 336 us, two
+// blocks' at a time 308).
+struct Scales {
+    uint4 s;
+    uint2 z;
+};
+// n (1, 2, 4 or 8) of them, of rows that start at multiples of n.
+template <bool kZeros>
+__device__ __forceinline__ Scales load_scales(const __nv_bfloat16 *s, const uint8_t *z, int n)
 {
-    if constexpr (GB == 4) return *reinterpret_cast<const uint2 *>(s);
-    else if constexpr (GB == 2) return make_uint2(*reinterpret_cast<const uint32_t *>(s), 0u);
-    else return make_uint2(*reinterpret_cast<const uint16_t *>(s), 0u);
+    Scales r{};
+    if (n == 8) {                                 // (groups of 32)
+        r.s = *reinterpret_cast<const uint4 *>(s);
+        if (kZeros) r.z = *reinterpret_cast<const uint2 *>(z);
+    } else if (n == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(s);
+        r.s.x = v.x;
+        r.s.y = v.y;
+        if (kZeros) r.z.x = *reinterpret_cast<const uint32_t *>(z);
+    } else if (n == 2) {
+        r.s.x = *reinterpret_cast<const uint32_t *>(s);
+        if (kZeros) r.z.x = *reinterpret_cast<const uint16_t *>(z);
+    } else {
+        r.s.x = *reinterpret_cast<const uint16_t *>(s);
+        if (kZeros) r.z.x = *z;
+    }
+    return r;
+}
+// The first n of 2n taken off.
+template <int n, bool kZeros>
+__device__ __forceinline__ void next_scales(Scales &r)
+{
+    if constexpr (n == 4) {
+        r.s.x = r.s.z;
+        r.s.y = r.s.w;
+        if (kZeros) r.z.x = r.z.y;
+    } else if constexpr (n == 2) {
+        r.s.x = r.s.y;
+        if (kZeros) r.z.x >>= 16;
+    }
 }
 // The largest magnitudes so far (two halves of 15 bits) with some scales' among them.
-__device__ __forceinline__ uint32_t larger_scale(uint32_t top, uint2 s)
+__device__ __forceinline__ uint32_t larger_scale(uint32_t top, uint4 s)
 {
-    return __vmaxu2(top, __vmaxu2(s.x & 0x7fff7fffu, s.y & 0x7fff7fffu));
+    return __vmaxu2(__vmaxu2(top, __vmaxu2(s.x & 0x7fff7fffu, s.y & 0x7fff7fffu)), __vmaxu2(s.z & 0x7fff7fffu, s.w & 0x7fff7fffu));
 }
 // Exponent field of the largest magnitude: 1 to 253.
 __device__ __forceinline__ uint32_t scale_field(uint32_t top) { return min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u); }
@@ -543,19 +577,16 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             sc_after = (kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at;
             if (kZeros) zr_after = (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at;
         };
-        uint32_t top = 0;                         // of the next unit's scales, read along with this one's blocks
-        uint2 s_next{};                           // loaded one block ahead
-        uint32_t z_next = 0;
-        auto fetch = [&](int kb) {
-            s_next = load_scales<GB>(sc + kb * GB);
-            if (kZeros) {
-                const uint8_t *z = zr + kb * GB;
-                z_next = GB == 1 ? *z : GB == 2 ? *reinterpret_cast<const uint16_t *>(z) : *reinterpret_cast<const uint32_t *>(z);
-            }
-        };
+        // Scales at a time: two blocks' where every row is aligned to that. (One scale a
+        // block is read alone: four at a time took 255 us for 1024 tokens, not 246.)
+        const int n_blocks = GB > 1 && blocks % 2 == 0 ? 2 : 1, n_scales = n_blocks * GB;
+        uint32_t top = 0;                         // of the next unit's scales, read along with this one's
+        Scales now{}, later{};                    // at work, and read ahead
+        uint4 s_after{};                          // of the next unit, for `top`
         if (blockIdx.x < total) {
             rows_of(blockIdx.x);
-            for (int kb = 0; kb < blocks; ++kb) top = larger_scale(top, load_scales<GB>(sc_after + kb * GB));
+            for (int kb = 0; kb < blocks; kb += n_blocks) top = larger_scale(top, load_scales<false>(sc_after + kb * GB, nullptr, n_scales).s);
+            later = load_scales<kZeros>(sc_after, zr_after, n_scales);
         }
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             // scales over the power of two below the row's largest: 2^(127 - field) as FP32
@@ -563,24 +594,31 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const float over = __uint_as_float((254u - field) << 23);
             sc = sc_after;
             zr = zr_after;
-            fetch(0);
             const bool more = u + (int)gridDim.x < total;
             if (more) rows_of(u + gridDim.x);
             top = 0;
+            s_after = make_uint4(0u, 0u, 0u, 0u);
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int st = it % kStages, ab = it & 1;
+                if ((kb & (n_blocks - 1)) == 0) {
+                    const int ahead = kb + n_blocks;
+                    now = later;
+                    if (ahead < blocks) later = load_scales<kZeros>(sc + ahead * GB, zr + ahead * GB, n_scales);
+                    else if (more) later = load_scales<kZeros>(sc_after, zr_after, n_scales);
+                    top = larger_scale(top, s_after);
+                    if (more) s_after = load_scales<false>(sc_after + kb * GB, nullptr, n_scales).s;
+                }
                 __half2 s24[GB], s20[GB], minus_z[GB];
 #pragma unroll
                 for (int gi = 0; gi < GB; ++gi) {
-                    const uint32_t two = gi < 2 ? s_next.x : s_next.y;
+                    const uint32_t two = gi < 2 ? now.s.x : now.s.y;
                     const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
-                    const uint32_t z = kZeros ? (z_next >> (8 * gi)) & 15u : 8u;
+                    const uint32_t z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
                     s24[gi] = __float2half2_rn(f * 0x1p15f);
                     s20[gi] = __hmul2(s24[gi], as_half2(0x2c002c00u));                          // 2^-4
                     minus_z[gi] = __hmul2(s24[gi], as_half2((0x8000u | z) * 0x00010001u));      // -z 2^-24
                 }
-                if (kb + 1 < blocks) fetch(kb + 1);
-                const uint2 s_after = more ? load_scales<GB>(sc_after + kb * GB) : uint2{};
+                next_scales<GB, kZeros>(now);
                 ok = wait(&T.cfull[st], (it / kStages) & 1);
                 if (!ok) break;
                 const uint8_t *src = codes + (size_t)st * 2 * kCodeTile + c * kCodeTile + row * 64;
@@ -608,8 +646,8 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                     mbar_arrive(&T.afull[ab]);
                     mbar_arrive(&T.cempty[st]);
                 }
-                top = larger_scale(top, s_after);
             }
+            top = larger_scale(top, s_after);
         }
     } else {
         // -------------------------------------------------------- results
