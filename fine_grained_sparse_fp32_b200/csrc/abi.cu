@@ -234,10 +234,12 @@ static FfnScratch take_ffn_scratch(Carver &c, int N, int d, int K, int I, int w_
 }
 
 // FP32 results stay on the kernel for few tokens: FP16 weights are not exact
-// enough for them.
-static bool linear_w4_tc(int N, int P, int rows, int E, int group, int y_dtype)
+// enough for them. So do inputs that the other one's 32-bit row offsets, in 16
+// bytes, do not span (64 GiB).
+static bool w4_tc_spans(long long rows, long long row_bytes) { return rows * (row_bytes / 16) < (1LL << 32); }
+static bool linear_w4_tc(int N, int P, int rows, int cols, int E, int group, int y_dtype)
 {
-    return y_dtype == KMOE_BF16 && N > 0 && w4_tensor_cores(P, E, (rows + 255) / 256, group);
+    return y_dtype == KMOE_BF16 && N > 0 && w4_tc_spans(N, cols * 2LL) && w4_tensor_cores(P, E, (rows + 255) / 256, group);
 }
 
 // Bytes of a moe_grouped_ffn workspace: the status block, then the scratch.
@@ -317,7 +319,8 @@ static kmoe_status run_ffn_w4(const __nv_bfloat16 *x, int N, int d, int I, int E
                               const int32_t *offsets, const kmoe_w4 *r, const kmoe_w4 *s, const FfnScratch &f, void *y_perm,
                               void *y_shared, int *status, bool clear, cudaStream_t st)
 {
-    const bool tc = w4_tensor_cores(N * K, E, (I + 127) / 128, r[0].group);
+    const bool tc = w4_tensor_cores(N * K, E, (I + 127) / 128, r[0].group) && w4_tc_spans(N, d * 2LL) &&
+                    w4_tc_spans((long long)N * K + N, I * 4LL);
     W4Product a{};
     a.P = N * K;
     a.n_shared = s ? N : 0;
@@ -763,9 +766,10 @@ kmoe_status moe_route(const void *logits, int l_dtype, const float *bias, int N,
 
 size_t moe_linear_w4_workspace_size(int N, int P, int rows, int cols, int E, int group, int y_dtype)
 {
-    if (N < 0 || P < 0 || rows < 1 || E < 1 || cols < 128 || cols % 128 || !linear_w4_tc(N, P, rows, E, group, y_dtype))
+    if (N < 0 || P < 0 || rows < 1 || E < 1 || cols < 128 || cols % 128 || !linear_w4_tc(N, P, rows, cols, E, group, y_dtype))
         return 0;
     Carver c(nullptr);
+    c.take<uint8_t>(kStatusBytes);
     c.take<uint8_t>((size_t)N * cols * 2);
     c.take<float>(N);
     return c.used;
@@ -810,8 +814,9 @@ kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, in
     a.y_dtype = y_dtype;
     if (need) {
         Carver c(ws);
+        a.status = reinterpret_cast<int *>(c.take<uint8_t>(kStatusBytes));
         void *x16 = c.take<uint8_t>((size_t)N * cols * 2);
-        return launch_w4_tc(a, x16, c.take<float>(N), nullptr, wait_limit(), static_cast<cudaStream_t>(stream));
+        return launch_w4_tc(a, x16, c.take<float>(N), a.status, wait_limit(), static_cast<cudaStream_t>(stream));
     }
     return launch_w4(a, static_cast<cudaStream_t>(stream));
 }

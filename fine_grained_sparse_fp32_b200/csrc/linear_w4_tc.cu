@@ -6,9 +6,9 @@
 // in FP16 with FP32 sums. With powers of two taken out, FP16 holds more of both
 // than BF16 would: 2^-a times x, a from the largest value of its row, is exact
 // for every BF16 x within 2^30 of that value, and (q - z) times the row's
-// scale over the power of two below its largest scale is rounded to 2^-12 of
-// the weight and of the zero point's share (a BF16 weight would be off by 2^-9,
-// the rounding of the result).
+// scale over the power of two below its largest scale is off by at most 2^-11 of
+// the weight and of the zero point's share z s (a BF16 weight would be off by
+// 2^-8, the rounding of the result).
 // The powers of two come back in FP32 with the sums.
 //
 // Unpacking costs this kernel most of its instructions (9 for 8 weights), so a weight is
@@ -85,7 +85,8 @@ struct Tail {
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
 // mbar_wait by a whole warp: true in every lane, or false in every lane. Past
-// the first look the warp is suspended for up to 20 us at a time.
+// the first look the warp is suspended for up to 20 us at a time, so a shorter
+// limit counts as that.
 __device__ __forceinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, long long limit)
 {
     const long long t0 = clock64();
@@ -231,7 +232,7 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_
 // 2^-20 four bits further up (so one shift serves the word), and one FMA takes it
 // to (q - z) s, rounded once. s24 = 2^24 s and s20 = 2^20 s are exact, and so is
 // minus_z = -z s for z = 8; a zero point of 9 to 15 can lose the last of its
-// product's 12 bits, 2^-12 of z s. For s24 to be an FP16 number, s lies below
+// product's 12 bits, 2^-11 of z s. For s24 to be an FP16 number, s lies below
 // 2^-8, which the token's factor gives back; weights below 2^-14 of that are off
 // by 2^-25, that is 2^-17 of the row's largest scale.
 constexpr float kTokenFactor = 512.f;

@@ -155,7 +155,7 @@ def load(path: str | None = None):
     lib.moe_set_wait_limit.argtypes = [ctypes.c_longlong]
     for f in ("moe_router_topk", "moe_permute", "moe_permute_noalloc", "moe_grouped_ffn", "moe_combine",
               "moe_forward", "moe_block_forward", "moe_quant_1x128", "moe_device_status", "moe_set_wait_limit",
-              "moe_route", "moe_linear_w4", "moe_linear_w4_workspace_size", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
+              "moe_route", "moe_linear_w4", "moe_forward_routed", "moe_block_forward_routed", "moe_quant_w4",
               "moe_dequant_w4"):
         getattr(lib, f).restype = i
     if lib.moe_abi_version() != 3:
@@ -196,6 +196,14 @@ def _call(name, t, stream, *args):
             status = fn(*args, s)
     if status:
         _check(status)
+
+
+def _empty(shape, dtype, device, stream):
+    """New memory of the stream that writes it: what it held before was used on that stream alone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _on_gpu(t, name):
@@ -445,8 +453,8 @@ class Layer:
         _dense(offsets, "offsets", torch.int32, (cfg.E + 1,), x.device)
         adt = act_dtype_for(cfg.w_dtype)
         if out is None:
-            y_perm = torch.empty((N * cfg.K, cfg.d), dtype=adt, device=x.device)
-            y_shared = torch.empty((N, cfg.d), dtype=adt, device=x.device) if with_shared else None
+            y_perm = _empty((N * cfg.K, cfg.d), adt, x.device, stream)
+            y_shared = _empty((N, cfg.d), adt, x.device, stream) if with_shared else None
         else:
             y_perm, y_shared = out
             _dense(y_perm, "y_perm", adt, (N * cfg.K, cfg.d), x.device)
@@ -512,11 +520,11 @@ def moe_route(logits, K, bias=None, routing=None, topk_idx=None, topk_w=None, st
     if bias is not None:
         _dense(bias, "bias", torch.float32, (E,), dev)
     if topk_idx is None:
-        topk_idx = torch.empty((N, K), dtype=torch.int32, device=dev)
+        topk_idx = _empty((N, K), torch.int32, dev, stream)
     else:
         _dense(topk_idx, "topk_idx", torch.int32, (N, K), dev)
     if topk_w is None:
-        topk_w = torch.empty((N, K), dtype=torch.float32, device=dev)
+        topk_w = _empty((N, K), torch.float32, dev, stream)
     else:
         _dense(topk_w, "topk_w", torch.float32, (N, K), dev)
     _call("moe_route", logits, stream, logits.data_ptr(), _DTYPE_CODES[logits.dtype],
@@ -540,9 +548,9 @@ def moe_quant_w4(w, group=128, zeros=False, out=None, stream=None) -> W4:
         raise ValueError(f"group {group} (32, 64 or 128) of cols {cols} (a multiple of 128)")
     if out is None:
         shape = lead + (cols // group,)
-        out = W4(torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device),
-                 torch.empty(shape, dtype=torch.bfloat16, device=w.device),
-                 torch.empty(shape, dtype=torch.uint8, device=w.device) if zeros else None)
+        out = W4(_empty(lead + (cols // 2,), torch.uint8, w.device, stream),
+                 _empty(shape, torch.bfloat16, w.device, stream),
+                 _empty(shape, torch.uint8, w.device, stream) if zeros else None)
     elif tuple(out.codes.shape) != lead + (cols // 2,) or out.group != group or (out.zeros is None) == bool(zeros) \
             or out.codes.device != w.device:
         raise ValueError("out: another shape, group, device or zero points")
@@ -557,7 +565,7 @@ def moe_dequant_w4(w4: W4, dtype=torch.bfloat16, out=None, stream=None):
     _on_gpu(w4.codes, "codes")
     if out is None:
         _act_code(dtype, "out")
-        out = torch.empty(shape, dtype=dtype, device=w4.codes.device)
+        out = _empty(shape, dtype, w4.codes.device, stream)
     else:
         _dense(out, "out", tuple(_DTYPE_CODES), shape, w4.codes.device)
     _call("moe_dequant_w4", w4.codes, stream, w4._ref, out.numel() // w4.cols, w4.cols, out.data_ptr(),
@@ -588,15 +596,14 @@ def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat
         _dense(offsets, "offsets", torch.int32, (w4.E + 1,), dev)
     if out is None:
         _act_code(y_dtype, "y")
-        out = torch.empty((P, w4.rows), dtype=y_dtype, device=dev)
+        out = _empty((P, w4.rows), y_dtype, dev, stream)
     else:
         _dense(out, "out", tuple(_DTYPE_CODES), (P, w4.rows), dev)
     code = _DTYPE_CODES[out.dtype]
     if ws is None and code == KMOE_BF16:
         need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.rows, w4.cols, w4.E, w4.group, code)
         if need:
-            with torch.cuda.stream(stream):       # memory of the stream that uses it
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = _empty(need, torch.uint8, dev, stream)
     _call("moe_linear_w4", x, stream, x.data_ptr(), KMOE_BF16, N, P, w4.rows, w4.cols, w4.E,
           None if perm_token is None else perm_token.data_ptr(), None if offsets is None else offsets.data_ptr(),
           w4._ref, out.data_ptr(), code, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())

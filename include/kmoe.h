@@ -93,8 +93,8 @@ typedef enum {
  *   W[g][r][c] = (q[g][r][c] - z[g][r][c / group]) * s[g][r][c / group]
  * with codes q and zero points z in 0..15; without zero points z = 8
  * everywhere. group is 32, 64 or 128; cols is a multiple of 128; rows is any
- * number. Values are used as this product, not rounded to BF16 first, except
- * where an entry point says so.
+ * number. Scales are finite. Values are used as this product, not rounded to
+ * BF16 first; moe_linear_w4 says how closely.
  *   codes  : device [G, rows, cols / 2] bytes. The 128 columns of a block take
  *            64 bytes: sixteen little-endian 32-bit words of eight columns,
  *            columns 8v .. 8v + 7 of the block in word 4 * (v % 4) + v / 4 (a
@@ -273,8 +273,9 @@ kmoe_status moe_permute_noalloc(const int32_t *topk_idx, int N, int K, int E,
  * row (x, and H before the down projection) is held as two E4M3 terms with
  * one FP32 scale, v = s * (hi + lo / 16), within about 2^-8 of |v| (BF16's
  * own rounding is 2^-9), over the whole BF16 range.
- * With KMOE_W4 weights x must be BF16 (KMOE_ERR_UNSUPPORTED otherwise) and H is
- * FP32.
+ * With KMOE_W4 weights x must be BF16 (KMOE_ERR_UNSUPPORTED otherwise), H is
+ * FP32 in the workspace, and both products are rounded as moe_linear_w4 says for
+ * BF16 y.
  * x device [N, d] (x_dtype F32 or BF16). perm_token, offsets as produced by
  * moe_permute. Output dtype: FP32 when the weights are FP32, else BF16.
  * y_perm device [N*K, d]; y_shared device [N, d]. With KMOE_E4M3_B128_A8
@@ -295,13 +296,20 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * accumulated in FP32. With offsets NULL every row uses W_0 (E must be 1).
  * Every x[.] row is BF16; a row p that no expert's range holds keeps what y
  * held. Row ranges are cut to [0, P), and a perm_token entry outside [0, N)
- * stands for a row of zeros.
+ * stands for a row of zeros. offsets must not descend, as moe_permute's do not.
+ * With F32 y, x is used to within 2^-22 of the largest value of its 128-column
+ * block. With BF16 y, few rows use x to within 2^-14 of that value; many rows use
+ * the tensor cores, with x to within 2^-39 of the largest value of its whole row
+ * (H, an FP32 input, to 2^-12 of its own value as well) and weights rounded to 11
+ * bits, z * s apart from q * s (a BF16 weight has 8). Which of the two depends on
+ * P and the sizes.
  * x device [N, cols] BF16; w: E matrices [rows, cols]; perm_token device [P]
  * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
  * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,
  * 128 <= cols <= 8192 (a multiple of 128), 1 <= E <= 1024. P == 0 is a no-op.
  * ws: device workspace of at least moe_linear_w4_workspace_size() bytes, which
- * is 0 (ws may be NULL) for few rows and for FP32 y.
+ * is 0 (ws may be NULL) for few rows and for FP32 y. Where it is not 0, the
+ * first 4 bytes are the status word that moe_device_status reads.
  */
 kmoe_status moe_linear_w4(const void *x, int x_dtype, int N, int P, int rows, int cols, int E,
                           const int32_t *perm_token, const int32_t *offsets, const kmoe_w4 *w,
@@ -434,10 +442,11 @@ kmoe_status moe_quant_w4(const void *w, int w_dtype, int rows, int cols, int gro
 kmoe_status moe_dequant_w4(const kmoe_w4 *w, int rows, int cols, void *out, int out_dtype, void *stream);
 
 /*
- * Device status word. moe_forward, moe_block_forward and moe_grouped_ffn clear the first 4
- * bytes of `ws` when they are enqueued; a tensor-core kernel whose pipeline
- * wait gives up (after about two seconds, which only a fault elsewhere can
- * cause) writes a non-zero code there and returns early, leaving its outputs
+ * Device status word. moe_forward, moe_block_forward (with their _routed
+ * forms), moe_grouped_ffn and moe_linear_w4 (where it takes a workspace) clear
+ * the first 4 bytes of `ws` when they are enqueued; a tensor-core kernel whose
+ * pipeline wait gives up (after about two seconds, which only a fault elsewhere
+ * can cause) writes a non-zero code there and returns early, leaving its outputs
  * invalid. This call copies the word to *status and synchronises `stream`
  * (the one exception to the no-synchronisation rule). Returns KMOE_OK when
  * the word is 0, KMOE_ERR_DEVICE otherwise (1 = a wait timed out).

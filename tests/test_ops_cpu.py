@@ -82,6 +82,9 @@ def test_linear_w4_checks_its_arguments(lib):
     assert need >= 5000 * (256 * 2 + 4)
     assert kmoe.moe_linear_w4_workspace_size(5000, 5000, 16, 256, y_dtype=torch.float32) == 0
     assert kmoe.moe_linear_w4_workspace_size(4, 4, 16, 256) == 0
+    assert kmoe.moe_linear_w4_workspace_size(1 << 19, 1 << 19, 4096, 8192) > 1 << 33        # more than 32 bits
+    assert kmoe.moe_linear_w4_workspace_size((1 << 22) - 1, 1 << 22, 16, 8192) > 1 << 35
+    assert kmoe.moe_linear_w4_workspace_size(1 << 22, 1 << 22, 16, 8192) == 0                 # beyond 64 GiB of x: the other kernel
     w = w4()
     call = lambda ws, n: lib.moe_linear_w4(A, 1, 5000, 5000, 16, 256, 1, None, None, ctypes.byref(w), A, 1, ws, n, None)
     assert call(A, need - 1) == kmoe.KMOE_ERR_WORKSPACE and call(None, need) == BAD

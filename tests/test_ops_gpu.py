@@ -6,8 +6,9 @@ one digit more); the sums of a group are exact, and in FP32 follow, for each dig
 per group of weights (at most cols / 32, each two roundings of 2^-24 and the addition's) and the joining of
 digits and of at most 16 column shares, all relative to S = sum |W| |x| (a digit's own sum of magnitudes is
 below 2 S): in all less than (cols / 16 + cols / 32 + 8) * 2^-23 * S plus sum |W| 2^-14 (or 2^-22) max|x|.
-Batches on the tensor cores (BF16 results) round each weight to FP16, 2^-11 S, have x exact to 2^-30 of a row's
-largest value, and FP32 sums of cols / 16 partial sums. For the FFN the errors of both sums go through
+Batches on the tensor cores (BF16 results) round each weight to FP16, 2^-11 S, have x exact to 2^-39 of a row's
+largest value, and FP32 sums of cols / 16 partial sums. (There a zero point's product z s is rounded apart, by
+2^-11 at worst and for odd z above 8 only; no allowance is made for it.) For the FFN the errors of both sums go through
 SiLU(g) * u, whose slopes are |dh/dg| <= 1.1 |u| and |dh/du| = |SiLU(g)|; the hardware exponential and reciprocal are off by less than 2^-20 together; H is rounded to BF16 at worst;
 all of it goes through |W_d|.
 """
@@ -278,6 +279,34 @@ def test_linear_w4_keeps_non_finite_rows_to_themselves(N):
     fine[[1, N - 1]] = False
     check_linear(y[fine], x[fine].double(), plain_ops.w4_values(w.codes[0], w.scales[0], w.zeros[0]), 384, rows=N)
     assert not torch.isfinite(y[1]).any() and not torch.isfinite(y[N - 1]).all()
+
+
+def test_products_on_the_tensor_cores_give_up_and_report():
+    """Waits run out (a limit of 100 clocks; a wait asleep in hardware looks again after 20 us, and the sums of
+    8192 or 6144 columns of 256 rows and 128 tokens take longer): the kernels return, the status word says so,
+    and the next call is right."""
+    g = gen(21)
+    x = randn(g, 1500, 8192).bfloat16()
+    w = kmoe.moe_quant_w4(randn(g, 700, 8192) * 0.03)
+    need = kmoe.moe_linear_w4_workspace_size(1500, 1500, 700, 8192)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    layer = make_inputs(LayerConfig("w4", 1500, 6144, 8, 2, 256, "bf16", "w4"), seed=3, device="cuda")
+    idx = torch.rand((1500, 8), device="cuda", generator=g).topk(2, 1).indices.int()
+    _, offsets, perm, _ = kmoe.moe_permute(idx, 8)
+    handle = kmoe.Layer(layer, 1500)
+    try:
+        kmoe.moe_set_wait_limit(100)
+        kmoe.moe_linear_w4(x, w, ws=ws)
+        handle.grouped_ffn(layer["x"], perm, offsets)
+        assert kmoe.moe_device_status(ws) == 1 and kmoe.moe_device_status(handle.ws) == 1
+    finally:
+        kmoe.moe_set_wait_limit(0)
+    y = kmoe.moe_linear_w4(x, w, ws=ws)
+    assert kmoe.moe_device_status(ws) == 0
+    check_linear(y, x.double(), plain_ops.w4_values(w.codes, w.scales), 8192)
+    check_ffn(layer, 1500, 2, 8, 77, handle=handle)
+    assert kmoe.moe_device_status(handle.ws) == 0
 
 
 # ------------------------------------------------------------- experts' FFN
