@@ -87,7 +87,7 @@ struct Tail {
     uint8_t field[4][2][kRows];                   // exponent fields of the rows' largest scales, of units in turn
     // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
     alignas(16) float tok[8][kTokens];
-    alignas(16) __nv_bfloat16 turn[8][16 * 32];
+    alignas(16) uint32_t turn[8][8 * 32];
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
@@ -316,39 +316,40 @@ __device__ __forceinline__ uint32_t d_col(int c, int slot) { return c * 128 + sl
 __device__ __forceinline__ uint32_t a_col(int c, int b) { return 256 + c * 128 + b * 64; }
 
 // 32 rows (one per lane) by 16 tokens of results to y [token][row] in BF16. They
-// turn in shared memory, so that a lane stores 16 bytes of a token's row: 4-byte
-// stores, four times as many, took up to 300 clocks each. at: the first token's
-// row of lane 0; left: rows from there to the end; n: tokens that are there.
-__device__ __forceinline__ void store_turned(__nv_bfloat16 *at, int pitch, int left, int n, __nv_bfloat16 *turn, const float (&o)[16])
+// turn in shared memory, two tokens a word, so that a lane stores 16 bytes of two
+// tokens' rows: 4-byte stores, four times as many, took up to 300 clocks each. at:
+// the first token's row of lane 0; left: rows from there to the end; n: tokens that
+// are there.
+__device__ __forceinline__ void store_turned(__nv_bfloat16 *at, int pitch, int left, int n, uint32_t *turn, const float (&o)[16])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) turn[i * 32 + lane] = __float2bfloat16_rn(o[i]);
+    for (int i = 0; i < 8; ++i) turn[i * 32 + lane] = as_u32(__floats2bfloat162_rn(o[2 * i], o[2 * i + 1]));
     __syncwarp();
+    const int i = lane >> 2, r = (lane & 3) * 8;
+    const uint4 a = *reinterpret_cast<const uint4 *>(turn + i * 32 + r), b = *reinterpret_cast<const uint4 *>(turn + i * 32 + r + 4);
+    __syncwarp();                                 // read, before the next ones are written
+    const uint32_t w[2][4] = {{__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410), __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410)},
+                              {__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632), __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632)}};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int i = h * 8 + (lane >> 2), r = (lane & 3) * 8;
-        const uint4 v = *reinterpret_cast<const uint4 *>(turn + i * 32 + r);
-        __nv_bfloat16 *dst = at + (size_t)i * pitch + r;
-        if (i < n) {
-            if (r + 8 <= left && pitch % 8 == 0) {
-                *reinterpret_cast<uint4 *>(dst) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        __nv_bfloat16 *dst = at + (size_t)(2 * i + h) * pitch + r;
+        if (2 * i + h >= n) continue;
+        if (r + 8 <= left && pitch % 8 == 0) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+        } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (r + k < left) dst[k] = __ushort_as_bfloat16((unsigned short)(w[k >> 1] >> (16 * (k & 1))));
-            }
+            for (int k = 0; k < 8; ++k)
+                if (r + k < left) dst[k] = __ushort_as_bfloat16((unsigned short)(w[h][k >> 1] >> (16 * (k & 1))));
         }
     }
-    __syncwarp();
 }
 
 // Results of 16 tokens (n of them there) from both tiles' sums v0, v1. at: the
 // first token's row r of y. All: every token is there and has an x row.
 template <bool kUp, bool kAll, class YT>
 __device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, int n, const float *tok, const float (&row_scale)[2],
-                                           __nv_bfloat16 *turn, const uint32_t (&v0)[16], const uint32_t (&v1)[16])
+                                           uint32_t *turn, const uint32_t (&v0)[16], const uint32_t (&v1)[16])
 {
     float o0[16], o1[16];
 #pragma unroll
@@ -377,7 +378,7 @@ __device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, in
 }
 
 // Slots that units take in turn: a unit of up to 64 tokens takes the next one,
-// a larger one both. `phase` holds, for each slot, the parity of its uses (the
+// a larger one both (the first of which is read, and free, first). `phase` holds, for each slot, the parity of its uses (the
 // MMA warp's: it waits for every use of a slot).
 struct Slots {
     uint32_t phase = 0;
@@ -386,7 +387,7 @@ struct Slots {
     {
         n = tokens > 64 ? 2 : 1;
         first = n == 2 ? 0 : next;
-        if (n == 1) next ^= 1;
+        next = n == 1 ? first ^ 1 : 0;
     }
     __device__ __forceinline__ uint32_t parity(int slot) const { return (phase >> slot) & 1; }
     __device__ __forceinline__ void done() { phase ^= n == 2 ? 3u : 1u << first; }
@@ -705,19 +706,20 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
-            auto release = [&] {
+            auto release = [&](int slot) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    for (int k = 0; k < sl.n; ++k) mbar_arrive(&T.dempty[sl.first + k]);
+                if (lane == 0) mbar_arrive(&T.dempty[slot]);
             };
-            if (16 * half >= U.n) release();      // nothing to read
+            // a group without a step in it leaves the last slot at once (the first one of two never)
+            if (U.n - (sl.n - 1) * 64 <= 16 * half) release(sl.first + sl.n - 1);
             for (int t0 = 16 * half; t0 < U.n; t0 += 32) {
                 uint32_t v0[16], v1[16];
                 tmem_ld16(tmem + lanes + d_col(0, sl.first) + t0, v0);
                 tmem_ld16(tmem + lanes + d_col(1, sl.first) + t0, v1);
                 tmem_ld_wait();
-                if (t0 + 32 >= U.n) release();    // all of it in registers
+                // the slot's last step is in registers
+                if (t0 + 32 >= U.n || (t0 & 32)) release(sl.first + (t0 >> 6));
                 // a whole step of tokens that are all there has no branch in it
                 if (t0 + 16 <= U.n && there)
                     store_step<kUp, true>(p, y + (size_t)t0 * p.rows + r, r, 16, tok + t0, row_scale, T.turn[warp], v0, v1);
