@@ -281,6 +281,22 @@ def test_linear_w4_keeps_non_finite_rows_to_themselves(N):
     assert not torch.isfinite(y[1]).any() and not torch.isfinite(y[N - 1]).all()
 
 
+@pytest.mark.parametrize("N,E,y_dtype", [(300000, 1, torch.bfloat16), (140000, 3, torch.bfloat16), (20000, 1, torch.float32),
+                                         (9000, 3, torch.float32)])
+def test_linear_w4_long_batches(N, E, y_dtype):
+    """More blocks of tokens than the kernels' tables name: each row's result, and each expert's last row."""
+    g = gen(N)
+    rows, cols = 72, 128
+    x = randn(g, 4096, cols).bfloat16()
+    w = make_w4(g, E, rows, cols, 64, True)
+    perm = torch.randint(0, 4096, (N,), dtype=torch.int32, device="cuda", generator=g)
+    off = [0, N] if E == 1 else [0, N // 2 + 5, N // 2 + 5 + N // 3, N]
+    y = kmoe.moe_linear_w4(x, w, perm, torch.tensor(off, dtype=torch.int32, device="cuda"), y_dtype=y_dtype)
+    v = plain_ops.w4_values(w.codes, w.scales, w.zeros)
+    for e in range(E):
+        check_linear(y[off[e]:off[e + 1]], x.double()[perm[off[e]:off[e + 1]].long()], v[e], cols, rows=N)
+
+
 def test_products_on_the_tensor_cores_give_up_and_report():
     """Waits run out (a limit of 100 clocks; a wait asleep in hardware looks again after 20 us, and the sums of
     8192 or 6144 columns of 256 rows and 128 tokens take longer): the kernels return, the status word says so,
