@@ -99,9 +99,9 @@ class W4:
 
 def _dense(t, name, dtype, shape, device):
     """Refuses a tensor that the library would read wrongly."""
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype and (dtype is not _ACT_DTYPES or t.dtype not in _ACT_DTYPES):
         raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:                          # a tuple
         raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -212,6 +212,7 @@ def _on_gpu(t, name):
 
 
 _DTYPE_CODES = {torch.float32: KMOE_F32, torch.bfloat16: KMOE_BF16}
+_ACT_DTYPES = tuple(_DTYPE_CODES)
 
 
 def dtype_code(t: torch.dtype) -> int:
@@ -448,7 +449,7 @@ class Layer:
         N = x.shape[0]
         if N > self.max_tokens:
             raise ValueError("more tokens than the workspace was sized for")
-        _dense(x, "x", tuple(_DTYPE_CODES), (N, cfg.d), self.ws.device)
+        _dense(x, "x", _ACT_DTYPES, (N, cfg.d), self.ws.device)
         _dense(perm_token, "perm_token", torch.int32, (N * cfg.K,), x.device)
         _dense(offsets, "offsets", torch.int32, (cfg.E + 1,), x.device)
         adt = act_dtype_for(cfg.w_dtype)
@@ -516,7 +517,7 @@ def moe_route(logits, K, bias=None, routing=None, topk_idx=None, topk_w=None, st
     N, E = logits.shape
     dev = logits.device
     _on_gpu(logits, "logits")
-    _dense(logits, "logits", tuple(_DTYPE_CODES), (N, E), dev)
+    _dense(logits, "logits", _ACT_DTYPES, (N, E), dev)
     if bias is not None:
         _dense(bias, "bias", torch.float32, (E,), dev)
     if topk_idx is None:
@@ -542,7 +543,7 @@ def moe_quant_w4(w, group=128, zeros=False, out=None, stream=None) -> W4:
     if w.dim() not in (2, 3):
         raise ValueError("w: [rows, cols] or [E, rows, cols]")
     _on_gpu(w, "w")
-    _dense(w, "w", tuple(_DTYPE_CODES), w.shape, w.device)
+    _dense(w, "w", _ACT_DTYPES, w.shape, w.device)
     lead, cols = tuple(w.shape[:-1]), w.shape[-1]
     if group not in (32, 64, 128) or cols % 128 or cols < 128:
         raise ValueError(f"group {group} (32, 64 or 128) of cols {cols} (a multiple of 128)")
@@ -567,7 +568,7 @@ def moe_dequant_w4(w4: W4, dtype=torch.bfloat16, out=None, stream=None):
         _act_code(dtype, "out")
         out = _empty(shape, dtype, w4.codes.device, stream)
     else:
-        _dense(out, "out", tuple(_DTYPE_CODES), shape, w4.codes.device)
+        _dense(out, "out", _ACT_DTYPES, shape, w4.codes.device)
     _call("moe_dequant_w4", w4.codes, stream, w4._ref, out.numel() // w4.cols, w4.cols, out.data_ptr(),
           _DTYPE_CODES[out.dtype])
     return out
@@ -598,7 +599,7 @@ def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat
         _act_code(y_dtype, "y")
         out = _empty((P, w4.rows), y_dtype, dev, stream)
     else:
-        _dense(out, "out", tuple(_DTYPE_CODES), (P, w4.rows), dev)
+        _dense(out, "out", _ACT_DTYPES, (P, w4.rows), dev)
     code = _DTYPE_CODES[out.dtype]
     if ws is None and code == KMOE_BF16:
         need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.rows, w4.cols, w4.E, w4.group, code)
