@@ -476,9 +476,9 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 __syncwarp();
             }
         }
-        if (!ok)                                  // let loads in flight land before the CTA exits
-            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
-                mbar_wait_drain(&T.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
+        // let loads in flight land before the CTA exits: another role may have left its units
+        for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
+            mbar_wait_drain(&T.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
     } else if (warp >= kGatherWarp) {
         // --------------------------------------------------------- gather
         // 16 threads take the 256 bytes of a row's 128 columns: warp w the rows
