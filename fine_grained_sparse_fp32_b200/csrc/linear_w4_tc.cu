@@ -8,7 +8,9 @@
 // for every BF16 x within 2^30 of that value, and (q - z) times the row's
 // scale over the power of two below its largest scale is off by at most 2^-11 of
 // the weight and of the zero point's share z s (a BF16 weight would be off by
-// 2^-8, the rounding of the result).
+// 2^-8, the rounding of the result). That holds for scales within 2^8 of the row's
+// largest; CTAs that meet others start anew in a pass that moves the power of
+// two along the row (`wide`, below).
 // The powers of two come back in FP32 with the sums.
 //
 // Unpacking costs this kernel most of its instructions (9 for 8 weights), so a weight is
@@ -77,14 +79,20 @@ struct Args {
     long long wait_limit;
 };
 
-struct Tail {
+struct Barriers {
     uint64_t cfull[kStages], cempty[kStages], bfull[kStages], bempty[kStages];
     uint64_t afull[2], aempty[2], dfull[2], dempty[2], drain;          // dfull: every second unit's sums; dempty: a slot read
+};
+
+enum { kGoOn = 0, kGaveUp = 1, kStartAnew = 2 };      // a wait ran out; a row's scales differ widely: the wide pass follows
+
+struct Tail {
+    Barriers bars[2];                             // of the usual pass and of the wide one
     uint32_t tmem_base;
-    int abort, total, sums[kThreads / 32];
+    int abort, total, sums[kThreads / 32];        // abort: kGoOn, or why every role leaves its units
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
-    uint8_t field[4][2][kRows];                   // exponent fields of the rows' largest scales, of units in turn
+    uint8_t field[4][2][kRows];                   // exponent fields of the rows' bases, of units in turn
     // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
     alignas(16) float tok[8][kTokens];
     alignas(16) uint32_t turn[8][8 * 32];
@@ -105,11 +113,11 @@ __device__ __forceinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, vola
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(4000)
             : "memory");
         done = ok != 0;
         if (!done && clock64() - t0 > limit) {
-            *abort = 1;
+            *abort = kGaveUp;
             if (err) atomicCAS(err, kErrNone, kErrWaitTimeout);
         }
         give_up = !done && *abort;
@@ -240,8 +248,8 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_
 // to (q - z) s, rounded once. s24 = 2^24 s and s20 = 2^20 s are exact, and so is
 // minus_z = -z s for z = 8; a zero point of 9 to 15 can lose the last of its
 // product's 12 bits, 2^-11 of z s. For s24 to be an FP16 number, s lies below
-// 2^-8, which the token's factor gives back; weights below 2^-14 of that are off
-// by 2^-25, that is 2^-17 of the row's largest scale.
+// 2^-8, which the token's factor gives back. Below 2^-14 FP16's places are 2^-24
+// wide: none is lost where s has its 8 bits above that.
 constexpr float kTokenFactor = 512.f;
 __device__ __forceinline__ void unpack_word(uint32_t word, __half2 s24, __half2 s20, __half2 minus_z, uint32_t *out)
 {
@@ -300,8 +308,9 @@ __device__ __forceinline__ uint32_t larger_scale(uint32_t top, uint4 s)
 {
     return __vmaxu2(__vmaxu2(top, __vmaxu2(s.x & 0x7fff7fffu, s.y & 0x7fff7fffu)), __vmaxu2(s.z & 0x7fff7fffu, s.w & 0x7fff7fffu));
 }
-// Exponent field of the largest magnitude: 1 to 253.
-__device__ __forceinline__ uint32_t scale_field(uint32_t top) { return min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u); }
+__device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xffffu, v >> 16); }
+// Exponent field of a magnitude's 15 bits: 1 to 253.
+__device__ __forceinline__ uint32_t scale_field(uint32_t bits) { return min(max(bits >> 7, 1u), 253u); }
 
 // This thread's row of M tile c of a unit, and its matrix.
 template <bool kUp>
@@ -309,6 +318,124 @@ __device__ __forceinline__ size_t tile_row(const Args &a, const Unit &u, int c, 
 {
     const int r = kUp ? u.tile * kRows + row : u.tile * 2 * kRows + c * kRows + row;
     return (u.grp >= a.p.E ? 0 : (size_t)u.grp * a.p.rows) + min(r, a.p.rows - 1);
+}
+
+// A row's weights are held over one power of two, its base: the one below the
+// row's largest scale. A scale within 2^kSpread of that keeps its 8 bits above FP16's
+// last place, 2^-24, and so does each |q - z| <= 8 times it. A row with a
+// smaller scale is `wide`, which the unpacking warps see as they use the scales: then every
+// role leaves its units as if a wait had run out, and the CTA takes all of them
+// again in the wide pass. There the base moves along the row: it is the power of
+// two of field f + kRoom for the first group (f: its scale's exponent field) and serves
+// fields from its own down to kSpread below; for a group outside, the row's sums so
+// far, FP32 numbers, are multiplied in tensor memory by the quotient of old base
+// and new. A group whose codes are all z adds nothing, whatever its scale (the
+// quantiser gives a group of zeros the scale 1), and is left out. A base stays within 2^-kFall of
+// the highest so far, and the sums so within FP32's range. A block's groups go to the tensor
+// core one by one, so the wide pass takes 2 to 2.5 times as long as the usual one
+// (1024 tokens, groups of 32, one group of zeros in each row: 766 us, not 296). Deciding
+// unit by unit, with no second pass, cost the usual one 5 to 15%: by registers in the
+// unpacking warps, by the scales' latency in others.
+constexpr uint32_t kSpread = 8, kRoom = 4, kFall = 96;
+
+// The base's field of a row from a group's on, whose scale has field f; 0: none so far.
+__device__ __forceinline__ uint32_t next_base(uint32_t base, uint32_t highest, uint32_t f)
+{
+    if (base != 0 && f <= base && f + kSpread >= base) return base;
+    return max(min(f + kRoom, 253u), highest > kFall ? highest - kFall : 1u);
+}
+
+// A group's factors for unpack_word. f: its scale over the power of two of its
+// row's base, magnitude below 2; z: its zero point.
+struct GroupFactors {
+    __half2 s24, s20, minus_z;
+    __device__ __forceinline__ void set(float f, uint32_t z)
+    {
+        s24 = __float2half2_rn(f * 0x1p15f);                          // 2^24 s, with s below 2^-8
+        s20 = __hmul2(s24, as_half2(0x2c002c00u));                    // 2^-4
+        minus_z = __hmul2(s24, as_half2((0x8000u | z) * 0x00010001u));        // -z 2^-24
+    }
+};
+
+// What an unpacking warp needs to know of a unit.
+struct UnpackAt {
+    const __nv_bfloat16 *sc;                      // scales and zero points of this thread's row
+    const uint8_t *zr, *codes;                    // its codes in stage 0
+    uint32_t d, to;                               // its warp's sums of the unit and buffer 0 in tensor memory
+    uint32_t it, step;                            // the first block, the first buffer
+    int blocks, n;                                // n: the unit's tokens
+    uint8_t *field;
+};
+
+// A unit of the wide pass, its groups one by one. False in every lane of a warp whose wait gave up.
+template <int G, bool kZeros>
+__device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long long limit, UnpackAt at)
+{
+    constexpr int GB = kW4Block / G, GS = G / 32; // groups of a block, 32-column slices of a group
+    const int lane = threadIdx.x & 31, swizzle = (lane >> 1) & 3;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &T.abort, err, limit); };
+    uint32_t base = 0, highest = 0;               // exponent fields (0: none so far)
+    for (int kb = 0; kb < at.blocks; ++kb, ++at.it) {
+        const Scales now = load_scales<kZeros>(at.sc + kb * GB, at.zr + kb * GB, GB);
+        const int st = at.it % kStages;
+        if (!wait(&B.cfull[st], (at.it / kStages) & 1)) return false;
+        const uint8_t *src = at.codes + (size_t)st * 2 * kCodeTile;
+#pragma unroll 1
+        for (int gi = 0; gi < GB; ++gi, ++at.step) {
+            const uint32_t ab = at.step & 1, two = gi < 2 ? now.s.x : now.s.y, bits = gi & 1 ? two & 0xffff0000u : two << 16;
+            const uint32_t z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
+            uint32_t w[GS][4], differ = 0;        // the group's words: slice, columns 8t
+#pragma unroll
+            for (int j = 0; j < GS; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    w[j][t] = *reinterpret_cast<const uint32_t *>(src + ((t ^ swizzle) << 4) + (gi * GS + j) * 4);
+                    differ |= w[j][t] ^ z * 0x11111111u;
+                }
+            const bool counts = differ != 0 && (bits & 0x7fffffffu) != 0;
+            const uint32_t next = counts ? next_base(base, highest, scale_field((bits & 0x7fffffffu) >> 16)) : base;
+            if (!wait(&B.aempty[ab], ((at.step >> 1) & 1) ^ 1)) return false;
+            const bool moves = base != 0 && next != base;
+            if (__any_sync(0xffffffffu, moves)) {
+                // the MMAs of the step before, too, which is one of this unit
+                if (!wait(&B.aempty[ab ^ 1], ((at.step - 1) >> 1) & 1)) return false;
+                tc_fence_after();
+                const int e = 127 + (int)base - (int)next;
+                const float by = !moves ? 1.f : e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
+#pragma unroll 1
+                for (int t0 = 0; t0 < at.n; t0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(at.d + t0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+                    tmem_st16(at.d + t0, v);
+                }
+            }
+            tc_fence_after();
+            base = next;
+            highest = max(highest, base);
+            GroupFactors f;
+            f.set(counts ? __uint_as_float(bits) * __uint_as_float((254u - base) << 23) : 0.f, z);
+#pragma unroll
+            for (int j = 0; j < GS; ++j) {
+                uint32_t r[16];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) unpack_word(w[j][t], f.s24, f.s20, f.minus_z, r + 4 * t);
+                tmem_st16(at.to + ab * 64 + (gi * GS + j) * 16, r);
+            }
+            const bool last = gi + 1 == GB;
+            if (last && kb + 1 == at.blocks) *at.field = (uint8_t)max(base, 1u);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&B.afull[ab]);
+                if (last) mbar_arrive(&B.cempty[st]);
+            }
+        }
+    }
+    return true;
 }
 
 // Tensor memory: sums of tile c in a slot, unpacked weights of tile c in a buffer.
@@ -393,46 +520,16 @@ struct Slots {
     __device__ __forceinline__ void done() { phase ^= n == 2 ? 3u : 1u << first; }
 };
 
-template <bool kUp, int G, bool kZeros, class YT>
-__global__ void __launch_bounds__(kThreads, 1)
-w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
+// Every unit of this CTA, by roles of its warps; kWide: in the wide pass.
+template <bool kUp, int G, bool kZeros, class YT, bool kWide>
+__device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail &T, uint8_t *codes, uint8_t *toks)
 {
-    constexpr int GB = kW4Block / G;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *codes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *toks = codes + (size_t)kStages * 2 * kCodeTile;
-    Tail &T = *reinterpret_cast<Tail *>(toks + (size_t)kStages * 2 * kPanel);
-    volatile int *abort = &T.abort;
+    constexpr int GB = kW4Block / G, kPasses = kWide ? GB : 1;
     const W4Product &p = a.p;
+    Barriers &B = T.bars[kWide];
+    volatile int *abort = &T.abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // known to be uniform
     const int lane = threadIdx.x & 31, blocks = p.cols / kW4Block;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&T.cfull[s], 1);
-            mbar_init(&T.cempty[s], 8);           // one arrival per unpacking warp
-            mbar_init(&T.bfull[s], kGatherThreads);
-            mbar_init(&T.bempty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&T.afull[b], 8);            // one arrival per unpacking warp
-            mbar_init(&T.aempty[b], 1);
-            mbar_init(&T.dfull[b], 1);
-            mbar_init(&T.dempty[b], 8);           // one arrival per result warp
-        }
-        mbar_init(&T.drain, 1);
-        T.abort = 0;
-        fence_mbar_init();
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&T.tmem_base, 512);
-        tmem_relinquish();
-    }
-    pdl_wait();
-    pdl_trigger();
-    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-    tc_fence_before();
-    build_tables(a, T);                           // its barriers also publish the mbarriers and the allocation
-    tc_fence_after();
     const int total = T.total;
     const uint32_t tmem = T.tmem_base;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort, a.err, a.wait_limit); };
@@ -465,20 +562,20 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const CUtensorMap *m0 = shared ? &maps.w_shared[0] : &maps.w[0], *m1 = shared ? &maps.w_shared[1] : &maps.w[1];
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
-                ok = wait(&T.cempty[s], ((it / kStages) & 1) ^ 1);
+                ok = wait(&B.cempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
                 uint8_t *C = codes + (size_t)s * 2 * kCodeTile;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&T.cfull[s], 2 * kCodeTile);
-                    tma_load_2d_hint(C, m0, &T.cfull[s], kb * 64, y0, pol_w);
-                    tma_load_2d_hint(C + kCodeTile, m1, &T.cfull[s], kb * 64, y1, pol_w);
+                    mbar_arrive_expect_tx(&B.cfull[s], 2 * kCodeTile);
+                    tma_load_2d_hint(C, m0, &B.cfull[s], kb * 64, y0, pol_w);
+                    tma_load_2d_hint(C + kCodeTile, m1, &B.cfull[s], kb * 64, y1, pol_w);
                 }
                 __syncwarp();
             }
         }
-        // let loads in flight land before the CTA exits: another role may have left its units
+        // let loads in flight land, whichever role has left its units
         for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
-            mbar_wait_drain(&T.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
+            mbar_wait_drain(&B.cfull[j % kStages], (j / kStages) & 1, kDefaultWaitLimit);
     } else if (warp >= kGatherWarp) {
         // --------------------------------------------------------- gather
         // 16 threads take the 256 bytes of a row's 128 columns: warp w the rows
@@ -510,7 +607,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const int passes = (U.n + 3) / 4;
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const int s = it % kStages;
-                ok = wait(&T.bempty[s], ((it / kStages) & 1) ^ 1);
+                ok = wait(&B.bempty[s], ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
                 const uint32_t dst = smem_u32(toks) + s * 2 * kPanel + panel + r8 * 128;
                 // the swizzle takes the row's low three bits: 4 (j & 1) + r8
@@ -526,7 +623,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                     for (int j = 0; j < 8; ++j)
                         if (j0 + j < passes) cp_async16((j & 1 ? dst1 : dst0) + (j0 + j) * 512, src + from[j], 16);
                 }
-                cp_async_arrive_noinc(&T.bfull[s]);       // once this thread's copies have landed
+                cp_async_arrive_noinc(&B.bfull[s]);       // once this thread's copies have landed
             }
         }
         cp_async_wait_all();
@@ -542,35 +639,61 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             const Unit U = unit_of(a, T, u);
             const uint32_t idesc = idesc_f16_f32(kRows, (U.n + 15) & ~15);
             sl.take(U.n);
-            for (int k = 0; k < sl.n; ++k) ok = ok && wait(&T.dempty[sl.first + k], sl.parity(sl.first + k) ^ 1);
+            for (int k = 0; k < sl.n; ++k) ok = ok && wait(&B.dempty[sl.first + k], sl.parity(sl.first + k) ^ 1);
             for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
-                const int s = it % kStages, ab = it & 1;
-                ok = wait(&T.bfull[s], (it / kStages) & 1) && wait(&T.afull[ab], (it >> 1) & 1);
-                if (!ok) break;
-                fence_proxy_async();              // the gathered rows, for the tensor core
-                tc_fence_after();
-                const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
-                const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
-                if (elect_one()) {
+                const int s = it % kStages;
+                ok = wait(&B.bfull[s], (it / kStages) & 1);
+                // a buffer holds a block, in the wide pass one group of it
+#pragma unroll 1
+                for (int g = 0; g < kPasses && ok; ++g) {
+                    const uint32_t step = it * kPasses + g;
+                    const int ab = step & 1;
+                    ok = wait(&B.afull[ab], (step >> 1) & 1);
+                    if (!ok) break;
+                    fence_proxy_async();          // the gathered rows, for the tensor core
+                    tc_fence_after();
+                    const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
+                    const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t dt = tmem + d_col(c, sl.first), at = tmem + a_col(c, ab);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t dt = tmem + d_col(c, sl.first), at = tmem + a_col(c, ab);
 #pragma unroll
-                        for (int k = 0; k < kW4Block / 16; ++k)
-                            umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
+                            for (int j = 0; j < kW4Block / 16 / kPasses; ++j) {
+                                const int k = g * (kW4Block / 16 / kPasses) + j;
+                                umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
+                            }
+                        }
+                        umma_commit(&B.aempty[ab]);
+                        if (g + 1 == kPasses) umma_commit(&B.bempty[s]);
+                        if (g + 1 == kPasses && kb + 1 == blocks) umma_commit(&B.dfull[turn]);
                     }
-                    umma_commit(&T.aempty[ab]);
-                    umma_commit(&T.bempty[s]);
-                    if (kb + 1 == blocks) umma_commit(&T.dfull[turn]);
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             sl.done();
         }
-        if (elect_one()) umma_commit(&T.drain);   // every MMA done before tensor memory is released
+        if (elect_one()) umma_commit(&B.drain);   // every MMA done before tensor memory is released
         __syncwarp();
-        mbar_wait_drain(&T.drain, 0, kDefaultWaitLimit);
+        mbar_wait_drain(&B.drain, 0, kDefaultWaitLimit);
         __syncwarp();
+    } else if (kWide && warp >= 8) {
+        // ---------------------------------------------------- unpack, wide
+        const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint32_t it = 0, nth = 0;
+        Slots sl;
+        for (int u = blockIdx.x; u < total; u += gridDim.x, it += blocks, ++nth) {
+            const Unit U = unit_of(a, T, u);
+            const bool shared = U.grp >= p.E;
+            const size_t at = tile_row<kUp>(a, U, c, row) * (p.cols / G);
+            sl.take(U.n);
+            const UnpackAt where = {(kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at,
+                                    kZeros ? (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at : nullptr,
+                                    codes + c * kCodeTile + row * 64, lanes + d_col(c, sl.first), lanes + a_col(c, 0), it, it * GB,
+                                    blocks, U.n, &T.field[nth & 3][c][row]};
+            if (!unpack_wide<G, kZeros>(T, B, a.err, a.wait_limit, where)) break;
+        }
     } else if (warp >= 8) {
         // --------------------------------------------------------- unpack
         const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane, gpr = p.cols / G;
@@ -599,7 +722,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         }
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             // scales over the power of two below the row's largest: 2^(127 - field) as FP32
-            const uint32_t field = scale_field(top);
+            const uint32_t field = scale_field(larger_half(top));
             const float over = __uint_as_float((254u - field) << 23);
             sc = sc_after;
             zr = zr_after;
@@ -622,19 +745,20 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 for (int gi = 0; gi < GB; ++gi) {
                     const uint32_t two = gi < 2 ? now.s.x : now.s.y;
                     const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
+                    if (fabsf(f) < 0x1p-8f && f != 0.f) *abort = kStartAnew;                    // below 2^-kSpread
                     const uint32_t z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
                     s24[gi] = __float2half2_rn(f * 0x1p15f);
                     s20[gi] = __hmul2(s24[gi], as_half2(0x2c002c00u));                          // 2^-4
                     minus_z[gi] = __hmul2(s24[gi], as_half2((0x8000u | z) * 0x00010001u));      // -z 2^-24
                 }
                 next_scales<GB, kZeros>(now);
-                ok = wait(&T.cfull[st], (it / kStages) & 1);
+                ok = wait(&B.cfull[st], (it / kStages) & 1);
                 if (!ok) break;
                 const uint8_t *src = codes + (size_t)st * 2 * kCodeTile + c * kCodeTile + row * 64;
                 uint4 w[4];                       // w[t]: words of columns 8t of each 32-column slice
 #pragma unroll
                 for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint4 *>(src + ((t ^ ((row >> 1) & 3)) << 4));
-                ok = wait(&T.aempty[ab], ((it >> 1) & 1) ^ 1);
+                ok = wait(&B.aempty[ab], ((it >> 1) & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 // for the results. The block two before is done, so at the earliest the
@@ -652,8 +776,8 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&T.afull[ab]);
-                    mbar_arrive(&T.cempty[st]);
+                    mbar_arrive(&B.afull[ab]);
+                    mbar_arrive(&B.cempty[st]);
                 }
             }
             top = larger_scale(top, s_after);
@@ -697,7 +821,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             there = __all_sync(0xffffffffu, there);
             __syncwarp();
             if (u + (int)gridDim.x < total) factors_of(u + gridDim.x);
-            ok = wait(&T.dfull[nth & 1], (nth >> 1) & 1);
+            ok = wait(&B.dfull[nth & 1], (nth >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             float row_scale[2];                   // the rows' powers of two
@@ -709,7 +833,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             auto release = [&](int slot) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&T.dempty[slot]);
+                if (lane == 0) mbar_arrive(&B.dempty[slot]);
             };
             // a group without a step in it leaves the last slot at once (the first one of two never)
             if (U.n - (sl.n - 1) * 64 <= 16 * half) release(sl.first + sl.n - 1);
@@ -729,11 +853,69 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             __syncwarp();                         // tok is read
         }
     }
+}
+
+// (a call: it costs the usual pass no registers)
+template <bool kUp, int G, bool kZeros, class YT>
+__device__ __noinline__ void run_units_wide(const Maps &maps, const Args &a, Tail &T, uint8_t *codes, uint8_t *toks)
+{
+    run_units<kUp, G, kZeros, YT, true>(maps, a, T, codes, toks);
+}
+
+template <bool kUp, int G, bool kZeros, class YT>
+__global__ void __launch_bounds__(kThreads, 1)
+w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *codes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *toks = codes + (size_t)kStages * 2 * kCodeTile;
+    Tail &T = *reinterpret_cast<Tail *>(toks + (size_t)kStages * 2 * kPanel);
+    const W4Product &p = a.p;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // known to be uniform
+    if (threadIdx.x == 0) {
+        for (Barriers &B : T.bars) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&B.cfull[s], 1);
+                mbar_init(&B.cempty[s], 8);       // one arrival per unpacking warp
+                mbar_init(&B.bfull[s], kGatherThreads);
+                mbar_init(&B.bempty[s], 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&B.afull[b], 8);        // one arrival per unpacking warp
+                mbar_init(&B.aempty[b], 1);
+                mbar_init(&B.dfull[b], 1);
+                mbar_init(&B.dempty[b], 8);       // one arrival per result warp
+            }
+            mbar_init(&B.drain, 1);
+        }
+        T.abort = kGoOn;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&T.tmem_base, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    tc_fence_before();
+    build_tables(a, T);                           // its barriers also publish the mbarriers and the allocation
+    tc_fence_after();
+    run_units<kUp, G, kZeros, YT, false>(maps, a, T, codes, toks);
+    tc_fence_before();
+    __syncthreads();
+    if (T.abort == kStartAnew) {
+        tc_fence_after();
+        __syncthreads();
+        if (threadIdx.x == 0) T.abort = kGoOn;
+        __syncthreads();
+        run_units_wide<kUp, G, kZeros, YT>(maps, a, T, codes, toks);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(T.tmem_base, 512);
     }
 }
 
