@@ -6,8 +6,8 @@
 // in FP16 with FP32 sums. With powers of two taken out, FP16 holds more of both
 // than BF16 would: 2^-a times x, a from the largest value of its row, is exact
 // for every BF16 x within 2^30 of that value, and (q - z) times the row's
-// scale over the power of two below its largest scale is off by at most 2^-11 of
-// the weight and of the zero point's share z s (a BF16 weight would be off by
+// scale over the power of two below its largest scale is exact for |q - z| <= 8 and
+// off by at most 2^-11 of the weight otherwise (a BF16 weight would be off by
 // 2^-8, the rounding of the result). That holds for scales within 2^8 of the row's
 // largest; CTAs that meet others start anew in a pass that moves the power of
 // two along the row (`wide`, below).
@@ -246,19 +246,38 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_
 // instructions: a code in the low bits of a half is that many times 2^-24, or
 // 2^-20 four bits further up (so one shift serves the word), and one FMA takes it
 // to (q - z) s, rounded once. s24 = 2^24 s and s20 = 2^20 s are exact, and so is
-// minus_z = -z s for z = 8; a zero point of 9 to 15 can lose the last of its
-// product's 12 bits, 2^-11 of z s. For s24 to be an FP16 number, s lies below
+// minus_z = -z s for z <= 8, a product of 11 bits. With a zero point of 9 to 15 it
+// would have 12, and a code equal to z would leave a weight of up to 2^-7 s: there
+// every code is flipped, q' = 15 - q, z' = 15 - z, and (q' - z') (-s) is the same weight.
+// The flip is part of the mask's instruction. For s24 to be an FP16 number, s lies below
 // 2^-8, which the token's factor gives back. Below 2^-14 FP16's places are 2^-24
 // wide: none is lost where s has its 8 bits above that.
 constexpr float kTokenFactor = 512.f;
-__device__ __forceinline__ void unpack_word(uint32_t word, __half2 s24, __half2 s20, __half2 minus_z, uint32_t *out)
+__device__ __forceinline__ void unpack_word(uint32_t word, uint32_t flip, __half2 s24, __half2 s20, __half2 minus_z, uint32_t *out)
 {
     const uint32_t up = word >> 8;
-    out[0] = half2_bits(__hfma2(as_half2(word & 0x000f000fu), s24, minus_z));
-    out[1] = half2_bits(__hfma2(as_half2(word & 0x00f000f0u), s20, minus_z));
-    out[2] = half2_bits(__hfma2(as_half2(up & 0x000f000fu), s24, minus_z));
-    out[3] = half2_bits(__hfma2(as_half2(up & 0x00f000f0u), s20, minus_z));
+    out[0] = half2_bits(__hfma2(as_half2((word ^ flip) & 0x000f000fu), s24, minus_z));
+    out[1] = half2_bits(__hfma2(as_half2((word ^ flip) & 0x00f000f0u), s20, minus_z));
+    out[2] = half2_bits(__hfma2(as_half2((up ^ flip) & 0x000f000fu), s24, minus_z));
+    out[3] = half2_bits(__hfma2(as_half2((up ^ flip) & 0x00f000f0u), s20, minus_z));
 }
+// Four groups' zero points, one a byte, after the flips, and those: the top bit of each byte.
+struct ZeroPoints {
+    uint32_t z = 0x08080808u, flips = 0;
+    __device__ __forceinline__ void set(uint32_t zeros)
+    {
+        z = zeros & 0x0f0f0f0fu;
+        flips = z + 0x77777777u;
+        z ^= ((flips >> 7) & 0x01010101u) * 15u;
+    }
+    __device__ __forceinline__ uint32_t flip(int gi) const        // that bit 32 times
+    {
+        uint32_t r;
+        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(flips), "r"(0x8888u + 0x1111u * gi));
+        return r;
+    }
+    __device__ __forceinline__ __half2 minus(int gi) const { return as_half2(__byte_perm(z, 0x80808080u, 0x4040u + 0x0101u * gi)); }      // -z 2^-24
+};
 
 // A few blocks' scales and zero points of a row, read at once: a load whose lanes
 // read a row each takes 32 clocks of the load unit, however few
@@ -346,14 +365,14 @@ __device__ __forceinline__ uint32_t next_base(uint32_t base, uint32_t highest, u
 }
 
 // A group's factors for unpack_word. f: its scale over the power of two of its
-// row's base, magnitude below 2; z: its zero point.
+// row's base, magnitude below 2; minus: -z 2^-24; flip: whether its codes are flipped.
 struct GroupFactors {
     __half2 s24, s20, minus_z;
-    __device__ __forceinline__ void set(float f, uint32_t z)
+    __device__ __forceinline__ void set(float f, __half2 minus, uint32_t flip)
     {
-        s24 = __float2half2_rn(f * 0x1p15f);                          // 2^24 s, with s below 2^-8
+        s24 = __float2half2_rn(__uint_as_float(__float_as_uint(f * 0x1p15f) ^ (flip & 0x80000000u)));        // 2^24 s, with s below 2^-8
         s20 = __hmul2(s24, as_half2(0x2c002c00u));                    // 2^-4
-        minus_z = __hmul2(s24, as_half2((0x8000u | z) * 0x00010001u));        // -z 2^-24
+        minus_z = __hmul2(s24, minus);
     }
 };
 
@@ -416,12 +435,15 @@ __device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long
             base = next;
             highest = max(highest, base);
             GroupFactors f;
-            f.set(counts ? __uint_as_float(bits) * __uint_as_float((254u - base) << 23) : 0.f, z);
+            ZeroPoints zp;
+            if (kZeros) zp.set(now.z.x);
+            const uint32_t flip = kZeros ? zp.flip(gi) : 0u;
+            f.set(counts ? __uint_as_float(bits) * __uint_as_float((254u - base) << 23) : 0.f, zp.minus(gi), flip);
 #pragma unroll
             for (int j = 0; j < GS; ++j) {
                 uint32_t r[16];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) unpack_word(w[j][t], f.s24, f.s20, f.minus_z, r + 4 * t);
+                for (int t = 0; t < 4; ++t) unpack_word(w[j][t], flip, f.s24, f.s20, f.minus_z, r + 4 * t);
                 tmem_st16(at.to + ab * 64 + (gi * GS + j) * 16, r);
             }
             const bool last = gi + 1 == GB;
@@ -740,16 +762,15 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
                     top = larger_scale(top, s_after);
                     if (more) s_after = load_scales<false>(sc_after + kb * GB, nullptr, n_scales).s;
                 }
-                __half2 s24[GB], s20[GB], minus_z[GB];
+                GroupFactors fac[GB];
+                ZeroPoints zp;
+                if (kZeros) zp.set(now.z.x);
 #pragma unroll
                 for (int gi = 0; gi < GB; ++gi) {
                     const uint32_t two = gi < 2 ? now.s.x : now.s.y;
                     const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
                     if (fabsf(f) < 0x1p-8f && f != 0.f) *abort = kStartAnew;                    // below 2^-kSpread
-                    const uint32_t z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
-                    s24[gi] = __float2half2_rn(f * 0x1p15f);
-                    s20[gi] = __hmul2(s24[gi], as_half2(0x2c002c00u));                          // 2^-4
-                    minus_z[gi] = __hmul2(s24[gi], as_half2((0x8000u | z) * 0x00010001u));      // -z 2^-24
+                    fac[gi].set(f, zp.minus(gi), kZeros ? zp.flip(gi) : 0u);
                 }
                 next_scales<GB, kZeros>(now);
                 ok = wait(&B.cfull[st], (it / kStages) & 1);
@@ -769,7 +790,8 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
                     const int gi = jj / (G / 32);
                     uint32_t r[16];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) unpack_word(word_of(w[t], jj), s24[gi], s20[gi], minus_z[gi], r + 4 * t);
+                    for (int t = 0; t < 4; ++t)
+                        unpack_word(word_of(w[t], jj), kZeros ? zp.flip(gi) : 0u, fac[gi].s24, fac[gi].s20, fac[gi].minus_z, r + 4 * t);
                     tmem_st16(tmem + lanes + a_col(c, ab) + jj * 16, r);
                 }
                 tmem_st_wait();

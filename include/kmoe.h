@@ -301,7 +301,7 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * block. With BF16 y, few rows use x to within 2^-14 of that value; many rows use
  * the tensor cores, with x to within 2^-39 of the largest value of its whole row
  * (H, an FP32 input, to 2^-11 of its own value as well) and weights rounded to 11
- * bits, z * s apart from q * s (a BF16 weight has 8); a scale below 2^-96 of its row's
+ * bits, which are exact for |q - z| <= 8 (a BF16 weight has 8); a scale below 2^-96 of its row's
  * largest one among groups that are not all zeros may lose more. Which of the two
  * depends on P and the sizes. Rows with scales further than 2^8 apart (a group of
  * zeros of small weights has such a scale) take longer on the tensor cores.

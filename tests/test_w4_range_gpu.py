@@ -92,7 +92,7 @@ def wide_w4(g, lead, rows, cols, group, zeros, binades):
     scales = torch.exp2((torch.rand(shape, device="cuda", generator=g) - 0.5) * binades) * 0.01
     pick = torch.rand(shape, device="cuda", generator=g)
     scales = torch.where(pick < 0.05, torch.zeros_like(scales), torch.where(pick > 0.9, -scales, scales))
-    z = torch.randint(0, 9, shape, dtype=torch.uint8, device="cuda", generator=g) if zeros else None
+    z = torch.randint(0, 16, shape, dtype=torch.uint8, device="cuda", generator=g) if zeros else None
     return kmoe.W4(codes, scales.bfloat16(), z)
 
 
@@ -135,6 +135,30 @@ def test_wide_and_ordinary_units_in_turn(group, zeros, cols):
         if off[e] < off[e + 1]:
             check(y[at], x[perm[at].long()], v[e], True)
     assert torch.equal(y, kmoe.moe_linear_w4(x, w, perm, offsets))
+
+
+@pytest.mark.parametrize("N", [2500])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("binades", [0, 4, 30])
+def test_a_weight_of_zero_stays_zero_for_every_zero_point(N, group, binades):
+    """Codes equal to their zero point (0 to 15) in columns where x is large, and one place away from it elsewhere,
+    with scales of every mantissa."""
+    g = gen(group + binades)
+    rows, cols = 256, 640
+    shape = (rows, cols // group)
+    z = torch.randint(0, 16, shape, dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(128, 256, shape, device="cuda", generator=g) * 2.0 ** -15
+    scales = scales * torch.exp2((torch.rand(shape, device="cuda", generator=g) * binades).round())
+    q = z.repeat_interleave(group, 1).short()
+    large = torch.arange(cols, device="cuda") % 5 == 0
+    step = torch.where(q == 0, 1, torch.where(q == 15, -1, torch.randint(0, 2, q.shape, device="cuda", generator=g) * 2 - 1))
+    q = torch.where(large, q, q + step).to(torch.uint8)
+    w = kmoe.W4(plain_ops.w4_bytes(q.cpu()).cuda(), scales.bfloat16(), z)
+    x = randn(g, N, cols)
+    x[:, large] *= 4000
+    x = x.bfloat16()
+    assert runs_on_tensor_cores(N, w) == (N == 2500)
+    check(kmoe.moe_linear_w4(x, w), x, values(w), N == 2500)
 
 
 @pytest.mark.parametrize("N", [40, 1500])
