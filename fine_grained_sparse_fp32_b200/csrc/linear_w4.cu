@@ -10,21 +10,21 @@
 // operands took 2.75 instructions per two codes and left the kernel bound by
 // its integer pipe (28% of HBM's rate). For that x is cut into digits: for each
 // token and 128 columns, with 2^E the power of two below the largest |x|,
-//   x = 2^(E - 13) * (256 t0 + t1) + r,                 |r| <= 2^(E - 14),
-// with t in -128..127, for BF16 results (r is 2^-6 of what a BF16 rounding of
-// that largest value may be off by), and for FP32 results
 //   x = 2^(E - 21) * (65536 t0 + 256 t1 + t2) + r,      |r| <= 2^(E - 22),
-// which is exact for every BF16 x within 2^14 of the block's largest value. The
-// digits of a token are two or three columns of the fragment, so it holds four
-// or two tokens. The integer sums of a group are exact, as is 256 t0 + t1 of
+// with t in -128..127, which is exact for every BF16 x within 2^14 of the block's
+// largest value. (Two digits, exact within 2^6 of it, would put four tokens into a
+// fragment, which 200 tokens and more would gain by; but one x 1000 times the others would
+// cost those 2% of their value, for all to see where its own weight is 0.) The
+// digits of a token are three columns of the fragment, so it holds two
+// tokens. The integer sums of a group are exact, as is 256 t0 + t1 of
 // them (below 2^27). Zero points come off as -z times the sum of the digits.
 // Group scale and power of two multiply the sums in FP32.
 //
 // With `up` weights, rows 0-7 of a fragment are eight gate features and rows
 // 8-15 the same eight up features, and SiLU(gate) * up is written.
 //
-// A unit is two fragments (32 rows; 16 features) of one expert for up to 8
-// tokens (4 with three digits): the digits read for one fragment serve both. The units of all experts
+// A unit is two fragments (32 rows; 16 features) of one expert for up to 4
+// tokens: the digits read for one fragment serve both. The units of all experts
 // that have rows are numbered through and every CTA (one per SM) takes a
 // contiguous share of them, in phases: as many units as the digits of their
 // tokens fit into shared memory (nearly always all). A unit of more tokens
@@ -54,7 +54,8 @@ constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Frags = 2;                       // row fragments of a unit
 constexpr int kW4Cols = 2;                        // column fragments of a unit
-__host__ __device__ constexpr int frag_tokens(int digits) { return digits == 2 ? 4 : 2; }
+constexpr int kW4FragTokens = 2;                  // tokens of a column fragment, three digits each
+constexpr int kW4Pieces = 2 * 4 * 3 * kW4FragTokens;       // 16-byte pieces of a fragment's block
 constexpr int kW4Stages = 3;                      // steps of a warp's copies in flight, plus the one in use
 constexpr int kW4MaxGroups = 1025;
 constexpr int kW4Entries = 32;                    // token blocks of a phase
@@ -64,7 +65,7 @@ constexpr int kW4Known = 1024;                    // token blocks whose expert i
 constexpr int kW4SmemMax = 226 * 1024;
 
 // Cost of a step by its tokens: what the CTAs' shares are cut by.
-__host__ __device__ constexpr int w4_cost(int tokens, int digits) { return 3 + (tokens + frag_tokens(digits) - 1) / frag_tokens(digits); }
+__host__ __device__ constexpr int w4_cost(int tokens) { return 3 + (tokens + kW4FragTokens - 1) / kW4FragTokens; }
 
 struct W4Args {
     W4Product p;
@@ -102,7 +103,7 @@ struct W4Stage {
 };
 
 struct alignas(16) W4Smem {
-    float head[kW4Warps][kW4Cols][kW4Frags][2][32];       // sums of a unit that an earlier warp began
+    float head[kW4Warps][kW4Cols][kW4Frags][32];  // sums of a unit that an earlier warp began
     long long scan_tmp[32];
     W4Entry ent[kW4Entries];
     int share[4];                                 // this CTA's first unit and the one behind its last: token block, tile
@@ -114,11 +115,9 @@ struct alignas(16) W4Smem {
 static_assert(sizeof(W4Smem) % 16 == 0, "what follows is 16-byte aligned");
 // Behind it: W4Stage [kW4Warps][kW4Stages], digits uint4 [fragment][block][2][digit columns][4], digit sums int
 // [fragment][block][128 / G][4], powers of two float [fragment][block][4], and four tables of the experts.
-// 16-byte pieces of a fragment's block: four tokens of two digits, or two of three.
-__host__ __device__ constexpr int digit_pieces(int digits) { return 2 * frag_tokens(digits) * digits * 4; }
-__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G, int digits)
+__host__ __device__ constexpr size_t w4_x_bytes(int cols, int G)
 {
-    return (size_t)(cols / kW4Block) * (16 * digit_pieces(digits) + 16 * (kW4Block / G) + 16);
+    return (size_t)(cols / kW4Block) * (16 * kW4Pieces + 16 * (kW4Block / G) + 16);
 }
 template <int G, bool kZeros>
 __host__ __device__ constexpr size_t w4_ring_bytes() { return sizeof(W4Stage<G, kZeros>) * kW4Warps * kW4Stages; }
@@ -157,14 +156,14 @@ __device__ __forceinline__ void scan2(int *count, long long *cost, W4Smem &sm)
 // The unit (token block, numbered through all experts, and tile) at which share
 // b of gridDim.x begins: the place b / gridDim.x of the total cost, in whole
 // units of cost and a rest over gridDim.x, so that everything fits into 32 bits.
-__device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Tables &tab, int b, int digits)
+__device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Tables &tab, int b)
 {
     const int c = tab.cost[a.groups], grid = gridDim.x;
     if (b >= grid) return make_int2(tab.pre[a.groups], 0);
     const int q = a.by_grid(c), r = (c - q * grid) * b, rq = a.by_grid(r), whole = q * b + rq, rest = r - rq * grid;
     const int g = last_not_above(tab.cost, a.groups, whole), count = tab.count[g];
-    const int full = w4_cost(a.tokens, digits), tb = min((whole - tab.cost[g]) / full, a.by_tokens(count - 1));
-    const int left = whole - tab.cost[g] - tb * full, w = w4_cost(min(a.tokens, count - tb * a.tokens), digits);
+    const int full = w4_cost(a.tokens), tb = min((whole - tab.cost[g]) / full, a.by_tokens(count - 1));
+    const int left = whole - tab.cost[g] - tb * full, w = w4_cost(min(a.tokens, count - tb * a.tokens));
     // left < 8, rest < grid, tiles <= 4096
     const int tile = (int)((uint32_t)(left * grid + rest) * (uint32_t)a.tiles / (uint32_t)(w * grid));
     return tile < a.tiles ? make_int2(tab.pre[g] + tb, tile) : make_int2(tab.pre[g] + tb + 1, 0);
@@ -173,13 +172,13 @@ __device__ __forceinline__ int2 share_begin(const W4Args &a, const W4Tables &tab
 // The token blocks of a phase that begins in token block `first`, by one warp:
 // lane k takes block first + k, as many as there are up to the share's last
 // (`last`, inclusive) and as fit into shared memory.
-__device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, const W4Tables &tab, int first, int last, int digits)
+__device__ __forceinline__ void plan_phase(const W4Args &a, W4Smem &sm, const W4Tables &tab, int first, int last)
 {
     const int lane = threadIdx.x & 31, tb = first + lane;
     const bool in = tb <= last;
     const int g = !in ? 0 : tb < kW4Known ? sm.known[tb] : last_not_above(tab.pre, a.groups, tb);
     const int skip = in ? (tb - tab.pre[g]) * a.tokens : 0, n = in ? min(a.tokens, tab.count[g] - skip) : 0;
-    const int per = frag_tokens(digits), frags = (n + per - 1) / per, row0 = in ? tab.start[g] + skip : 0;
+    const int frags = (n + kW4FragTokens - 1) / kW4FragTokens, row0 = in ? tab.start[g] + skip : 0;
     int upto = frags;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -348,18 +347,16 @@ __device__ __forceinline__ void read_zeros(const uint4 &w, uint32_t at, int (&z)
 
 // One step: a 128-column block of two row fragments times NT column fragments.
 // dig, sums and sx point to this lane's share of the first one's block.
-// acc[column fragment][row fragment][half]: rows g and g + 8, with two digits
-// of token t, with three of token t >> 1 (digits 0 and 1 in even lanes, digit
-// 2 in odd ones).
-template <int G, bool kZeros, int DIG, int NT>
+// acc[column fragment][row fragment][half]: rows g and g + 8 of token t >> 1, digits
+// 0 and 1 in even lanes, digit 2 in odd ones.
+template <int G, bool kZeros, int NT>
 __device__ __forceinline__ void w4_step(const uint4 (&q)[4], const float (&s)[4][kW4Block / G],
                                         const int (&z)[4][kW4Block / G], const uint4 *dig, const int *sums,
                                         const float *sx, int blocks, float (&acc)[NT][kW4Frags][2])
 {
     constexpr int GB = kW4Block / G, GS = G / 32; // groups of a block; 32-column slices of a group
-    constexpr int P = digit_pieces(DIG);
-    // three digits: odd lanes hold digit 2 and a column without meaning
-    const int second = DIG == 2 ? 1 : 1 - (threadIdx.x & 1);
+    constexpr int P = kW4Pieces;
+    const int second = 1 - (threadIdx.x & 1);     // odd lanes hold digit 2 and a column without meaning
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const uint4 d0 = dig[n * blocks * P], d1 = dig[n * blocks * P + P / 2];
@@ -392,46 +389,37 @@ __device__ __forceinline__ void w4_step(const uint4 (&q)[4], const float (&s)[4]
     }
 }
 
-// The sums of a unit's column fragment: with two digits they are acc; with
-// three, digits are joined and lane (g, t) gets row g + 8 (t & 1) of token
-// t >> 1 (in v[0]).
-template <int DIG>
-__device__ __forceinline__ void join_digits(const float (&acc)[2], float (&v)[4 - DIG])
+// Joins the digits of a unit's fragments: lane (g, t) gets row g + 8 (t & 1) of
+// token t >> 1.
+__device__ __forceinline__ float join_digits(const float (&acc)[2])
 {
-    if constexpr (DIG == 2) {
-        v[0] = acc[0];
-        v[1] = acc[1];
-    } else {
-        const bool odd = threadIdx.x & 1;
-        const float mine = odd ? acc[1] : acc[0], other = __shfl_xor_sync(0xffffffffu, odd ? acc[0] : acc[1], 1);
-        v[0] = fmaf(odd ? other : mine, 256.f, (odd ? mine : other) * (1.f / 256.f));
-    }
+    const bool odd = threadIdx.x & 1;
+    const float mine = odd ? acc[1] : acc[0], other = __shfl_xor_sync(0xffffffffu, odd ? acc[0] : acc[1], 1);
+    return fmaf(odd ? other : mine, 256.f, (odd ? mine : other) * (1.f / 256.f));
 }
 
 // Stores the sums v[column fragment][row fragment] of a unit.
-template <bool kUp, class YT, int DIG, int NT>
-__device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e, int tile, const float (&v)[NT][kW4Frags][4 - DIG])
+template <bool kUp, class YT, int NT>
+__device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e, int tile, const float (&v)[NT][kW4Frags])
 {
-    static_assert(!kUp || DIG == 2, "SwiGLU takes two digits");
     const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
     const bool shared = e.grp >= p.E;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int i = n * frag_tokens(DIG) + (DIG == 2 ? t : t >> 1);
-        if (i >= e.n) continue;
+        const int i = n * kW4FragTokens + (t >> 1);
         const size_t row = (size_t)e.row0 + i;
-        YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (row - p.P) * p.rows : static_cast<YT *>(p.y) + row * p.rows;
+        if constexpr (kUp) {                      // even lanes hold gates, odd ones ups: they take feature f of the two fragments
+            const float o = __shfl_xor_sync(0xffffffffu, t & 1 ? v[n][0] : v[n][1], 1);
+            const float gate = t & 1 ? o : v[n][0], up = t & 1 ? v[n][1] : o;
+            const int f = tile * 16 + g8 + 8 * (t & 1);
+            if (i < e.n && f < p.rows) store_val(static_cast<YT *>(p.y) + row * p.rows + f, silu_mul(gate, up));
+        } else {
+            if (i >= e.n) continue;
+            YT *y = shared ? static_cast<YT *>(p.y_shared) + (row - p.P) * p.rows : static_cast<YT *>(p.y) + row * p.rows;
 #pragma unroll
-        for (int f = 0; f < kW4Frags; ++f) {
-            if constexpr (kUp) {                  // rows g: gate, g + 8: up of one feature
-                const int r = tile * 16 + 8 * f + g8;
-                if (r < p.rows) store_val(y + r, silu_mul(v[n][f][0], v[n][f][1]));
-            } else {
-#pragma unroll
-                for (int h = 0; h < 4 - DIG; ++h) {
-                    const int r = tile * 32 + 16 * f + g8 + 8 * (DIG == 2 ? h : t & 1);
-                    if (r < p.rows) store_val(y + r, v[n][f][h]);
-                }
+            for (int f = 0; f < kW4Frags; ++f) {
+                const int r = tile * 32 + 16 * f + g8 + 8 * (t & 1);
+                if (r < p.rows) store_val(y + r, v[n][f]);
             }
         }
     }
@@ -440,8 +428,7 @@ __device__ __forceinline__ void store_unit(const W4Product &p, const W4Entry &e,
 // Two 4-byte operand words per digit from eight fixed-point values: bytes of
 // columns 0 4 1 5 and 2 6 3 7. v + 0x808080 has the balanced digits + 128 as its
 // bytes, and flipping their top bits makes them signed bytes.
-template <int DIG>
-__device__ __forceinline__ void split_digits(const int (&v)[8], uint32_t (&w)[DIG][2])
+__device__ __forceinline__ void split_digits(const int (&v)[8], uint32_t (&w)[3][2])
 {
     uint32_t b[8];
 #pragma unroll
@@ -449,18 +436,16 @@ __device__ __forceinline__ void split_digits(const int (&v)[8], uint32_t (&w)[DI
 #pragma unroll
     for (int h = 0; h < 2; ++h) {                 // columns 2h, 2h + 4, 2h + 1, 2h + 5
         const uint32_t lo = __byte_perm(b[2 * h], b[2 * h + 4], 0x5140), lo1 = __byte_perm(b[2 * h + 1], b[2 * h + 5], 0x5140);
-        w[DIG - 1][h] = __byte_perm(lo, lo1, 0x5410);
-        w[DIG - 2][h] = __byte_perm(lo, lo1, 0x7632);
-        if constexpr (DIG == 3) {
-            const uint32_t hi = __byte_perm(b[2 * h], b[2 * h + 4], 0x0062), hi1 = __byte_perm(b[2 * h + 1], b[2 * h + 5], 0x0062);
-            w[0][h] = __byte_perm(hi, hi1, 0x5410);
-        }
+        const uint32_t hi = __byte_perm(b[2 * h], b[2 * h + 4], 0x0062), hi1 = __byte_perm(b[2 * h + 1], b[2 * h + 5], 0x0062);
+        w[2][h] = __byte_perm(lo, lo1, 0x5410);
+        w[1][h] = __byte_perm(lo, lo1, 0x7632);
+        w[0][h] = __byte_perm(hi, hi1, 0x5410);
     }
 }
 
 // Eight columns of kW4Ahead staged tokens' blocks, from item it0 on (16 lanes
 // take the 128 columns of an item). A token that is not there stands for zeros.
-template <int DIG, class XT>
+template <class XT>
 __device__ __forceinline__ void load_items(const W4Args &a, const W4Smem &sm, int it0, int items, float (&v)[kW4Ahead][8])
 {
     const W4Product &p = a.p;
@@ -470,8 +455,8 @@ __device__ __forceinline__ void load_items(const W4Args &a, const W4Smem &sm, in
         const int it = it0 + k * (kW4Threads / 16), slot = a.by_blocks(it), b = it - slot * blocks;
         int xi = -1;
         if (it < items) {
-            const W4Entry e = sm.ent[sm.frag_ent[slot / frag_tokens(DIG)]];
-            const int i = slot - frag_tokens(DIG) * e.tile0;
+            const W4Entry e = sm.ent[sm.frag_ent[slot / kW4FragTokens]];
+            const int i = slot - kW4FragTokens * e.tile0;
             if (i < e.n) {
                 xi = e.row0 + i;
                 if (!p.x_by_row) xi = e.grp >= p.E ? xi - p.P : !p.perm ? xi : xi < kW4Perm ? sm.perm[xi] : p.perm[xi];
@@ -485,12 +470,12 @@ __device__ __forceinline__ void load_items(const W4Args &a, const W4Smem &sm, in
 }
 
 // Digits of the phase's tokens; v holds the first items' values.
-template <int G, bool kZeros, int DIG, class XT>
+template <int G, bool kZeros, class XT>
 __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, int frags, float (&v)[kW4Ahead][8], uint4 *dig,
                                              int *sums, float *sx)
 {
     constexpr int GB = kW4Block / G, GL = G / 8;  // groups of a block; lanes of a group
-    constexpr int kItems = kW4Threads / 16, kPer = frag_tokens(DIG), kShift = DIG == 2 ? 13 : 21;
+    constexpr int kItems = kW4Threads / 16, kPer = kW4FragTokens, kShift = 21;
     const int blocks = a.p.cols / kW4Block, items = frags * kPer * blocks;
     const int l16 = threadIdx.x & 15, jj = l16 >> 2, t = l16 & 3;
 #pragma unroll 1
@@ -513,25 +498,23 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
             int q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(x[i] * mul);
-            uint32_t w[DIG][2];
-            split_digits<DIG>(q, w);
-            int sum[DIG];
+            uint32_t w[3][2];
+            split_digits(q, w);
+            int sum[3];
 #pragma unroll
-            for (int j = 0; j < DIG; ++j) sum[j] = __dp4a((int)w[j][0], 0x01010101, __dp4a((int)w[j][1], 0x01010101, 0));
+            for (int j = 0; j < 3; ++j) sum[j] = __dp4a((int)w[j][0], 0x01010101, __dp4a((int)w[j][1], 0x01010101, 0));
 #pragma unroll
             for (int o = 1; o < GL; o <<= 1)
 #pragma unroll
-                for (int j = 0; j < DIG; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+                for (int j = 0; j < 3; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
             if (it >= items) continue;
             const int at = slot / kPer * blocks + b;
-            uint2 *out = reinterpret_cast<uint2 *>(dig + at * digit_pieces(DIG) + (jj >> 1) * (digit_pieces(DIG) / 2)) + (jj & 1);
+            uint2 *out = reinterpret_cast<uint2 *>(dig + at * kW4Pieces + (jj >> 1) * (kW4Pieces / 2)) + (jj & 1);
 #pragma unroll
-            for (int j = 0; j < DIG; ++j) out[((tok * DIG + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
+            for (int j = 0; j < 3; ++j) out[((tok * 3 + j) * 4 + t) * 2] = make_uint2(w[j][0], w[j][1]);
             if (l16 % GL == 0) {
-                int *c = sums + (at * GB + l16 / GL) * 4 + tok * (DIG - 1);
                 const int f = kZeros ? 1 : -8;
-                if constexpr (DIG == 2) c[0] = f * (256 * sum[0] + sum[1]);
-                else *reinterpret_cast<int2 *>(c) = make_int2(f * (256 * sum[0] + sum[1]), f * 256 * sum[2]);
+                *reinterpret_cast<int2 *>(sums + (at * GB + l16 / GL) * 4 + tok * 2) = make_int2(f * (256 * sum[0] + sum[1]), f * 256 * sum[2]);
             }
             // a block with an infinity or a NaN makes this token's results NaN, and no other's
             if (l16 == 0)
@@ -539,7 +522,7 @@ __device__ __forceinline__ void stage_digits(const W4Args &a, const W4Smem &sm, 
         }
         it0 += kItems * kW4Ahead;
         if (it0 - (int)(threadIdx.x >> 4) % 2 >= items) break;
-        load_items<DIG, XT>(a, sm, it0, items, v);
+        load_items<XT>(a, sm, it0, items, v);
     }
 }
 
@@ -552,7 +535,7 @@ struct WarpRun {
 };
 
 // The units of one token block that are this warp's, for its NT column fragments.
-template <bool kUp, int G, bool kZeros, class YT, int DIG, int NT>
+template <bool kUp, int G, bool kZeros, class YT, int NT>
 __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G, kZeros> *ring, const uint4 *dig, const int *sums,
                                           const float *sx, WarpRun &r, Copier<kUp, G, kZeros> &cp)
 {
@@ -561,12 +544,11 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
     const int blocks = a.p.cols / kW4Block;
     const W4Entry e = sm.ent[r.ent];
     const int at0 = e.tile0 * blocks;
-    // column g of a fragment: digit g & 1 of token g >> 1, or digit g & 3 of token g >> 2 (there is no fourth
-    // digit: its column repeats the third)
-    const int column = DIG == 2 ? lane >> 2 : (lane >> 4) * 3 + min((lane >> 2) & 3, 2);
-    const uint4 *d0 = dig + at0 * digit_pieces(DIG) + column * 4 + t;
+    // column g of a fragment: digit g & 3 of token g >> 2 (there is no fourth digit: its column repeats the third)
+    const int column = (lane >> 4) * 3 + min((lane >> 2) & 3, 2);
+    const uint4 *d0 = dig + at0 * kW4Pieces + column * 4 + t;
     const int *c0 = sums + at0 * GB * 4 + t;
-    const float *x0 = sx + at0 * 4 + (DIG == 2 ? t : t >> 1);
+    const float *x0 = sx + at0 * 4 + (t >> 1);
     uint32_t at = 0;                              // index of the first row's group at hand, modulo 2^32
     bool fresh = true;
     while (true) {
@@ -574,7 +556,7 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
             at = (uint32_t)unit_row<kUp>(a, e.grp, r.tile, 0) * (uint32_t)(a.p.cols / G) + r.block * GB;
             fresh = false;
         }
-        const uint4 *d = d0 + r.block * digit_pieces(DIG);
+        const uint4 *d = d0 + r.block * kW4Pieces;
         const int *c = c0 + r.block * GB * 4;
         const float *x = x0 + r.block * 4;
         float acc[NT][kW4Frags][2];
@@ -602,8 +584,8 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
             }
             cp_async_commit();                    // an empty group past the end keeps the count
             r.stage = r.stage + 1 == kW4Stages ? 0 : r.stage + 1;
-            w4_step<G, kZeros, DIG, NT>(q, s, z, d, c, x, blocks, acc);
-            d += digit_pieces(DIG);
+            w4_step<G, kZeros, NT>(q, s, z, d, c, x, blocks, acc);
+            d += kW4Pieces;
             c += GB * 4;
             x += 4;
             at += GB;
@@ -611,25 +593,22 @@ __device__ __forceinline__ void run_entry(const W4Args &a, W4Smem &sm, W4Stage<G
         r.s += n_steps;
         const bool whole = r.block == 0, ends = r.block + n_steps == blocks;
         r.block = 0;
-        constexpr int H = 4 - DIG;
-        float v[NT][kW4Frags][H];
+        float v[NT][kW4Frags];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int f = 0; f < kW4Frags; ++f) join_digits<DIG>(acc[n][f], v[n][f]);
+            for (int f = 0; f < kW4Frags; ++f) v[n][f] = join_digits(acc[n][f]);
         if (whole && ends) {
-            store_unit<kUp, YT, DIG, NT>(a.p, e, r.tile, v);
+            store_unit<kUp, YT, NT>(a.p, e, r.tile, v);
         } else {
             // begun by an earlier warp; or later warps go on with it: the warp's last step, its ring is free
             if (whole) r.open = true;
             __syncwarp();
-            float *to = whole ? reinterpret_cast<float *>(ring) : &sm.head[warp][0][0][0][0];
+            float *to = whole ? reinterpret_cast<float *>(ring) : &sm.head[warp][0][0][0];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int f = 0; f < kW4Frags; ++f)
-#pragma unroll
-                    for (int h = 0; h < H; ++h) to[((n * kW4Frags + f) * 2 + h) * 32 + lane] = v[n][f][h];
+                for (int f = 0; f < kW4Frags; ++f) to[(n * kW4Frags + f) * 32 + lane] = v[n][f];
         }
         if (r.s >= r.s1) return;
         at += a.s_jump;
@@ -647,13 +626,13 @@ w4_kernel(const __grid_constant__ W4Args a)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     W4Smem &sm = *reinterpret_cast<W4Smem *>(smem_raw);
-    constexpr int GB = kW4Block / G, DIG = !kUp && sizeof(YT) == 4 ? 3 : 2, H = 4 - DIG;
+    constexpr int GB = kW4Block / G;
     const W4Product &p = a.p;
     const int blocks = p.cols / kW4Block;
     uint8_t *behind = smem_raw + sizeof(W4Smem);
     W4Stage<G, kZeros> *ring = reinterpret_cast<W4Stage<G, kZeros> *>(behind) + (threadIdx.x >> 5) * kW4Stages;
     uint4 *dig = reinterpret_cast<uint4 *>(behind + w4_ring_bytes<G, kZeros>());
-    int *sums = reinterpret_cast<int *>(dig + a.x_frags * blocks * digit_pieces(DIG));
+    int *sums = reinterpret_cast<int *>(dig + a.x_frags * blocks * kW4Pieces);
     float *sx = reinterpret_cast<float *>(sums + a.x_frags * blocks * GB * 4);
     W4Tables tab;
     tab.pre = reinterpret_cast<int *>(sx + a.x_frags * blocks * 4);
@@ -682,7 +661,7 @@ w4_kernel(const __grid_constant__ W4Args a)
                 tab.count[g] = count;
                 const int full = a.by_tokens(count), rest = count - full * a.tokens;
                 n_blocks[i] = full + (rest > 0);
-                cost[i] = full * w4_cost(a.tokens, DIG) + (rest ? w4_cost(rest, DIG) : 0);
+                cost[i] = full * w4_cost(a.tokens) + (rest ? w4_cost(rest) : 0);
             }
             run += n_blocks[i];
             run_cost += cost[i];
@@ -709,9 +688,9 @@ w4_kernel(const __grid_constant__ W4Args a)
     __syncthreads();
     if (tab.cost[a.groups] == 0) return;           // no rows
     if (warp == 0) {
-        if (lane < 2) reinterpret_cast<int2 *>(sm.share)[lane] = share_begin(a, tab, blockIdx.x + lane, DIG);
+        if (lane < 2) reinterpret_cast<int2 *>(sm.share)[lane] = share_begin(a, tab, blockIdx.x + lane);
         __syncwarp();
-        plan_phase(a, sm, tab, sm.share[0], sm.share[2] - (sm.share[3] == 0), DIG);
+        plan_phase(a, sm, tab, sm.share[0], sm.share[2] - (sm.share[3] == 0));
     }
     __syncthreads();
     const int2 u1 = make_int2(sm.share[2], sm.share[3]);
@@ -727,7 +706,7 @@ w4_kernel(const __grid_constant__ W4Args a)
         const int s0 = (int)((long long)steps * warp / kW4Warps);
         const int unit0 = a.by_blocks(s0);
         float v[kW4Ahead][8];
-        load_items<DIG, XT>(a, sm, threadIdx.x >> 4, used * frag_tokens(DIG) * blocks, v);
+        load_items<XT>(a, sm, threadIdx.x >> 4, used * kW4FragTokens * blocks, v);
         WarpRun r{s0, (int)((long long)steps * (warp + 1) / kW4Warps), s0, 0, s0 - unit0 * blocks, false, 0, 0};
         Copier<kUp, G, kZeros> cp{};
         if (r.s < r.s1) {
@@ -746,35 +725,34 @@ w4_kernel(const __grid_constant__ W4Args a)
             cp_async_commit();
         }
         prefetch_units<kUp>(a, sm, r.ent, r.tile, r.block, r.s1 - r.s);
-        stage_digits<G, kZeros, DIG, XT>(a, sm, used, v, dig, sums, sx);
+        stage_digits<G, kZeros, XT>(a, sm, used, v, dig, sums, sx);
         __syncthreads();
         while (r.s < r.s1) {
-            if (sm.ent[r.ent].n <= frag_tokens(DIG)) run_entry<kUp, G, kZeros, YT, DIG, 1>(a, sm, ring, dig, sums, sx, r, cp);
-            else run_entry<kUp, G, kZeros, YT, DIG, 2>(a, sm, ring, dig, sums, sx, r, cp);
+            if (sm.ent[r.ent].n <= kW4FragTokens) run_entry<kUp, G, kZeros, YT, 1>(a, sm, ring, dig, sums, sx, r, cp);
+            else run_entry<kUp, G, kZeros, YT, 2>(a, sm, ring, dig, sums, sx, r, cp);
         }
         __syncthreads();
         if (r.open) {                             // the warp that began a shared unit adds it up
             const W4Entry e = sm.ent[r.ent];
             const int end = a.by_blocks(r.s1 - 1) * blocks + blocks;     // the unit's last step + 1
-            float v[kW4Cols][kW4Frags][H];
+            float v[kW4Cols][kW4Frags];
             const float *mine = reinterpret_cast<const float *>(ring);
 #pragma unroll
-            for (int i = 0; i < kW4Cols * kW4Frags * H; ++i)      // (fragments that the unit does not have: no token is stored)
-                v[i / (kW4Frags * H)][i / H % kW4Frags][i % H] = mine[(i / H * 2 + i % H) * 32 + lane];
+            for (int i = 0; i < kW4Cols * kW4Frags; ++i)          // (fragments that the unit does not have: no token is stored)
+                v[i / kW4Frags][i % kW4Frags] = mine[i * 32 + lane];
             for (int w = warp + 1; w < kW4Warps; ++w) {
                 const int w0 = (int)((long long)steps * w / kW4Warps), w1 = (int)((long long)steps * (w + 1) / kW4Warps);
                 if (w0 >= end) break;
                 if (w0 == w1) continue;           // a warp without steps
 #pragma unroll
-                for (int i = 0; i < kW4Cols * kW4Frags * H; ++i)
-                    v[i / (kW4Frags * H)][i / H % kW4Frags][i % H] += (&sm.head[w][0][0][0][0])[(i / H * 2 + i % H) * 32 + lane];
+                for (int i = 0; i < kW4Cols * kW4Frags; ++i) v[i / kW4Frags][i % kW4Frags] += (&sm.head[w][0][0][0])[i * 32 + lane];
             }
-            store_unit<kUp, YT, DIG, kW4Cols>(p, e, r.tile, v);
+            store_unit<kUp, YT, kW4Cols>(p, e, r.tile, v);
         }
         u0 = next;
         if (u0.x < u1.x || (u0.x == u1.x && u0.y < u1.y)) {
             __syncthreads();                      // tables and digits are free again
-            if (warp == 0) plan_phase(a, sm, tab, u0.x, u1.x - (u1.y == 0), DIG);
+            if (warp == 0) plan_phase(a, sm, tab, u0.x, u1.x - (u1.y == 0));
             __syncthreads();
         }
     }
@@ -792,12 +770,11 @@ static int sm_count_w4()
 template <bool kUp, int G, bool kZeros, class XT, class YT>
 static kmoe_status run_w4(W4Args a, cudaStream_t st)
 {
-    constexpr int DIG = !kUp && sizeof(YT) == 4 ? 3 : 2;
-    const size_t x_bytes = w4_x_bytes(a.p.cols, G, DIG);
+    const size_t x_bytes = w4_x_bytes(a.p.cols, G);
     const size_t fixed = sizeof(W4Smem) + w4_ring_bytes<G, kZeros>() + 4 * sizeof(int) * (a.groups + 1);
     a.x_frags = (int)std::min<size_t>((kW4SmemMax - fixed) / x_bytes, kW4Entries * kW4Cols);
     if (a.x_frags < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
-    a.tokens = frag_tokens(DIG) * std::min(a.x_frags, kW4Cols);
+    a.tokens = kW4FragTokens * std::min(a.x_frags, kW4Cols);
     constexpr int kTileRows = kUp ? 16 : 32;
     a.tiles = (a.p.rows + kTileRows - 1) / kTileRows;
     a.q_jump = (kTileRows - 1) * (a.p.cols / 2);

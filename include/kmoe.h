@@ -297,14 +297,14 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * Every x[.] row is BF16; a row p that no expert's range holds keeps what y
  * held. Row ranges are cut to [0, P), and a perm_token entry outside [0, N)
  * stands for a row of zeros. offsets must not descend, as moe_permute's do not.
- * With F32 y, x is used to within 2^-22 of the largest value of its 128-column
- * block. With BF16 y, few rows use x to within 2^-14 of that value; many rows use
- * the tensor cores, with x to within 2^-39 of the largest value of its whole row
- * (H, an FP32 input, to 2^-11 of its own value as well) and weights rounded to 11
- * bits, which are exact for |q - z| <= 8 (a BF16 weight has 8); a scale below 2^-96 of its row's
- * largest one among groups that are not all zeros may lose more. Which of the two
- * depends on P and the sizes. Rows with scales further than 2^8 apart (a group of
- * zeros of small weights has such a scale) take longer on the tensor cores.
+ * Few rows, and F32 y, use x to within 2^-22 of the largest value of its 128-column
+ * block, and weights exactly. Many rows of BF16 y use the tensor cores, with x to
+ * within 2^-39 of the largest value of its whole row (H, an FP32 input, to 2^-11 of its
+ * own value as well) and weights rounded to 11 bits, which are exact for
+ * |q - z| <= 8 (a BF16 weight has 8); a scale below 2^-96 of its row's largest one
+ * among groups that are not all zeros may lose more. Which of the two depends on P and
+ * the sizes. Rows with scales further than 2^8 apart (a group of zeros among small
+ * weights has such a scale) take longer on the tensor cores.
  * x device [N, cols] BF16; w: E matrices [rows, cols]; perm_token device [P]
  * int32 or NULL (then N must be >= P); offsets device [E + 1] int32 or NULL;
  * y device [P, rows] of y_dtype (F32 or BF16). 1 <= rows <= 65536,

@@ -137,7 +137,7 @@ def test_wide_and_ordinary_units_in_turn(group, zeros, cols):
     assert torch.equal(y, kmoe.moe_linear_w4(x, w, perm, offsets))
 
 
-@pytest.mark.parametrize("N", [2500])
+@pytest.mark.parametrize("N", [8, 2500])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("binades", [0, 4, 30])
 def test_a_weight_of_zero_stays_zero_for_every_zero_point(N, group, binades):
@@ -197,3 +197,21 @@ def test_experts_with_groups_of_zeros(N, group, zeros):
         tol = dh @ v[2].abs().t() + sums_bound(h.abs() + dh, v[2], tc) + BF16 * ref.abs() + 1e-37
         off_by = ((got.double() - ref).abs() / tol).max()
         assert off_by <= 1, (e, float(off_by))
+
+
+@pytest.mark.parametrize("large", [1000.0, 30000.0])
+@pytest.mark.parametrize("N", [1, 3, 21, 2000])
+@pytest.mark.parametrize("group,zeros,y_dtype", [(32, True, torch.bfloat16), (64, False, torch.bfloat16),
+                                                 (128, False, torch.bfloat16), (128, True, torch.float32)])
+def test_one_large_channel_costs_the_others_nothing(large, N, group, zeros, y_dtype):
+    """One x of 128 columns far above the rest, in a column whose weights are zero in many rows."""
+    g = gen(N + group)
+    rows, cols = 200, 512
+    w = randn(g, rows, cols) * 0.02
+    w[:, 77::128] = 0.0
+    w[::3, 77::128] = 0.01
+    q = kmoe.moe_quant_w4(w, group=group, zeros=zeros)
+    x = randn(g, N, cols)
+    x[:, 77::128] = large
+    x = x.bfloat16()
+    check(kmoe.moe_linear_w4(x, q, y_dtype=y_dtype), x, values(q), runs_on_tensor_cores(N, q, y_dtype))
