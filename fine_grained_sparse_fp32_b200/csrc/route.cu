@@ -11,8 +11,12 @@
 //
 // The choice is the one that FP64 scores make, at the cost of FP32 ones. FP32
 // scores are off by at most D = 2^-20 max s + 2^-22 max |c| (the hardware
-// exponential and reciprocal, the sum; the error of s is s (1 - s) times that of
-// the exponential, or s times it, whose growth with the exponent s outweighs).
+// exponential and reciprocal; the error of s is s (1 - s) times that of
+// the exponential, or s times it, whose growth with the exponent s outweighs). In a softmax,
+// in units of 2^-24 max s, two scores are off by 5.4 each (exponential 4, its argument 0.9,
+// the product 0.5), and all of them by one factor, that of their sum: 5 + NPL + 5 of its
+// terms, NPL additions in a lane and 5 over the warp. Their difference is off by
+// less than NPL + 24 of them, and D takes half of that.
 // Where the K + 1 best are further than 2 D apart, and the last group that stays
 // further than 4 D from the first that goes, every exact score has the same
 // order. Any other token (about one in 300) is decided again in FP64. Without a
@@ -229,7 +233,7 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
                 key[i] = key_of(c);
             }
         }
-        const float D = s_max * 0x1p-20f + (s_max + b_max) * 0x1p-22f + 1e-36f;
+        const float D = s_max * (a.softmax ? (NPL + 24) * 0x1p-25f : 0x1p-20f) + (s_max + b_max) * 0x1p-22f + 1e-36f;
         // whether two neighbours' order is not the exact one for sure (hi >= lo)
         auto unsure = [&](float hi, float lo, float width) {
             const float d = hi - lo;

@@ -1,0 +1,46 @@
+"""Choices of moe_route that lie next to what FP32 scores can tell apart, against the plain FP64 form."""
+import pytest
+import torch
+
+from fine_grained_sparse_fp32_b200 import _build, kmoe
+import plain_ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _build.build()
+    kmoe.load()
+
+
+def check_route(logits, K, bias, **kw):
+    idx, w = kmoe.moe_route(logits, K, bias=bias, routing=kmoe.Routing(**kw))
+    ri, rw = plain_ops.route(logits, K, bias, **kw)
+    assert torch.equal(idx.cpu(), ri)
+    # FP32 arithmetic of an exponential, a sum and quotients: under 16 roundings of 2^-24 (a sum of many terms
+    # next to 2^-24 of the first adds as many more)
+    assert torch.allclose(w.cpu().double(), rw, rtol=(16 + logits.shape[1] / kw.get("n_groups", 1)) * 2.0 ** -24, atol=1e-37)
+
+
+@pytest.mark.parametrize("E,groups", [(1020, 17), (1008, 18), (512, 16), (720, 9)])
+@pytest.mark.parametrize("term", [-16.64, -16.63])
+@pytest.mark.parametrize("by", ["max", "top2"])
+def test_softmax_with_many_terms_next_to_the_last_place(E, groups, term, by):
+    """The first expert's group holds terms just below (-16.64) or above (-16.63) half of the last place of 1, which
+    an FP32 sum loses or doubles one by one, and a bias brings another group's expert within that of the first. Every
+    other choice is far from the next."""
+    size = E // groups
+    logits = torch.full((1, E), -60.0)
+    logits[0, :size] = term
+    logits[0, 0] = 0.0
+    other = E - size + 2
+    s = torch.softmax(logits[0].double(), 0)
+    for gap in torch.linspace(-6e-6, 6e-6, 121).tolist():
+        bias = -0.01 * (torch.arange(E) // size + 1.0) - 0.01 * (torch.arange(E) % size != 0)
+        bias[0] = 0.0
+        bias[other] = float(s[0] - s[other] + gap)
+        check_route(logits.cuda(), 2, bias.cuda(), score="softmax", n_groups=groups, topk_groups=3, group_score=by,
+                    renormalise=False)
