@@ -16,7 +16,9 @@
 // in units of 2^-24 max s, two scores are off by 5.4 each (exponential 4, its argument 0.9,
 // the product 0.5), and all of them by one factor, that of their sum: 5 + NPL + 5 of its
 // terms, NPL additions in a lane and 5 over the warp. Their difference is off by
-// less than NPL + 24 of them, and D takes half of that.
+// less than NPL + 24 of them, and D takes half of that. Where a bias lies outside
+// +-kFarBias, each score's own |c| counts instead of the largest: with that, one expert switched
+// off by -1e9 sends every token to FP64 (65536 tokens: 343 us, not 95).
 // Where the K + 1 best are further than 2 D apart, and the last group that stays
 // further than 4 D from the first that goes, every exact score has the same
 // order. Any other token (about one in 300) is decided again in FP64. Without a
@@ -30,9 +32,11 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 namespace kmoe {
 
+constexpr float kFarBias = 4.f;
 constexpr int kRouteWarps = 8, kRouteCtas = 4;       // tokens in work of a CTA, CTAs of an SM
 
 struct RouteArgs {
@@ -199,6 +203,7 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         }
         b_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b_max)));
     }
+    const bool far = kBias && b_max > kFarBias;
     const int step = gridDim.x * kRouteWarps;
     for (int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < a.N; t += step) {
         const LT *lr = logits + (size_t)t * a.E, *mine_of = lr + base + sub;
@@ -233,7 +238,7 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
                 key[i] = key_of(c);
             }
         }
-        const float D = s_max * (a.softmax ? (NPL + 24) * 0x1p-25f : 0x1p-20f) + (s_max + b_max) * 0x1p-22f + 1e-36f;
+        const float D = s_max * (a.softmax ? (NPL + 24) * 0x1p-25f : 0x1p-20f) + (far ? 0.f : (s_max + b_max) * 0x1p-22f) + 1e-36f;
         // whether two neighbours' order is not the exact one for sure (hi >= lo)
         auto unsure = [&](float hi, float lo, float width) {
             const float d = hi - lo;
@@ -267,8 +272,14 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
                 before += o > mine || (o == mine && g < group);
             }
             const bool stays = group < a.n_groups && before < a.topk_groups;
-            const int last = __reduce_min_sync(0xffffffffu, stays ? mine : INT_MAX);
-            const int next = __reduce_max_sync(0xffffffffu, stays ? kGoneKey : mine);
+            int low = mine, high = mine;          // what a group score's own size leaves open
+            if (far && mine > kMaskedKey) {
+                const float own = (fabsf(value_of(g1)) + (a.top2 && g2 > kMaskedKey ? fabsf(value_of(g2)) : 0.f)) * 0x1p-22f;
+                low = key_of(value_of(mine) - own + 0.f);
+                high = key_of(value_of(mine) + own + 0.f);
+            }
+            const int last = __reduce_min_sync(0xffffffffu, stays ? low : INT_MAX);
+            const int next = __reduce_max_sync(0xffffffffu, stays ? kGoneKey : high);
             if (next > kMaskedKey) {              // (masked groups come last in order of their index)
                 const float hi = value_of(last), lo = value_of(next);
                 if (kBias || !a.top2) again = unsure(hi, lo, 4 * D);
@@ -279,36 +290,42 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         uint64_t gone = 0;
         int chosen = 0;
         float prev = INFINITY, gap = INFINITY;    // gap: between neighbours in the order
-        for (int k = 0;; ++k) {
-            const int best = __reduce_max_sync(0xffffffffu, m1);
-            const float v = value_of(best);
-            if (best > kMaskedKey) {
-                if (kBias) gap = fminf(gap, prev - v);
-                else if (k > 0) again |= unsure(prev, v, 0.f);
+        auto choose = [&](auto each) {            // each: every score's own share counts
+            for (int k = 0;; ++k) {
+                const int best = __reduce_max_sync(0xffffffffu, m1);
+                const float v = value_of(best);
+                if (best > kMaskedKey) {
+                    // (infinities: NaN, and sure)
+                    if (each.value) gap = fminf(gap, fmaf(fabsf(prev) + fabsf(v), -0x1p-23f, prev - v));
+                    else if (kBias) gap = fminf(gap, prev - v);
+                    else if (k > 0) again |= unsure(prev, v, 0.f);
+                }
+                if (k == a.K) break;
+                if (best <= kMaskedKey) {             // fewer than K experts to choose from: masked ones in order
+                    again = true;
+                    break;
+                }
+                const int mine = base + sub + a.lanes * i1;
+                const int e = __reduce_min_sync(0xffffffffu, m1 == best ? mine : INT_MAX);
+                if (lane == k) chosen = e;
+                prev = v;
+                const bool owner = m1 == best && mine == e;
+                if (owner) {
+                    gone |= 1ull << i1;
+                    m1 = m2;
+                    i1 = i2;
+                    m2 = kGoneKey;
+                }
+                // a lane whose two best are both gone looks for the next ones
+                if (__any_sync(0xffffffffu, owner && m1 == kGoneKey)) {
+                    int n1, n2, j1, j2;
+                    best_two(key, gone, n1, n2, j1, j2);
+                    if (owner) { m1 = n1; m2 = n2; i1 = j1; i2 = j2; }
+                }
             }
-            if (k == a.K) break;
-            if (best <= kMaskedKey) {             // fewer than K experts to choose from: masked ones in order
-                again = true;
-                break;
-            }
-            const int mine = base + sub + a.lanes * i1;
-            const int e = __reduce_min_sync(0xffffffffu, m1 == best ? mine : INT_MAX);
-            if (lane == k) chosen = e;
-            prev = v;
-            const bool owner = m1 == best && mine == e;
-            if (owner) {
-                gone |= 1ull << i1;
-                m1 = m2;
-                i1 = i2;
-                m2 = kGoneKey;
-            }
-            // a lane whose two best are both gone looks for the next ones
-            if (__any_sync(0xffffffffu, owner && m1 == kGoneKey)) {
-                int n1, n2, j1, j2;
-                best_two(key, gone, n1, n2, j1, j2);
-                if (owner) { m1 = n1; m2 = n2; i1 = j1; i2 = j2; }
-            }
-        }
+        };
+        if (far) choose(std::true_type{});
+        else choose(std::false_type{});
         if (kBias) again |= !(gap > 2 * D);
         float s = 0.f;                            // score of choice `lane`
         if (!again && lane < a.K) {

@@ -44,3 +44,36 @@ def test_softmax_with_many_terms_next_to_the_last_place(E, groups, term, by):
         bias[other] = float(s[0] - s[other] + gap)
         check_route(logits.cuda(), 2, bias.cuda(), score="softmax", n_groups=groups, topk_groups=3, group_score=by,
                     renormalise=False)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,keep,by", [(1, 1, "max"), (8, 3, "max"), (8, 3, "top2"), (32, 9, "top2")])
+@pytest.mark.parametrize("large", [-1e9, 100.0, 1e9, -3e38])
+def test_experts_with_a_bias_far_from_the_others(score, groups, keep, by, large):
+    """A large finite bias: experts switched off by it (of some groups all, or all but one), and experts it prefers."""
+    g = torch.Generator(device="cuda").manual_seed(groups)
+    E, K = 64, 6
+    logits = torch.randn((40, E), device="cuda", generator=g)
+    logits[1] = logits[1].round()                            # ties
+    logits[2] = 1.0 + torch.randint(0, 3, (E,), device="cuda", generator=g) * 2.0 ** -23
+    for n in (1, 5, 20, 61):
+        bias = torch.rand(E, device="cuda", generator=g) * 0.1
+        bias[torch.randperm(E, device="cuda", generator=g)[:n]] = large
+        check_route(logits, K, bias, score=score, n_groups=groups, topk_groups=keep, group_score=by, renormalise=n < 20)
+    bias = torch.rand(E, device="cuda", generator=g) * 0.1
+    bias[:24] = large                                        # whole groups
+    bias[3] = 0.05
+    check_route(logits, K, bias, score=score, n_groups=groups, topk_groups=keep, group_score=by)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("by", ["max", "top2"])
+def test_scores_next_to_each_other_among_large_biases(score, by):
+    """Biases of 1, 100 and 1e6 that differ by a few FP32 places, where s decides below those places or not."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    E = 48
+    logits = torch.randn((64, E), device="cuda", generator=g) * 3
+    for at in (1.0, 100.0, 1e6):
+        bias = at * (1 + torch.randint(-3, 4, (E,), device="cuda", generator=g) * 2.0 ** -23)
+        for groups, keep in ((1, 1), (6, 2), (12, 7)):
+            check_route(logits, 4, bias, score=score, n_groups=groups, topk_groups=keep, group_score=by)
