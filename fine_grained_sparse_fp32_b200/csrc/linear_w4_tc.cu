@@ -919,7 +919,6 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     }
     pdl_wait();
     pdl_trigger();
-    if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     tc_fence_before();
     build_tables(a, T);                           // its barriers also publish the mbarriers and the allocation
     tc_fence_after();
@@ -996,10 +995,12 @@ static kmoe_status pick(const Maps &m, const Args &a, int grid, cudaStream_t st)
 // L1). `out` may start where x starts, with rows the same bytes apart (H, FP32):
 // a step's values are read before any of its results is written.
 template <class XT>
-__global__ void __launch_bounds__(256) to_f16_kernel(const XT *x, int rows, int cols, __half *out, size_t out_pitch, float *scale)
+__global__ void __launch_bounds__(256) to_f16_kernel(const XT *x, int rows, int cols, __half *out, size_t out_pitch, float *scale, int *status)
 {
     pdl_wait();
     pdl_trigger();
+    // here, not in the products' launch, whose CTAs may report in it before its first one starts
+    if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const XT *src = x + (size_t)row * cols;
@@ -1042,8 +1043,8 @@ kmoe_status launch_w4_tc(const W4Product &p, void *x16, float *x_scale, int *err
     a.x_scale = x_scale;
     const int x_grid = (p.x_rows + 7) / 8;
     __half *out = static_cast<__half *>(x16);
-    if (p.x_f32) launch_pdl(to_f16_kernel<float>, x_grid, 256, 0, st, static_cast<const float *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols * 2, x_scale);
-    else launch_pdl(to_f16_kernel<__nv_bfloat16>, x_grid, 256, 0, st, static_cast<const __nv_bfloat16 *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols, x_scale);
+    if (p.x_f32) launch_pdl(to_f16_kernel<float>, x_grid, 256, 0, st, static_cast<const float *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols * 2, x_scale, p.status);
+    else launch_pdl(to_f16_kernel<__nv_bfloat16>, x_grid, 256, 0, st, static_cast<const __nv_bfloat16 *>(p.x), p.x_rows, p.cols, out, (size_t)p.cols, x_scale, p.status);
     const kmoe_status conv = check_launch("to_f16");
     if (conv != KMOE_OK) return conv;
     a.p = p;

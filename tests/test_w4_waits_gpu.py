@@ -32,3 +32,22 @@ def test_calls_after_one_that_gave_up_are_right(cols):
             assert torch.equal(kmoe.moe_linear_w4(x, w), want)
     finally:
         kmoe.moe_set_wait_limit(0)
+
+
+def test_every_call_that_gave_up_says_so():
+    """Many short products whose waits all run out: the word that reports it is cleared before any CTA can write it."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((1300, 8192), device="cuda", generator=g).bfloat16()
+    w = kmoe.moe_quant_w4(torch.randn((700, 8192), device="cuda", generator=g) * 0.03)
+    ws = torch.empty(kmoe.moe_linear_w4_workspace_size(1300, 1300, 700, 8192), dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    try:
+        for _ in range(30):
+            kmoe.moe_set_wait_limit(1)
+            kmoe.moe_linear_w4(x, w, ws=ws)
+            assert kmoe.moe_device_status(ws) == 1
+            kmoe.moe_set_wait_limit(0)
+            kmoe.moe_linear_w4(x, w, ws=ws)
+            assert kmoe.moe_device_status(ws) == 0
+    finally:
+        kmoe.moe_set_wait_limit(0)
