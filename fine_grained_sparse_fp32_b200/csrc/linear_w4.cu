@@ -75,6 +75,7 @@ struct W4Args {
     int tokens;             // tokens of a unit: those of kW4Cols fragments, fewer where x_frags is less
     int q_jump, s_jump;     // from the end of a row to the row of the next tile: code bytes, groups
     DivideBy by_blocks, by_tiles, by_tokens, by_grid;
+    bool check;             // look whether offsets descend
 };
 
 // D += A B with unsigned codes and signed digits, 16 rows x 8 columns, 32 deep.
@@ -644,6 +645,7 @@ w4_kernel(const __grid_constant__ W4Args a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (a.p.status && blockIdx.x == 0 && threadIdx.x == 0) *a.p.status = 0;
 
+    if (a.check && offsets_descend(p)) return;     // then nothing is done
     // rows, token blocks and cost of every expert, the latter as exclusive prefixes
     if (p.perm && threadIdx.x < min(p.P, kW4Perm)) sm.perm[threadIdx.x] = p.perm[threadIdx.x];
     {
@@ -678,7 +680,7 @@ w4_kernel(const __grid_constant__ W4Args a)
             run += n_blocks[i];
             run_cost += cost[i];
             if (g == a.groups - 1) {
-                // ranges that overlap (which no dispatch makes) could count beyond 32 bits: then nothing is done
+                // ranges that overlap could count beyond 32 bits: then nothing is done
                 const bool fits = run_cost < 0x7fffffffLL;
                 tab.pre[a.groups] = fits ? run : 0;
                 tab.cost[a.groups] = fits ? (int)run_cost : 0;
@@ -775,6 +777,7 @@ static kmoe_status run_w4(W4Args a, cudaStream_t st)
     a.x_frags = (int)std::min<size_t>((kW4SmemMax - fixed) / x_bytes, kW4Entries * kW4Cols);
     if (a.x_frags < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
     a.tokens = kW4FragTokens * std::min(a.x_frags, kW4Cols);
+    a.check = may_overflow(a.p, a.tokens);
     constexpr int kTileRows = kUp ? 16 : 32;
     a.tiles = (a.p.rows + kTileRows - 1) / kTileRows;
     a.q_jump = (kTileRows - 1) * (a.p.cols / 2);

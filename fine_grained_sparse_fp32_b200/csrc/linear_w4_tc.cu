@@ -72,6 +72,7 @@ struct Args {
     W4Product p;
     int tiles, groups;                            // units of a token block; experts, the shared one included
     DivideBy by_tiles;
+    bool check;                                   // look whether offsets descend
     const void *x16;                              // x in FP16, rows x_pitch bytes apart
     size_t x_pitch;
     const float *x_scale;                         // its rows' powers of two
@@ -154,6 +155,11 @@ __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
 {
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.check && offsets_descend(a.p)) {        // then nothing is done
+        if (threadIdx.x == 0) T.total = 0;
+        __syncthreads();
+        return;
+    }
     int run = 0;
     for (int g0 = 0; g0 < a.groups; g0 += kThreads) {
         const int g = g0 + threadIdx.x;
@@ -190,7 +196,7 @@ __device__ __forceinline__ void build_tables(const Args &a, Tail &T)
     }
     if (threadIdx.x == 0) {
         T.pre[a.groups] = run;
-        // ranges that overlap (which no dispatch makes) could count beyond the units' 32 bits: then nothing is done
+        // ranges that overlap could count beyond the units' 32 bits: then nothing is done
         T.total = (long long)run * a.tiles < 0x7fff0000LL ? run * a.tiles : 0;
     }
     __syncthreads();
@@ -1048,6 +1054,7 @@ kmoe_status launch_w4_tc(const W4Product &p, void *x16, float *x_scale, int *err
     const kmoe_status conv = check_launch("to_f16");
     if (conv != KMOE_OK) return conv;
     a.p = p;
+    a.check = may_overflow(p, kTokens);
     a.groups = p.E + (p.n_shared > 0 ? 1 : 0);
     if (a.groups > kMaxGroups) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: too many experts");
     const bool up = p.up.q != nullptr;

@@ -70,6 +70,17 @@ struct DivideBy {
     __device__ __forceinline__ int operator()(int n) const { return m ? (int)__umul64hi((unsigned long long)(uint32_t)n, m) : n; }
 };
 
+// Whether ranges that overlap, as descending offsets give them (which no dispatch
+// makes), could add up to more blocks of `tokens` rows than the kernels' sums hold.
+inline bool may_overflow(const W4Product &p, int tokens) { return p.offsets && (long long)p.E * (p.P / tokens + 1) >= 1LL << 28; }
+// By a whole CTA: whether offsets descend somewhere.
+__device__ __forceinline__ bool offsets_descend(const W4Product &p)
+{
+    bool down = false;
+    for (int g = threadIdx.x; g < p.E; g += blockDim.x) down = down || p.offsets[g + 1] < p.offsets[g];
+    return __syncthreads_or(down);
+}
+
 // Rows [start, start + count) of group g (expert or shared expert), cut to the batch.
 __device__ __forceinline__ void group_rows(const W4Product &p, int g, int *start, int *count)
 {
