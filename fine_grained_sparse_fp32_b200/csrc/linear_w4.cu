@@ -777,6 +777,9 @@ static kmoe_status run_w4(W4Args a, cudaStream_t st)
     a.x_frags = (int)std::min<size_t>((kW4SmemMax - fixed) / x_bytes, kW4Entries * kW4Cols);
     if (a.x_frags < 1) return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: cols=%d", a.p.cols);
     a.tokens = kW4FragTokens * std::min(a.x_frags, kW4Cols);
+    // the units' cost is counted in 31 bits
+    if (((long long)(a.p.P + a.p.n_shared) / a.tokens + a.groups) * w4_cost(a.tokens) >= 0x7fffffffLL)
+        return fail(KMOE_ERR_UNSUPPORTED, "4-bit products: %d rows of %d columns", a.p.P, a.p.cols);
     a.check = may_overflow(a.p, a.tokens);
     constexpr int kTileRows = kUp ? 16 : 32;
     a.tiles = (a.p.rows + kTileRows - 1) / kTileRows;
