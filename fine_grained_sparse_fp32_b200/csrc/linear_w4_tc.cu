@@ -334,8 +334,10 @@ __device__ __forceinline__ uint32_t larger_scale(uint32_t top, uint4 s)
     return __vmaxu2(__vmaxu2(top, __vmaxu2(s.x & 0x7fff7fffu, s.y & 0x7fff7fffu)), __vmaxu2(s.z & 0x7fff7fffu, s.w & 0x7fff7fffu));
 }
 __device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xffffu, v >> 16); }
-// Exponent field of a magnitude's 15 bits: 1 to 253.
-__device__ __forceinline__ uint32_t scale_field(uint32_t bits) { return min(max(bits >> 7, 1u), 253u); }
+// Exponent field of a magnitude's 15 bits: 1 to 254.
+__device__ __forceinline__ uint32_t scale_field(uint32_t bits) { return min(max(bits >> 7, 1u), 254u); }
+// 2^(127 - field) as FP32.
+__device__ __forceinline__ float over_field(uint32_t field) { return __uint_as_float(field == 254u ? 0x00400000u : (254u - field) << 23); }
 
 // This thread's row of M tile c of a unit, and its matrix.
 template <bool kUp>
@@ -367,7 +369,7 @@ constexpr uint32_t kSpread = 8, kRoom = 4, kFall = 96;
 __device__ __forceinline__ uint32_t next_base(uint32_t base, uint32_t highest, uint32_t f)
 {
     if (base != 0 && f <= base && f + kSpread >= base) return base;
-    return max(min(f + kRoom, 253u), highest > kFall ? highest - kFall : 1u);
+    return max(min(f + kRoom, 254u), highest > kFall ? highest - kFall : 1u);
 }
 
 // A group's factors for unpack_word. f: its scale over the power of two of its
@@ -444,7 +446,7 @@ __device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long
             ZeroPoints zp;
             if (kZeros) zp.set(now.z.x);
             const uint32_t flip = kZeros ? zp.flip(gi) : 0u;
-            f.set(counts ? __uint_as_float(bits) * __uint_as_float((254u - base) << 23) : 0.f, zp.minus(gi), flip);
+            f.set(counts ? __uint_as_float(bits) * over_field(base) : 0.f, zp.minus(gi), flip);
 #pragma unroll
             for (int j = 0; j < GS; ++j) {
                 uint32_t r[16];
@@ -503,7 +505,7 @@ __device__ __forceinline__ void store_turned(__nv_bfloat16 *at, int pitch, int l
 // Results of 16 tokens (n of them there) from both tiles' sums v0, v1. at: the
 // first token's row r of y. All: every token is there and has an x row.
 template <bool kUp, bool kAll, class YT>
-__device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, int n, const float *tok, const float (&row_scale)[2],
+__device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, int n, const float *tok, const float (&row_scale)[2][2],
                                            uint32_t *turn, const uint32_t (&v0)[16], const uint32_t (&v1)[16])
 {
     float o0[16], o1[16];
@@ -513,8 +515,9 @@ __device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, in
         const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            o0[i + k] = __uint_as_float(v0[i + k]) * row_scale[0] * f[k];
-            o1[i + k] = __uint_as_float(v1[i + k]) * row_scale[1] * f[k];
+            // (in halves: weights of 2^100 and tokens of 2^-100 must not meet infinity on the way)
+            o0[i + k] = __uint_as_float(v0[i + k]) * row_scale[0][0] * f[k] * row_scale[0][1];
+            o1[i + k] = __uint_as_float(v1[i + k]) * row_scale[1][0] * f[k] * row_scale[1][1];
             if (!kAll && f[k] == 0.f) o0[i + k] = o1[i + k] = 0.f;    // a token without an x row stands for zeros
         }
     }
@@ -751,7 +754,7 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             // scales over the power of two below the row's largest: 2^(127 - field) as FP32
             const uint32_t field = scale_field(larger_half(top));
-            const float over = __uint_as_float((254u - field) << 23);
+            const float over = over_field(field);
             sc = sc_after;
             zr = zr_after;
             const bool more = u + (int)gridDim.x < total;
@@ -852,9 +855,13 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
             ok = wait(&B.dfull[nth & 1], (nth >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            float row_scale[2];                   // the rows' powers of two
+            float row_scale[2][2];                // the rows' powers of two, halved
 #pragma unroll
-            for (int c = 0; c < 2; ++c) row_scale[c] = __uint_as_float((uint32_t)T.field[nth & 3][c][row] << 23);
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t field = T.field[nth & 3][c][row], half = (field + 127u) >> 1;
+                row_scale[c][0] = __uint_as_float(half << 23);
+                row_scale[c][1] = __uint_as_float((field + 127u - half) << 23);
+            }
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;

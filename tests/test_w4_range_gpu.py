@@ -215,3 +215,25 @@ def test_one_large_channel_costs_the_others_nothing(large, N, group, zeros, y_dt
     x[:, 77::128] = large
     x = x.bfloat16()
     check(kmoe.moe_linear_w4(x, q, y_dtype=y_dtype), x, values(q), runs_on_tensor_cores(N, q, y_dtype))
+
+
+@pytest.mark.parametrize("N", [8, 2500])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, False)])
+@pytest.mark.parametrize("w_size,x_size", [(1e37, 1e-30), (1e37, 1e-8), (1e-36, 1e30), (1e-30, 1e37)])
+def test_large_weights_and_small_tokens_meet_in_range(N, group, zeros, w_size, x_size):
+    g = gen(N + group)
+    q = kmoe.moe_quant_w4((randn(g, 200, 256).clamp(-6, 6) * w_size), group=group, zeros=zeros)
+    x = (randn(g, N, 256) * x_size).bfloat16()
+    check(kmoe.moe_linear_w4(x, q), x, values(q), N == 2500)
+
+
+@pytest.mark.parametrize("N", [8, 2500])
+def test_the_largest_scales(N):
+    """Scales up to the largest finite one, with codes at most one place from their zero point."""
+    g = gen(N)
+    codes = torch.randint(7, 10, (200, 256), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.tensor([2.0 ** 127 * 1.9921875, 2.0 ** 127, -2.0 ** 126.5, 2.0 ** 120], device="cuda")
+    scales = scales[torch.randint(0, 4, (200, 4), device="cuda", generator=g)].bfloat16()
+    w = kmoe.W4(plain_ops.w4_bytes(codes.cpu()).cuda(), scales)
+    x = (randn(g, N, 256) * 1e-25).bfloat16()
+    check(kmoe.moe_linear_w4(x, w), x, values(w), N == 2500)
