@@ -47,6 +47,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kmoe {
 using namespace sm100;
@@ -94,9 +95,18 @@ struct Tail {
     int pre[kMaxGroups + 1], start[kMaxGroups], count[kMaxGroups], size[kMaxGroups];   // size: tokens of a block
     uint16_t known[kKnown];
     uint8_t field[4][2][kRows];                   // exponent fields of the rows' bases, of units in turn
+    // Wide pass: whether an unpacking warp has a row whose groups need a base each, of blocks in
+    // turn (the MMA warp is at most two buffers behind), and when all of them have said so.
+    alignas(8) uint8_t split[8][8];
+    uint64_t vote;
     // result warps: the tokens' powers of two, and 16 tokens' results of 32 rows
     alignas(16) float tok[8][kTokens];
     alignas(16) uint32_t turn[8][8 * 32];
+
+    __device__ __forceinline__ bool any_split(uint32_t it) const
+    {
+        return *reinterpret_cast<const volatile unsigned long long *>(split[it & 7]) != 0;
+    }
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
@@ -259,13 +269,20 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 v) { return *reinterpret_
 // 2^-8, which the token's factor gives back. Below 2^-14 FP16's places are 2^-24
 // wide: none is lost where s has its 8 bits above that.
 constexpr float kTokenFactor = 512.f;
+// (a ^ b) & c in one instruction: the compiler shares a ^ b among the masks, which costs one more a word.
+__device__ __forceinline__ uint32_t flip_and_mask(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 __device__ __forceinline__ void unpack_word(uint32_t word, uint32_t flip, __half2 s24, __half2 s20, __half2 minus_z, uint32_t *out)
 {
     const uint32_t up = word >> 8;
-    out[0] = half2_bits(__hfma2(as_half2((word ^ flip) & 0x000f000fu), s24, minus_z));
-    out[1] = half2_bits(__hfma2(as_half2((word ^ flip) & 0x00f000f0u), s20, minus_z));
-    out[2] = half2_bits(__hfma2(as_half2((up ^ flip) & 0x000f000fu), s24, minus_z));
-    out[3] = half2_bits(__hfma2(as_half2((up ^ flip) & 0x00f000f0u), s20, minus_z));
+    out[0] = half2_bits(__hfma2(as_half2(flip_and_mask(word, flip, 0x000f000fu)), s24, minus_z));
+    out[1] = half2_bits(__hfma2(as_half2(flip_and_mask(word, flip, 0x00f000f0u)), s20, minus_z));
+    out[2] = half2_bits(__hfma2(as_half2(flip_and_mask(up, flip, 0x000f000fu)), s24, minus_z));
+    out[3] = half2_bits(__hfma2(as_half2(flip_and_mask(up, flip, 0x00f000f0u)), s20, minus_z));
 }
 // Four groups' zero points, one a byte, after the flips, and those: the top bit of each byte.
 struct ZeroPoints {
@@ -282,6 +299,8 @@ struct ZeroPoints {
         asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(flips), "r"(0x8888u + 0x1111u * gi));
         return r;
     }
+    // of groups gi and gi + 1, at the top of two halves (other bits, too)
+    __device__ __forceinline__ uint32_t signs(int gi) const { return __byte_perm(flips, 0, 0x1010 * gi + 0x1000); }
     __device__ __forceinline__ __half2 minus(int gi) const { return as_half2(__byte_perm(z, 0x80808080u, 0x4040u + 0x0101u * gi)); }      // -z 2^-24
 };
 
@@ -350,35 +369,37 @@ __device__ __forceinline__ size_t tile_row(const Args &a, const Unit &u, int c, 
 // A row's weights are held over one power of two, its base: the one below the
 // row's largest scale. A scale within 2^kSpread of that keeps its 8 bits above FP16's
 // last place, 2^-24, and so does each |q - z| <= 8 times it. A row with a
-// smaller scale is `wide`, which the unpacking warps see as they use the scales: then every
+// smaller scale is `wide`, which the unpacking warps see at the end of a unit: then every
 // role leaves its units as if a wait had run out, and the CTA takes all of them
 // again in the wide pass. There the base moves along the row: it is the power of
-// two of field f + kRoom for the first group (f: its scale's exponent field) and serves
-// fields from its own down to kSpread below; for a group outside, the row's sums so
-// far, FP32 numbers, are multiplied in tensor memory by the quotient of old base
-// and new. A group whose codes are all z adds nothing, whatever its scale (the
-// quantiser gives a group of zeros the scale 1), and is left out. A base stays within 2^-kFall of
-// the highest so far, and the sums so within FP32's range. A block's groups go to the tensor
-// core one by one, so the wide pass takes 2 to 2.5 times as long as the usual one
-// (1024 tokens, groups of 32, one group of zeros in each row: 766 us, not 296). Deciding
-// unit by unit, with no second pass, cost the usual one 5 to 15%: by registers in the
-// unpacking warps, by the scales' latency in others.
+// two kRoom above the first groups' scales and serves those from its own
+// down to kSpread below; for groups outside, the row's sums so far, FP32 numbers, are
+// multiplied in tensor memory by the quotient of old base and new. A group whose codes are
+// all z adds nothing, whatever its scale (the quantiser gives a group of zeros the
+// scale 1), and is left out. A base stays within 2^-kFall of the highest so far, and the
+// sums so within FP32's range. Where the groups of a block need a base each in one of the
+// unit's rows, they go to the tensor core one by one.
+// 1024 tokens, all rows with a block of zeros behind scales of 2^-11: 349 us, not 247, with
+// groups of 128, 520, not 305, with groups of 32. Deciding unit by unit, with no second
+// pass, cost the usual pass 5 to 15%: by registers in the unpacking warps, by the scales'
+// latency in others.
 constexpr uint32_t kSpread = 8, kRoom = 4, kFall = 96;
 
-// The base's field of a row from a group's on, whose scale has field f; 0: none so far.
-__device__ __forceinline__ uint32_t next_base(uint32_t base, uint32_t highest, uint32_t f)
+// The base's field of a row from some groups on, whose scales have fields low to
+// high, at most kSpread apart; 0: none so far.
+__device__ __forceinline__ uint32_t next_base(uint32_t base, uint32_t highest, uint32_t low, uint32_t high)
 {
-    if (base != 0 && f <= base && f + kSpread >= base) return base;
-    return max(min(f + kRoom, 254u), highest > kFall ? highest - kFall : 1u);
+    if (base != 0 && high <= base && low + kSpread >= base) return base;
+    return max(min((low + high) / 2 + kRoom, 254u), highest > kFall ? highest - kFall : 1u);
 }
 
-// A group's factors for unpack_word. f: its scale over the power of two of its
-// row's base, magnitude below 2; minus: -z 2^-24; flip: whether its codes are flipped.
+// A group's factors for unpack_word. scale: 2^24 s with s below 2^-8, that is 2^15
+// times the scale over its row's base, negative where codes are flipped; minus: -z 2^-24.
 struct GroupFactors {
     __half2 s24, s20, minus_z;
-    __device__ __forceinline__ void set(float f, __half2 minus, uint32_t flip)
+    __device__ __forceinline__ void set(__half2 scale, __half2 minus)
     {
-        s24 = __float2half2_rn(__uint_as_float(__float_as_uint(f * 0x1p15f) ^ (flip & 0x80000000u)));        // 2^24 s, with s below 2^-8
+        s24 = scale;
         s20 = __hmul2(s24, as_half2(0x2c002c00u));                    // 2^-4
         minus_z = __hmul2(s24, minus);
     }
@@ -386,41 +407,67 @@ struct GroupFactors {
 
 // What an unpacking warp needs to know of a unit.
 struct UnpackAt {
-    const __nv_bfloat16 *sc;                      // scales and zero points of this thread's row
-    const uint8_t *zr, *codes;                    // its codes in stage 0
+    const __nv_bfloat16 *sc, *sc_after;           // scales and zero points of this thread's row, and of the next unit's
+    const uint8_t *zr, *zr_after, *codes;         // its codes in stage 0
+    Scales ahead;                                 // of the first block; then of the next unit's
     uint32_t d, to;                               // its warp's sums of the unit and buffer 0 in tensor memory
-    uint32_t it, step;                            // the first block, the first buffer
+    uint32_t it, step;                            // blocks and buffers so far
     int blocks, n;                                // n: the unit's tokens
-    uint8_t *field;
+    uint8_t *field;                               // where the result warps find its last base
 };
 
-// A unit of the wide pass, its groups one by one. False in every lane of a warp whose wait gave up.
+// A unit of the wide pass. False in every lane of a warp whose wait gave up.
 template <int G, bool kZeros>
-__device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long long limit, UnpackAt at)
+__device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long long limit, UnpackAt &at)
 {
-    constexpr int GB = kW4Block / G, GS = G / 32; // groups of a block, 32-column slices of a group
+    constexpr int GB = kW4Block / G;              // groups of a block
     const int lane = threadIdx.x & 31, swizzle = (lane >> 1) & 3;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &T.abort, err, limit); };
     uint32_t base = 0, highest = 0;               // exponent fields (0: none so far)
     for (int kb = 0; kb < at.blocks; ++kb, ++at.it) {
-        const Scales now = load_scales<kZeros>(at.sc + kb * GB, at.zr + kb * GB, GB);
+        const Scales now = at.ahead;
+        if (kb + 1 < at.blocks) at.ahead = load_scales<kZeros>(at.sc + (kb + 1) * GB, at.zr + (kb + 1) * GB, GB);
+        else at.ahead = load_scales<kZeros>(at.sc_after, at.zr_after, GB);
         const int st = at.it % kStages;
         if (!wait(&B.cfull[st], (at.it / kStages) & 1)) return false;
-        const uint8_t *src = at.codes + (size_t)st * 2 * kCodeTile;
+        uint4 w[4];                               // w[t]: words of columns 8t of each 32-column slice
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint4 *>(at.codes + (size_t)st * 2 * kCodeTile + ((t ^ swizzle) << 4));
+        uint32_t bits[GB], low = 255u, high = 0;  // scales, 0 where a group adds nothing; fields of the others
+#pragma unroll
+        for (int gi = 0; gi < GB; ++gi) {
+            const uint32_t two = gi < 2 ? now.s.x : now.s.y, z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
+            uint32_t differ = 0;
+#pragma unroll
+            for (int jj = gi * (G / 32); jj < (gi + 1) * (G / 32); ++jj)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) differ |= word_of(w[t], jj) ^ z * 0x11111111u;
+            bits[gi] = differ == 0 ? 0u : gi & 1 ? two & 0xffff0000u : two << 16;
+            if ((bits[gi] & 0x7fffffffu) == 0) continue;
+            low = min(low, scale_field((bits[gi] & 0x7fffffffu) >> 16));
+            high = max(high, scale_field((bits[gi] & 0x7fffffffu) >> 16));
+        }
+        bool split = false;                       // some row's groups need a base each
+        if constexpr (GB > 1) {
+            const bool mine = __any_sync(0xffffffffu, high > low + kSpread);
+            if (lane == 0) {
+                T.split[at.it & 7][(threadIdx.x >> 5) - 8] = mine;
+                mbar_arrive(&T.vote);
+            }
+            if (!wait(&T.vote, at.it & 1)) return false;
+            split = T.any_split(at.it);
+        }
 #pragma unroll 1
-        for (int gi = 0; gi < GB; ++gi, ++at.step) {
-            const uint32_t ab = at.step & 1, two = gi < 2 ? now.s.x : now.s.y, bits = gi & 1 ? two & 0xffff0000u : two << 16;
-            const uint32_t z = kZeros ? (now.z.x >> (8 * gi)) & 15u : 8u;
-            uint32_t w[GS][4], differ = 0;        // the group's words: slice, columns 8t
+        for (int pass = 0; pass < (split ? GB : 1); ++pass, ++at.step) {
+            const uint32_t ab = at.step & 1;
+            if (split) {
+                uint32_t f = 0;
 #pragma unroll
-            for (int j = 0; j < GS; ++j)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    w[j][t] = *reinterpret_cast<const uint32_t *>(src + ((t ^ swizzle) << 4) + (gi * GS + j) * 4);
-                    differ |= w[j][t] ^ z * 0x11111111u;
-                }
-            const bool counts = differ != 0 && (bits & 0x7fffffffu) != 0;
-            const uint32_t next = counts ? next_base(base, highest, scale_field((bits & 0x7fffffffu) >> 16)) : base;
+                for (int gi = 0; gi < GB; ++gi) f = gi == pass ? bits[gi] & 0x7fffffffu : f;
+                high = f ? scale_field(f >> 16) : 0u;
+                low = f ? high : 255u;
+            }
+            const uint32_t next = high != 0 ? next_base(base, highest, low, high) : base;
             if (!wait(&B.aempty[ab], ((at.step >> 1) & 1) ^ 1)) return false;
             const bool moves = base != 0 && next != base;
             if (__any_sync(0xffffffffu, moves)) {
@@ -442,19 +489,24 @@ __device__ __forceinline__ bool unpack_wide(Tail &T, Barriers &B, int *err, long
             tc_fence_after();
             base = next;
             highest = max(highest, base);
-            GroupFactors f;
             ZeroPoints zp;
             if (kZeros) zp.set(now.z.x);
-            const uint32_t flip = kZeros ? zp.flip(gi) : 0u;
-            f.set(counts ? __uint_as_float(bits) * over_field(base) : 0.f, zp.minus(gi), flip);
 #pragma unroll
-            for (int j = 0; j < GS; ++j) {
-                uint32_t r[16];
+            for (int gi = 0; gi < GB; ++gi) {
+                if (split && gi != pass) continue;
+                const uint32_t flip = kZeros ? zp.flip(gi) : 0u;
+                GroupFactors f;
+                const float scale = bits[gi] ? __uint_as_float(bits[gi]) * over_field(base) * 0x1p15f : 0.f;
+                f.set(__float2half2_rn(flip ? -scale : scale), zp.minus(gi));
 #pragma unroll
-                for (int t = 0; t < 4; ++t) unpack_word(w[j][t], flip, f.s24, f.s20, f.minus_z, r + 4 * t);
-                tmem_st16(at.to + ab * 64 + (gi * GS + j) * 16, r);
+                for (int jj = gi * (G / 32); jj < (gi + 1) * (G / 32); ++jj) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) unpack_word(word_of(w[t], jj), flip, f.s24, f.s20, f.minus_z, r + 4 * t);
+                    tmem_st16(at.to + ab * 64 + jj * 16, r);
+                }
             }
-            const bool last = gi + 1 == GB;
+            const bool last = !split || pass + 1 == GB;
             if (last && kb + 1 == at.blocks) *at.field = (uint8_t)max(base, 1u);
             tmem_st_wait();
             tc_fence_before();
@@ -503,7 +555,8 @@ __device__ __forceinline__ void store_turned(__nv_bfloat16 *at, int pitch, int l
 }
 
 // Results of 16 tokens (n of them there) from both tiles' sums v0, v1. at: the
-// first token's row r of y. All: every token is there and has an x row.
+// first token's row r of y. All: every token is there and has an x row, and the rows'
+// powers of two, whole then in row_scale[.][0], are within 2^+-100.
 template <bool kUp, bool kAll, class YT>
 __device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, int n, const float *tok, const float (&row_scale)[2][2],
                                            uint32_t *turn, const uint32_t (&v0)[16], const uint32_t (&v1)[16])
@@ -515,9 +568,11 @@ __device__ __forceinline__ void store_step(const W4Product &p, YT *at, int r, in
         const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+            o0[i + k] = __uint_as_float(v0[i + k]) * row_scale[0][0] * f[k];
+            o1[i + k] = __uint_as_float(v1[i + k]) * row_scale[1][0] * f[k];
             // (in halves: weights of 2^100 and tokens of 2^-100 must not meet infinity on the way)
-            o0[i + k] = __uint_as_float(v0[i + k]) * row_scale[0][0] * f[k] * row_scale[0][1];
-            o1[i + k] = __uint_as_float(v1[i + k]) * row_scale[1][0] * f[k] * row_scale[1][1];
+            if (!kAll) o0[i + k] *= row_scale[0][1];
+            if (!kAll) o1[i + k] *= row_scale[1][1];
             if (!kAll && f[k] == 0.f) o0[i + k] = o1[i + k] = 0.f;    // a token without an x row stands for zeros
         }
     }
@@ -551,11 +606,14 @@ struct Slots {
     __device__ __forceinline__ void done() { phase ^= n == 2 ? 3u : 1u << first; }
 };
 
+template <int N>
+using Const = std::integral_constant<int, N>;
+
 // Every unit of this CTA, by roles of its warps; kWide: in the wide pass.
 template <bool kUp, int G, bool kZeros, class YT, bool kWide>
 __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail &T, uint8_t *codes, uint8_t *toks)
 {
-    constexpr int GB = kW4Block / G, kPasses = kWide ? GB : 1;
+    constexpr int GB = kW4Block / G;
     const W4Product &p = a.p;
     Barriers &B = T.bars[kWide];
     volatile int *abort = &T.abort;
@@ -663,7 +721,7 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
         // The whole warp walks; one elected lane issues. Kept converged, the
         // descriptors live in uniform registers and an MMA costs 11 clocks at 16
         // tokens; issued under `lane == 0` each took 170.
-        uint32_t it = 0;
+        uint32_t it = 0, step = 0;                // step: buffers
         Slots sl;
         bool ok = true;
         for (int u = blockIdx.x, turn = 0; u < total && ok; u += gridDim.x, turn ^= 1) {
@@ -674,30 +732,38 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
             for (int kb = 0; kb < blocks && ok; ++kb, ++it) {
                 const int s = it % kStages;
                 ok = wait(&B.bfull[s], (it / kStages) & 1);
-                // a buffer holds a block, in the wide pass one group of it
+                // a buffer holds a block, in the wide pass sometimes one group of it
+                int passes = 1;
 #pragma unroll 1
-                for (int g = 0; g < kPasses && ok; ++g) {
-                    const uint32_t step = it * kPasses + g;
+                for (int g = 0; g < passes && ok; ++g, ++step) {
                     const int ab = step & 1;
                     ok = wait(&B.afull[ab], (step >> 1) & 1);
                     if (!ok) break;
+                    if (kWide && GB > 1 && g == 0 && __shfl_sync(0xffffffffu, (int)T.any_split(it), 0)) passes = GB;
                     fence_proxy_async();          // the gathered rows, for the tensor core
                     tc_fence_after();
                     const uint32_t b0 = smem_u32(toks) + s * 2 * kPanel;
                     const uint64_t bd0 = sw128_kmajor_desc(b0), bd1 = sw128_kmajor_desc(b0 + kPanel);
-                    if (elect_one()) {
+                    // 16 columns each of both tiles, from the k0-th on
+                    auto issue = [&](auto k0, auto n) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const uint32_t dt = tmem + d_col(c, sl.first), at = tmem + a_col(c, ab);
 #pragma unroll
-                            for (int j = 0; j < kW4Block / 16 / kPasses; ++j) {
-                                const int k = g * (kW4Block / 16 / kPasses) + j;
+                            for (int k = k0.value; k < k0.value + n.value; ++k)
                                 umma_f16_ts(dt, at + k * 8, (k < 4 ? bd0 : bd1) + (uint64_t)((k & 3) * 2), idesc, (kb | k) != 0);
-                            }
                         }
+                    };
+                    if (elect_one()) {
+                        constexpr int kAll = kW4Block / 16, kOne = G / 16;
+                        if (!kWide || passes == 1) issue(Const<0>{}, Const<kAll>{});
+                        else if (g == 0) issue(Const<0>{}, Const<kOne>{});
+                        else if (g == 1) issue(Const<kOne % kAll>{}, Const<kOne>{});
+                        else if (g == 2) issue(Const<2 * kOne % kAll>{}, Const<kOne>{});
+                        else issue(Const<3 * kOne % kAll>{}, Const<kOne>{});
                         umma_commit(&B.aempty[ab]);
-                        if (g + 1 == kPasses) umma_commit(&B.bempty[s]);
-                        if (g + 1 == kPasses && kb + 1 == blocks) umma_commit(&B.dfull[turn]);
+                        if (g + 1 == passes) umma_commit(&B.bempty[s]);
+                        if (g + 1 == passes && kb + 1 == blocks) umma_commit(&B.dfull[turn]);
                     }
                     __syncwarp();
                 }
@@ -712,18 +778,32 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
         // ---------------------------------------------------- unpack, wide
         const int c = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        uint32_t it = 0, nth = 0;
+        uint32_t nth = 0;
         Slots sl;
-        for (int u = blockIdx.x; u < total; u += gridDim.x, it += blocks, ++nth) {
+        UnpackAt at{};
+        at.codes = codes + c * kCodeTile + row * 64;
+        at.to = lanes + a_col(c, 0);
+        at.blocks = blocks;
+        auto rows_of = [&](int u) {
             const Unit U = unit_of(a, T, u);
             const bool shared = U.grp >= p.E;
-            const size_t at = tile_row<kUp>(a, U, c, row) * (p.cols / G);
-            sl.take(U.n);
-            const UnpackAt where = {(kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + at,
-                                    kZeros ? (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + at : nullptr,
-                                    codes + c * kCodeTile + row * 64, lanes + d_col(c, sl.first), lanes + a_col(c, 0), it, it * GB,
-                                    blocks, U.n, &T.field[nth & 3][c][row]};
-            if (!unpack_wide<G, kZeros>(T, B, a.err, a.wait_limit, where)) break;
+            const size_t first = tile_row<kUp>(a, U, c, row) * (p.cols / G);
+            at.sc_after = (kUp && c ? (shared ? p.up_shared.s : p.up.s) : (shared ? p.w_shared.s : p.w.s)) + first;
+            if (kZeros) at.zr_after = (kUp && c ? (shared ? p.up_shared.z : p.up.z) : (shared ? p.w_shared.z : p.w.z)) + first;
+        };
+        if (blockIdx.x < total) {
+            rows_of(blockIdx.x);
+            at.ahead = load_scales<kZeros>(at.sc_after, at.zr_after, GB);
+        }
+        for (int u = blockIdx.x; u < total; u += gridDim.x, ++nth) {
+            at.sc = at.sc_after;
+            at.zr = at.zr_after;
+            at.n = unit_of(a, T, u).n;
+            at.field = &T.field[nth & 3][c][row];
+            sl.take(at.n);
+            at.d = lanes + d_col(c, sl.first);
+            if (u + (int)gridDim.x < total) rows_of(u + gridDim.x);
+            if (!unpack_wide<G, kZeros>(T, B, a.err, a.wait_limit, at)) break;
         }
     } else if (warp >= 8) {
         // --------------------------------------------------------- unpack
@@ -754,7 +834,8 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
         for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++nth) {
             // scales over the power of two below the row's largest: 2^(127 - field) as FP32
             const uint32_t field = scale_field(larger_half(top));
-            const float over = over_field(field);
+            const uint32_t to_half = (30u - field) * (128u * 0x00010001u);
+            uint32_t low = GB == 1 ? 0x7fffu : 0x7fff7fffu;           // the smallest magnitudes
             sc = sc_after;
             zr = zr_after;
             const bool more = u + (int)gridDim.x < total;
@@ -775,11 +856,14 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
                 ZeroPoints zp;
                 if (kZeros) zp.set(now.z.x);
 #pragma unroll
-                for (int gi = 0; gi < GB; ++gi) {
-                    const uint32_t two = gi < 2 ? now.s.x : now.s.y;
-                    const float f = __uint_as_float(gi & 1 ? two & 0xffff0000u : two << 16) * over;     // 2^9 s, magnitude below 2
-                    if (fabsf(f) < 0x1p-8f && f != 0.f) *abort = kStartAnew;                    // below 2^-kSpread
-                    fac[gi].set(f, zp.minus(gi), kZeros ? zp.flip(gi) : 0u);
+                for (int gi = 0; gi < GB; gi += 2) {
+                    const uint32_t two = gi < 2 ? now.s.x : now.s.y, size = two & 0x7fff7fffu;
+                    low = GB == 1 ? min(low, size) : __vminu2(low, size);
+                    // 2^15 over the base, for two scales at once: exponents in FP16's field
+                    const uint32_t half2 = (size + to_half) << 3, sign = two ^ (kZeros ? zp.signs(gi) : 0u);
+                    const uint32_t both = half2 | (sign & 0x80008000u);
+                    fac[gi].set(as_half2(__byte_perm(both, 0, 0x1010)), zp.minus(gi));
+                    if (gi + 1 < GB) fac[gi + 1].set(as_half2(__byte_perm(both, 0, 0x3232)), zp.minus(gi + 1));
                 }
                 next_scales<GB, kZeros>(now);
                 ok = wait(&B.cfull[st], (it / kStages) & 1);
@@ -812,6 +896,12 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
                 }
             }
             top = larger_scale(top, s_after);
+            // scales that are wide, or 0 or below 2^-126, whose exponents the addition did not take right
+            const uint32_t least = (GB == 1 ? low : min(low & 0xffffu, low >> 16)) >> 7;
+            if (__any_sync(0xffffffffu, least == 0 || field > least + kSpread)) {
+                *abort = kStartAnew;
+                break;                            // (the others run out of work then, and look)
+            }
         }
     } else {
         // -------------------------------------------------------- results
@@ -843,13 +933,12 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
             const bool shared = U.grp >= p.E;
             sl.take(U.n);
             float *tok = T.tok[warp];             // 0 for a token that is not there
-            bool there = true;
+            bool there = !kWide;                  // nothing out of the ordinary
 #pragma unroll
             for (int j = 0; j < kTokens / 32; ++j) {
                 tok[lane + 32 * j] = f_after[j] * kTokenFactor;
                 there = there && f_after[j] != 0.f;
             }
-            there = __all_sync(0xffffffffu, there);
             __syncwarp();
             if (u + (int)gridDim.x < total) factors_of(u + gridDim.x);
             ok = wait(&B.dfull[nth & 1], (nth >> 1) & 1);
@@ -859,9 +948,12 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint32_t field = T.field[nth & 3][c][row], half = (field + 127u) >> 1;
+                there = there && field >= 27u && field <= 227u;
                 row_scale[c][0] = __uint_as_float(half << 23);
                 row_scale[c][1] = __uint_as_float((field + 127u - half) << 23);
             }
+            there = __all_sync(0xffffffffu, there);
+            float row_whole[2][2] = {{row_scale[0][0] * row_scale[0][1]}, {row_scale[1][0] * row_scale[1][1]}};
             YT *y = !kUp && shared ? static_cast<YT *>(p.y_shared) + (size_t)(U.row0 - p.P) * p.rows
                                    : static_cast<YT *>(p.y) + (size_t)U.row0 * p.rows;
             const int r = kUp ? U.tile * kRows + row : U.tile * 2 * kRows + row;
@@ -881,20 +973,13 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
                 if (t0 + 32 >= U.n || (t0 & 32)) release(sl.first + (t0 >> 6));
                 // a whole step of tokens that are all there has no branch in it
                 if (t0 + 16 <= U.n && there)
-                    store_step<kUp, true>(p, y + (size_t)t0 * p.rows + r, r, 16, tok + t0, row_scale, T.turn[warp], v0, v1);
+                    store_step<kUp, true>(p, y + (size_t)t0 * p.rows + r, r, 16, tok + t0, row_whole, T.turn[warp], v0, v1);
                 else
                     store_step<kUp, false>(p, y + (size_t)t0 * p.rows + r, r, U.n - t0, tok + t0, row_scale, T.turn[warp], v0, v1);
             }
             __syncwarp();                         // tok is read
         }
     }
-}
-
-// (a call: it costs the usual pass no registers)
-template <bool kUp, int G, bool kZeros, class YT>
-__device__ __noinline__ void run_units_wide(const Maps &maps, const Args &a, Tail &T, uint8_t *codes, uint8_t *toks)
-{
-    run_units<kUp, G, kZeros, YT, true>(maps, a, T, codes, toks);
 }
 
 template <bool kUp, int G, bool kZeros, class YT>
@@ -923,6 +1008,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             }
             mbar_init(&B.drain, 1);
         }
+        mbar_init(&T.vote, 8);
         T.abort = kGoOn;
         fence_mbar_init();
     }
@@ -943,7 +1029,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         __syncthreads();
         if (threadIdx.x == 0) T.abort = kGoOn;
         __syncthreads();
-        run_units_wide<kUp, G, kZeros, YT>(maps, a, T, codes, toks);
+        run_units<kUp, G, kZeros, YT, true>(maps, a, T, codes, toks);
     }
     tc_fence_before();
     __syncthreads();
