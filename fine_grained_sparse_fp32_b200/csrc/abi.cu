@@ -185,20 +185,23 @@ static size_t h_bytes(int w_dtype)
 // (BF16-precision) activations: below kTcMinTokens tokens.
 static bool two_term(int w_dtype, int N) { return w_dtype == KMOE_E4M3_B128 && N < kTcMinTokens; }
 
-// Whether P rows of a product with E matrices of `unit_rows` 256-row units (128
-// for gate and up) go to the tensor-core kernel. It unpacks a weight once for up
-// to 128 rows and costs nearly the same for one; the kernel for few tokens pays
-// for every four rows, more with small groups. Measured on the layer's FFN (384
-// experts), with even and uneven experts, the two meet at 510 and 380 tokens for
-// groups of 128 (240 and 206 us), 320 and 170 for groups of 64 (261 and 175 us),
-// 125 and about 90 for groups of 32 (250 us); the rule lies between. One matrix
-// has few units to deal out, and the more rows are needed the fewer there are:
-// 24 units (6144 x 2560) meet at 35 rows (20 us), 10 (2560 x 6144) at 130 (56
-// us), 2 (512 x 2560) at 1000 (30 us).
+// Whether P rows of a product with E matrices of `units` 256-row units (128 for
+// gate and up) go to the tensor-core kernel. It unpacks a weight once for up to
+// 128 rows and costs nearly the same for one; the kernel for few tokens pays for
+// every two rows, more with small groups. Measured on the layer's FFN (384
+// experts, K = 6), with even and uneven experts, the two meet at 310 and 140 tokens for
+// groups of 128 (247 and 141 us), 145 and below 60 for groups of 64 (236 us), 45 and
+// below 20 for groups of 32 (161 us): the rule takes 223, 101 and 30. One matrix has few
+// units to deal out, and where they are fewer than 10 each has many rows. Groups of 128
+// and 32 meet at 600 and 350 rows for 2 units (512 x 2560: 30 and 33 us), 265 and 190
+// for 4 (1024 x 1024: 17 us), 57 and 38 for 10 (2560 x 6144: 42 and 51 us), 27 and 20 for
+// 24 (6144 x 2560: 21 and 25 us), 12 and 8 for 64 (16384 x 2560: 21 and 24 us); the
+// rule takes 601 and 375, 229 and 144, 75 and 47, 30 and 18, 13 and 7.
 static bool w4_tensor_cores(int P, int E, int units, int group)
 {
-    const int rows = group == 32 ? 1 : group == 64 ? 3 : 6;
-    return (long long)P * units >= ((long long)rows * units * E + 1100);
+    const int tenths = group == 32 ? 1 : group == 64 ? 11 : 29;       // of a row for each matrix
+    const int base = group == 32 ? 400 : group == 64 ? 500 : 600, few = group == 32 ? 700 : group == 64 ? 1000 : 1200;
+    return (long long)P * units >= (long long)tenths * units * E / 10 + base + few / units;
 }
 
 // The grouped FFN's scratch after the status block: H [N*K + N, I] and, with
