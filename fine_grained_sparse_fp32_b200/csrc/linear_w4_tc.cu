@@ -990,7 +990,6 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     uint8_t *codes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *toks = codes + (size_t)kStages * 2 * kCodeTile;
     Tail &T = *reinterpret_cast<Tail *>(toks + (size_t)kStages * 2 * kPanel);
-    const W4Product &p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // known to be uniform
     if (threadIdx.x == 0) {
         for (Barriers &B : T.bars) {
