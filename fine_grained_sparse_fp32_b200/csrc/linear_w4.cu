@@ -38,8 +38,8 @@
 // warp order at the end, so results do not depend on timing.
 //
 // Measured on the layer's experts (384 of 512 x 2560, groups of 128, K = 6 and a
-// shared one), cold: 32 tokens take 52 us for gate and up (208 MB: 4.0 TB/s) and 31
-// us for down (104 MB: 3.3 TB/s). The steps run at HBM's rate; some 10 us of each
+// shared one), cold: 32 tokens take 50 us for gate and up (208 MB: 4.2 TB/s) and 30
+// us for down (104 MB: 3.5 TB/s). The steps run at HBM's rate; some 10 us of each
 // launch go by before the first one (tables, plan, first copies, digits), of
 // which the copies into L2 hide a part.
 #include "w4.cuh"

@@ -31,8 +31,9 @@
 //   warps 18-19  gather token rows with cp.async (a TMA gather of four rows
 //                costs its issuer 80 clocks, too much for 64 tokens)
 // Measured on the layer's experts (384 of 512 x 2560, groups of 128, K = 6 and a
-// shared one), cold: 4096 tokens take 218 us for gate and up (150 GFLOP: 690
-// TFLOP/s, tensor pipe 43% busy) and 145 us for down (75 GFLOP: 520 TFLOP/s, 30%).
+// shared one), cold and alone: 4096 tokens take 224 us for gate and up (150 GFLOP: 670
+// TFLOP/s; the tensor pipe was 43% busy at 218) and 145 us for down (75 GFLOP: 520 TFLOP/s,
+// 30%). Call after call the FFN takes 450 us in all, since the power limit lowers the clock.
 // Instruction issue bounds it: 2.3 a clock over warps that wait for one another,
 // with room for two buffers of unpacked weights only. Unpacking by 16 warps took
 // 408 us in all, not 372: their reads hold up the token rows' copies.

@@ -5,9 +5,10 @@
 //               q = clamp(rint(w / s) + z, 0, 15),  lo <= 0 <= hi
 // A thread owns one 8-column word, so a group of 32, 64 or 128 columns is 4, 8
 // or 16 neighbouring lanes, its extremes come from two to four shuffles, and
-// sixteen lanes write the 64 bytes of a 128-column block. HBM bounds it: 83.9 M
-// FP32 values (groups of 32, zero points) take 82 us, 4.7 TB/s of reads and
-// writes, and 64 us back, 6.0 TB/s. CTAs of 128 threads: of 256, both took 150 us
+// sixteen lanes write the 64 bytes of a 128-column block. Instruction issue bounds the
+// quantiser: 83.9 M FP32 values (groups of 32, zero points) take 82 us at 3.25 of 4
+// instructions a clock and SM, the ALU pipe at 62% (4.7 TB/s of reads and writes). HBM bounds
+// the way back: 64 us, 6.0 TB/s at 1.9 instructions. CTAs of 128 threads: of 256, both took 150 us
 // together; two words a thread: one took 91 us, four 82.
 #include "w4.cuh"
 

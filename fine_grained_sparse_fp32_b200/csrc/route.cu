@@ -181,7 +181,7 @@ __device__ __forceinline__ void best_two(const int (&key)[NPL], uint64_t gone, i
 }
 
 // Instructions bound it: 65536 tokens of 384 experts in 8 groups, K = 6, FP32
-// logits, bias, take 92 us (1.1 TB/s), 941 instructions a token, the integer pipe
+// logits, bias, take 94 us (1.1 TB/s), 941 instructions a token at 92, the integer pipe
 // (comparisons, selects) at 65% of its rate. Four CTAs an SM (64 registers): two
 // (120 registers) took 127 us where four took 111.
 template <class LT, int NPL, bool kBias>
