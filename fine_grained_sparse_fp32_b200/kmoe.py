@@ -403,7 +403,7 @@ class Layer:
         if N > self.max_tokens:
             raise ValueError("more tokens than the workspace was sized for")
         if y is None:
-            y = torch.empty((N, cfg.d), dtype=self.y_dtype, device=x.device)
+            y = _empty((N, cfg.d), self.y_dtype, x.device, stream)
         L = self.layer
         if self.routing is not None:
             _call("moe_forward_routed", x, stream, _ptr(x), dtype_code(x.dtype), N, cfg.d, cfg.E, cfg.K, cfg.I,
@@ -426,7 +426,7 @@ class Layer:
         if N > self.max_tokens:
             raise ValueError("more tokens than the workspace was sized for")
         if h_out is None:
-            h_out = torch.empty_like(h)
+            h_out = _empty(h.shape, h.dtype, h.device, stream)
         L = self.layer
         if self.routing is not None:
             _call("moe_block_forward_routed", h, stream, _ptr(h), N, cfg.d, cfg.E, cfg.K, cfg.I, self.routing._ref,
@@ -471,14 +471,15 @@ def moe_forward(x, layer, y_dtype=torch.bfloat16, with_outputs=False, stream=Non
     """One whole-layer call; with_outputs also returns (topk_idx, topk_w, counts)."""
     cfg = layer["cfg"]
     N = x.shape[0]
-    lay = Layer(layer, N, y_dtype, score, routing=routing)
-    if not with_outputs:
-        return lay.forward(x, stream=stream)
-    idx = torch.empty((N, cfg.K), dtype=torch.int32, device=x.device)
-    w = torch.empty((N, cfg.K), dtype=torch.float32, device=x.device)
-    counts = torch.empty(cfg.E, dtype=torch.int32, device=x.device)
-    y = lay.forward(x, topk_idx=idx, topk_w=w, counts=counts, stream=stream)
-    return y, idx, w, counts
+    with torch.cuda.stream(stream):      # the workspace, given back on return, is that stream's, too
+        lay = Layer(layer, N, y_dtype, score, routing=routing)
+        if not with_outputs:
+            return lay.forward(x, stream=stream)
+        idx = torch.empty((N, cfg.K), dtype=torch.int32, device=x.device)
+        w = torch.empty((N, cfg.K), dtype=torch.float32, device=x.device)
+        counts = torch.empty(cfg.E, dtype=torch.int32, device=x.device)
+        y = lay.forward(x, topk_idx=idx, topk_w=w, counts=counts, stream=stream)
+        return y, idx, w, counts
 
 
 def moe_block_forward(h, layer, gamma_pre, gamma_post, eps: float, with_outputs=False, stream=None,
@@ -486,16 +487,17 @@ def moe_block_forward(h, layer, gamma_pre, gamma_post, eps: float, with_outputs=
     """One sandwich-block call; with_outputs also returns (x, topk_idx, topk_w, counts)."""
     cfg = layer["cfg"]
     N = h.shape[0]
-    lay = Layer(layer, N, torch.bfloat16, score, block=True, routing=routing)
-    if not with_outputs:
-        return lay.block_forward(h, gamma_pre, gamma_post, eps, h_out=h_out, stream=stream)
-    idx = torch.empty((N, cfg.K), dtype=torch.int32, device=h.device)
-    w = torch.empty((N, cfg.K), dtype=torch.float32, device=h.device)
-    counts = torch.empty(cfg.E, dtype=torch.int32, device=h.device)
-    x = torch.empty_like(h)
-    out = lay.block_forward(h, gamma_pre, gamma_post, eps, h_out=h_out, topk_idx=idx, topk_w=w, counts=counts,
-                            x_out=x, stream=stream)
-    return out, x, idx, w, counts
+    with torch.cuda.stream(stream):      # as in moe_forward
+        lay = Layer(layer, N, torch.bfloat16, score, block=True, routing=routing)
+        if not with_outputs:
+            return lay.block_forward(h, gamma_pre, gamma_post, eps, h_out=h_out, stream=stream)
+        idx = torch.empty((N, cfg.K), dtype=torch.int32, device=h.device)
+        w = torch.empty((N, cfg.K), dtype=torch.float32, device=h.device)
+        counts = torch.empty(cfg.E, dtype=torch.int32, device=h.device)
+        x = torch.empty_like(h)
+        out = lay.block_forward(h, gamma_pre, gamma_post, eps, h_out=h_out, topk_idx=idx, topk_w=w, counts=counts,
+                                x_out=x, stream=stream)
+        return out, x, idx, w, counts
 
 
 def moe_quant_1x128(x, codes=None, scales=None, stream=None):
