@@ -397,6 +397,18 @@ class Layer:
         self.max_tokens = max_tokens
         self.score = SCORES[score]
 
+    def _check_routed(self, x, topk_idx, topk_w, counts):
+        """Refuses what a call with `routing` on x [N, d] would misread."""
+        cfg, L, dev = self.cfg, self.layer, x.device
+        _on_gpu(x, "x")
+        _dense(L["w_router"], "w_router", torch.float32, (cfg.E, cfg.d), dev)
+        for t, name, dtype, shape in ((L["bias"], "bias", torch.float32, (cfg.E,)),
+                                      (topk_idx, "topk_idx", torch.int32, (x.shape[0], cfg.K)),
+                                      (topk_w, "topk_w", torch.float32, (x.shape[0], cfg.K)),
+                                      (counts, "counts", torch.int32, (cfg.E,))):
+            if t is not None:
+                _dense(t, name, dtype, shape, dev)
+
     def forward(self, x, y=None, topk_idx=None, topk_w=None, counts=None, stream=None):
         cfg = self.cfg
         N = x.shape[0]
@@ -406,6 +418,9 @@ class Layer:
             y = _empty((N, cfg.d), self.y_dtype, x.device, stream)
         L = self.layer
         if self.routing is not None:
+            _dense(x, "x", _ACT_DTYPES, (N, cfg.d), self.ws.device)
+            _dense(y, "y", _ACT_DTYPES, (N, cfg.d), x.device)
+            self._check_routed(x, topk_idx, topk_w, counts)
             _call("moe_forward_routed", x, stream, _ptr(x), dtype_code(x.dtype), N, cfg.d, cfg.E, cfg.K, cfg.I,
                   self.routing._ref, _ptr(L["w_router"]), _ptr(L["bias"]), ctypes.byref(self.routed),
                   ctypes.byref(self.shared), _ptr(y), dtype_code(y.dtype), _ptr(topk_idx), _ptr(topk_w), _ptr(counts),
@@ -429,6 +444,12 @@ class Layer:
             h_out = _empty(h.shape, h.dtype, h.device, stream)
         L = self.layer
         if self.routing is not None:
+            for t, name in ((h, "h"), (h_out, "h_out"), (x_out, "x_out")):
+                if t is not None:
+                    _dense(t, name, torch.bfloat16, (N, cfg.d), self.ws.device)
+            for t, name in ((gamma_pre, "gamma_pre"), (gamma_post, "gamma_post")):
+                _dense(t, name, torch.bfloat16, (cfg.d,), h.device)
+            self._check_routed(h, topk_idx, topk_w, counts)
             _call("moe_block_forward_routed", h, stream, _ptr(h), N, cfg.d, cfg.E, cfg.K, cfg.I, self.routing._ref,
                   _ptr(gamma_pre), _ptr(gamma_post), float(eps), _ptr(L["w_router"]), _ptr(L["bias"]),
                   ctypes.byref(self.routed), ctypes.byref(self.shared), _ptr(h_out), _ptr(x_out), _ptr(topk_idx),
@@ -607,6 +628,8 @@ def moe_linear_w4(x, w4: W4, perm_token=None, offsets=None, y_dtype=torch.bfloat
         need = (_lib or load()).moe_linear_w4_workspace_size(N, P, w4.rows, w4.cols, w4.E, w4.group, code)
         if need:
             ws = _empty(need, torch.uint8, dev, stream)
+    elif ws is not None:
+        _dense(ws, "ws", torch.uint8, (ws.numel(),), dev)
     _call("moe_linear_w4", x, stream, x.data_ptr(), KMOE_BF16, N, P, w4.rows, w4.cols, w4.E,
           None if perm_token is None else perm_token.data_ptr(), None if offsets is None else offsets.data_ptr(),
           w4._ref, out.data_ptr(), code, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())

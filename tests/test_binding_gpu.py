@@ -63,3 +63,17 @@ def test_outputs_of_a_handle_on_a_stream(monkeypatch):
     monkeypatch.undo()
     st.synchronize()
     assert seen == [st] and torch.equal(y, want)
+
+
+def test_a_workspace_elsewhere_is_refused():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = kmoe.moe_quant_w4(torch.randn((700, 256), device="cuda", generator=g))
+    x = torch.randn((2500, 256), device="cuda", generator=g).bfloat16()
+    need = kmoe.moe_linear_w4_workspace_size(2500, 2500, 700, 256)
+    assert need > 0
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.int16, device="cuda"),
+                torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            kmoe.moe_linear_w4(x, w, ws=bad)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(kmoe.moe_linear_w4(x, w, ws=ws), kmoe.moe_linear_w4(x, w))
