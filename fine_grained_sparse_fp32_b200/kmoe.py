@@ -54,7 +54,17 @@ class _RoutingStruct(ctypes.Structure):
                 ("group_score", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
-class Routing:
+class _Fixed:
+    """An object whose C struct is made once: setting an attribute afterwards would not reach it."""
+    _ref = None
+
+    def __setattr__(self, name, value):
+        if self._ref is not None:
+            raise AttributeError(f"{type(self).__name__} is fixed: make another for a different {name}")
+        object.__setattr__(self, name, value)
+
+
+class Routing(_Fixed):
     """How experts are chosen and weighted (kmoe_routing in include/kmoe.h): scores from a sigmoid or
     a softmax over all experts, the correction bias added to the score, selection limited to the best
     groups of experts, weights optionally renormalised and scaled."""
@@ -73,7 +83,7 @@ class Routing:
         self._ref = ctypes.byref(self._struct)
 
 
-class W4:
+class W4(_Fixed):
     """Weights in the 4-bit format of kmoe_w4: codes uint8 [..., rows, cols / 2], scales BF16
     [..., rows, cols / group], zeros uint8 of the scales' shape or None (8 everywhere). One leading
     dimension stacks the matrices of several experts."""

@@ -50,3 +50,13 @@ def test_routed_layer_calls_refuse_tensors_of_the_host():
     g = torch.ones(256, dtype=torch.bfloat16)
     refuses(lambda: plain.forward(layer["x"]), "CUDA")
     refuses(lambda: block.block_forward(layer["x"], g, g, 1e-6), "CUDA")
+
+
+def test_rules_and_4_bit_weights_cannot_be_changed_behind_their_struct():
+    rule = kmoe.Routing(n_groups=2, topk_groups=1, scale=2.0)
+    w = kmoe.W4(torch.zeros((16, 128), dtype=torch.uint8), torch.ones((16, 2), dtype=torch.bfloat16))
+    for thing, name, value in ((rule, "scale", 1.0), (rule, "topk_groups", 2), (w, "scales", w.scales.clone()), (w, "zeros", None)):
+        with pytest.raises(AttributeError, match=name):
+            setattr(thing, name, value)
+    assert rule.scale == 2.0 and rule._struct.scale == 2.0
+    w.scales.fill_(0.5)                       # values are the caller's to change
