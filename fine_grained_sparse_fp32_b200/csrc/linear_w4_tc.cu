@@ -112,7 +112,7 @@ struct Tail {
 constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kCodeTile + 2 * kPanel) + sizeof(Tail);
 
 // mbar_wait by a whole warp: true in every lane, or false in every lane. Past
-// the first look the warp is suspended for up to 20 us at a time, so a shorter
+// the first look the warp is suspended for up to 4 us at a time, so a shorter
 // limit counts as that.
 __device__ __forceinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, long long limit)
 {
@@ -983,6 +983,23 @@ __device__ __forceinline__ void run_units(const Maps &maps, const Args &a, Tail 
     }
 }
 
+__device__ __forceinline__ void init_barriers(Barriers &B)
+{
+    for (int s = 0; s < kStages; ++s) {
+        mbar_init(&B.cfull[s], 1);
+        mbar_init(&B.cempty[s], 8);               // one arrival per unpacking warp
+        mbar_init(&B.bfull[s], kGatherThreads);
+        mbar_init(&B.bempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+        mbar_init(&B.afull[b], 8);                // one arrival per unpacking warp
+        mbar_init(&B.aempty[b], 1);
+        mbar_init(&B.dfull[b], 1);
+        mbar_init(&B.dempty[b], 8);               // one arrival per result warp
+    }
+    mbar_init(&B.drain, 1);
+}
+
 template <bool kUp, int G, bool kZeros, class YT>
 __global__ void __launch_bounds__(kThreads, 1)
 w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
@@ -993,22 +1010,7 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     Tail &T = *reinterpret_cast<Tail *>(toks + (size_t)kStages * 2 * kPanel);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // known to be uniform
     if (threadIdx.x == 0) {
-        for (Barriers &B : T.bars) {
-            for (int s = 0; s < kStages; ++s) {
-                mbar_init(&B.cfull[s], 1);
-                mbar_init(&B.cempty[s], 8);       // one arrival per unpacking warp
-                mbar_init(&B.bfull[s], kGatherThreads);
-                mbar_init(&B.bempty[s], 1);
-            }
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&B.afull[b], 8);        // one arrival per unpacking warp
-                mbar_init(&B.aempty[b], 1);
-                mbar_init(&B.dfull[b], 1);
-                mbar_init(&B.dempty[b], 8);       // one arrival per result warp
-            }
-            mbar_init(&B.drain, 1);
-        }
-        mbar_init(&T.vote, 8);
+        init_barriers(T.bars[0]);
         T.abort = kGoOn;
         fence_mbar_init();
     }
@@ -1027,7 +1029,12 @@ w4_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     if (T.abort == kStartAnew) {
         tc_fence_after();
         __syncthreads();
-        if (threadIdx.x == 0) T.abort = kGoOn;
+        if (threadIdx.x == 0) {
+            init_barriers(T.bars[1]);
+            mbar_init(&T.vote, 8);
+            T.abort = kGoOn;
+            fence_mbar_init();
+        }
         __syncthreads();
         run_units<kUp, G, kZeros, YT, true>(maps, a, T, codes, toks);
     }
