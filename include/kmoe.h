@@ -296,7 +296,8 @@ kmoe_status moe_grouped_ffn(const void *x, int x_dtype, int N, int d, int I, int
  * accumulated in FP32. With offsets NULL every row uses W_0 (E must be 1).
  * Every x[.] row is BF16; a row p that no expert's range holds keeps what y
  * held. Row ranges are cut to [0, P), and a perm_token entry outside [0, N)
- * stands for a row of zeros. offsets must not descend, as moe_permute's do not.
+ * stands for a row of zeros. offsets must not descend, as moe_permute's do not
+ * (rows of ranges that overlap are unspecified, all rows where E and P are large).
  * Few rows, and F32 y, use x to within 2^-22 of the largest value of its 128-column
  * block, and weights exactly. Many rows of BF16 y use the tensor cores, with x to
  * within 2^-39 of the largest value of its whole row (H, an FP32 input, to 2^-11 of its
@@ -457,8 +458,8 @@ kmoe_status moe_device_status(const void *ws, int *status, void *stream);
 
 /*
  * Give-up limit of the pipeline waits in the tensor-core expert FFN kernels
- * that later calls of the calling host thread launch (moe_grouped_ffn,
- * moe_forward, moe_block_forward), in SM clock cycles; 0 restores the
+ * that later calls of the calling host thread launch (moe_grouped_ffn, moe_linear_w4,
+ * moe_forward, moe_block_forward and their _routed forms), in SM clock cycles; 0 restores the
  * default of 2^32 cycles (about 2 s). This exists to test the failure path
  * without faulting a GPU: with a limit far below what a wait normally takes,
  * a kernel gives up, writes 1 to the workspace status word, lets its
