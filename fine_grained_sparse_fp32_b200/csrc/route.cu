@@ -328,13 +328,21 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         else choose(std::false_type{});
         if (kBias) again |= !(gap > 2 * D);
         float s = 0.f;                            // score of choice `lane`
-        if (!again && lane < a.K) {
-            const float l = to_f32(lr[chosen]);
-            if (!a.softmax) s = sigmoidf_(l);
-            else s = (l == top ? 1.f : expf(l - top)) / (a.renormalise ? 1.f : sum);
+        if (!again) {
+            const float l = lane < a.K ? to_f32(lr[chosen]) : -INFINITY;
+            if (!a.softmax) {
+                s = lane < a.K ? sigmoidf_(l) : 0.f;
+            } else {
+                // weights that are renormalised need no common divisor, and over the largest
+                // choice, not the largest logit, none of them is lost below 2^-126
+                const float over = a.renormalise ? value_of(__reduce_max_sync(0xffffffffu, key_of(l + 0.f))) : top;
+                s = lane < a.K ? (l == over ? 1.f : expf(l - over)) / (a.renormalise ? 1.f : sum) : 0.f;
+            }
         }
         const float total = warp_sum(s);          // 0 from lanes without a choice
-        if (again || (a.renormalise && total < 1e-30f)) {     // scores that FP32 cannot weigh against each other, too
+        // Scores that FP32 cannot weigh against each other, too: below 2^-126 a score is off by up
+        // to 2^-150, which over a sum of 1e-8 is less than 1e-37 of weight.
+        if (again || (a.renormalise && total < 1e-8f)) {
             double exact;
             chosen = route_exact(lr, a, exact_c + (threadIdx.x >> 5) * a.exact_places, &exact);
             if (a.renormalise) {

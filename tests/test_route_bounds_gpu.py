@@ -77,3 +77,25 @@ def test_scores_next_to_each_other_among_large_biases(score, by):
         bias = at * (1 + torch.randint(-3, 4, (E,), device="cuda", generator=g) * 2.0 ** -23)
         for groups, keep in ((1, 1), (6, 2), (12, 7)):
             check_route(logits, 4, bias, score=score, n_groups=groups, topk_groups=keep, group_score=by)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("low", [-40.0, -60.0, -75.0, -100.0])
+def test_renormalised_weights_of_scores_far_below_the_largest(score, low):
+    """The bias chooses experts whose scores lie down to e^-105 below the largest one (or 1): their shares of the sum
+    do not lose places to FP32's smallest numbers. Each logit's distance from the largest choice, 40 at most, is off by
+    one rounding, which its exponential multiplies: 40 more roundings than check_route allows."""
+    g = torch.Generator(device="cuda").manual_seed(int(-low))
+    E, K = 64, 6
+    logits = low - torch.rand((50, E), device="cuda", generator=g) * 5
+    logits[:, ::7] -= 35
+    logits[:, 3] = 2.0
+    bias = torch.zeros(E, device="cuda")
+    bias[torch.randperm(E, device="cuda", generator=g)[:12]] = 3.0 + 0.1 * torch.arange(12, device="cuda")
+    bias[3] = -1.0
+    for groups, keep in ((1, 1), (8, 5)):
+        kw = dict(score=score, n_groups=groups, topk_groups=keep, group_score="max", renormalise=True)
+        idx, w = kmoe.moe_route(logits, K, bias=bias, routing=kmoe.Routing(**kw))
+        ri, rw = plain_ops.route(logits, K, bias, **kw)
+        assert torch.equal(idx.cpu(), ri)
+        assert torch.allclose(w.cpu().double(), rw, rtol=56 * 2.0 ** -24, atol=1e-37)
