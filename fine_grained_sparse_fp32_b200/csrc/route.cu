@@ -25,7 +25,9 @@
 // bias the order of scores is that of the logits, which are exact: equal ones
 // are equal in FP64 too, and only logits whose FP64 scores may round to the same
 // number go to FP64: closer than 1e-13, with scores below e^-600, or above 20
-// under a sigmoid.
+// under a sigmoid. Two equal ones at the end of the choice can hide a third that is
+// such a neighbour of both; it takes scores like those, or logits below 2e-6, whose
+// places are that close.
 #include "permute_dev.cuh"
 #include "w4.cuh"
 
@@ -243,7 +245,8 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         auto unsure = [&](float hi, float lo, float width) {
             const float d = hi - lo;
             if (kBias) return !(d > width);
-            return d != 0.f && (!(d > 1e-13f) || (a.softmax ? hi - top < -600.f : lo > 20.f || hi < -600.f));
+            const bool ties = a.softmax ? hi - top < -600.f : lo > 20.f || hi < -600.f;
+            return ties || (d == 0.f ? fabsf(hi) < 2e-6f : !(d > 1e-13f));
         };
         int m1, m2, i1, i2;
         best_two(key, 0, m1, m2, i1, i2);

@@ -99,3 +99,25 @@ def test_renormalised_weights_of_scores_far_below_the_largest(score, low):
         ri, rw = plain_ops.route(logits, K, bias, **kw)
         assert torch.equal(idx.cpu(), ri)
         assert torch.allclose(w.cpu().double(), rw, rtol=56 * 2.0 ** -24, atol=1e-37)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_equal_logits_at_the_end_of_the_choice_hide_no_third(score, dtype):
+    """The last choice and the first that goes are equal, and an expert of a lower index has another logit but the same
+    FP64 score: saturated sigmoids, scores that are 0, and logits whose places are below those of their scores."""
+    E = 42
+    rows = []
+    for pair, third, rest in ((82.0, 56.0, -1.0), (40.0, 39.0, 3.0), (-760.0, -800.0, -900.0), (1e-9, 1e-9 - 1.1e-16, -2.0)):
+        l = torch.full((E,), rest)
+        l[[17, 19, 35]] = pair
+        l[10] = third
+        if pair < 0:
+            l[5] = 1.0                                       # the largest, which is chosen first
+        rows.append(l)
+    logits = torch.stack(rows).to(dtype).cuda()
+    for K in (1, 2, 3):
+        for groups, keep in ((1, 1), (2, 1), (6, 1), (6, 2), (21, 1), (21, 3)):
+            if keep * E // groups >= K:
+                for by in ("max", "top2"):
+                    check_route(logits, K, None, score=score, n_groups=groups, topk_groups=keep, group_score=by, renormalise=False)
