@@ -334,7 +334,8 @@ route_kernel(const LT *__restrict__ logits, const RouteArgs a)
         if (!again) {
             const float l = lane < a.K ? to_f32(lr[chosen]) : -INFINITY;
             if (!a.softmax) {
-                s = lane < a.K ? sigmoidf_(l) : 0.f;
+                const float e = expf(-fabsf(l));          // (not e^-l, which is infinite where the score is not yet 0)
+                s = lane < a.K ? (l < 0.f ? e : 1.f) / (1.f + e) : 0.f;
             } else {
                 // weights that are renormalised need no common divisor, and over the largest
                 // choice, not the largest logit, none of them is lost below 2^-126

@@ -121,3 +121,18 @@ def test_equal_logits_at_the_end_of_the_choice_hide_no_third(score, dtype):
             if keep * E // groups >= K:
                 for by in ("max", "top2"):
                     check_route(logits, K, None, score=score, n_groups=groups, topk_groups=keep, group_score=by, renormalise=False)
+
+
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_sigmoids_down_to_the_smallest_numbers(renormalise):
+    """Scores of logits below -88.7, where e^-l is infinite in FP32, are not 0 yet: each is off by at most a half of
+    2^-149, and a share of a sum of 0.01 or more by 2^-143."""
+    logits = torch.full((60, 8), -200.0, device="cuda")
+    logits[:, 0] = -4.0
+    logits[:, 1] = -86.0 - torch.arange(60, device="cuda") * 0.3
+    bias = torch.tensor([2.0, 1.0, 0.0, 0, 0, 0, 0, 0], device="cuda")
+    kw = dict(score="sigmoid", renormalise=renormalise)
+    idx, w = kmoe.moe_route(logits, 2, bias=bias, routing=kmoe.Routing(**kw))
+    ri, rw = plain_ops.route(logits, 2, bias, **kw)
+    assert torch.equal(idx.cpu(), ri)
+    assert torch.allclose(w.cpu().double(), rw, rtol=16 * 2.0 ** -24, atol=2.0 ** -143)
